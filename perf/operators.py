@@ -105,7 +105,8 @@ def _choices(g, T, k, E, drop):
 
 
 def _plan(ids, E):
-    """(order, offsets, pos) of a stable sort of the choices by expert; dropped choices go last."""
+    """(order, offsets, pos) of a stable sort of the choices by expert. Dropped choices go last, and
+    the position of one is -1 - row."""
     flat = ids.reshape(-1)
     key = torch.where((flat >= 0) & (flat < E), flat, E)
     order = torch.argsort(key, stable=True)
@@ -113,7 +114,7 @@ def _plan(ids, E):
     offsets = torch.cat([counts.new_zeros(1), counts.cumsum(0)]).to(torch.int32)
     pos = torch.empty_like(order)
     pos[order] = torch.arange(flat.numel(), device=flat.device)
-    pos = torch.where(key < E, pos, -1).to(torch.int32).reshape(ids.shape)
+    pos = torch.where(key < E, pos, -1 - pos).to(torch.int32).reshape(ids.shape)
     return order, offsets, pos
 
 
@@ -268,12 +269,18 @@ def exact(case, seed):
         for j in range(k):
             if 0 <= ids[t][j] < E:
                 rows_of[ids[t][j]].append((t, j))
-    edge, source, at = [0], [], [[-1] * k for _ in range(T)]
+    edge, source, at = [0], [], [[None] * k for _ in range(T)]
     for e in range(E):
         for t, j in rows_of[e]:
             at[t][j] = len(source)
             source.append(t * k + j)
         edge.append(len(source))
+    behind = len(source)                                  # the rows that dropped choices leave unused
+    for t in range(T):
+        for j in range(k):
+            if at[t][j] is None:
+                at[t][j] = -1 - behind
+                behind += 1
     source = torch.tensor(source, dtype=torch.int64, device="cuda")
     n = source.numel()
     w = st["w"].detach().double().reshape(-1)

@@ -40,7 +40,9 @@ EXPORTS = ["ep_compress", "ep_free", "ep_stream_info", "ep_upload", "ep_handle_i
            "ep_decompress_many", "ep_decode_symbols", "ep_linear_forward", "ep_gemm_bf16", "ep_handle_check",
            "ep_release", "ep_last_error", "ep_version", "ep_linear_forward_fp8", "ep_quantize_rows_fp8",
            "ep_gemm_fp8", "ep_compress_device", "ep_linear_forward_noalloc", "ep_linear_forward_many",
-           "ep_linear_forward_fp8_many"]
+           "ep_linear_forward_fp8_many", "ep_quantize_rows_int8", "ep_gemm_int8", "ep_gemm_int8_experts",
+           "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_sort_tokens_scratch", "ep_sort_tokens",
+           "ep_combine_tokens", "ep_combine_tokens_grad"]
 
 
 class EPError(RuntimeError):
@@ -96,6 +98,15 @@ def lib() -> C.CDLL:
         L.ep_linear_forward_fp8.argtypes = [vp, vp, i64, vp, vp, vp]
         L.ep_quantize_rows_fp8.argtypes = [vp, i64, i64, vp, vp, vp]
         L.ep_gemm_fp8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, vp, vp]
+        L.ep_quantize_rows_int8.argtypes = [vp, C.c_int, i64, i64, i64, vp, vp, vp]
+        L.ep_gemm_int8.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, C.c_int, vp, vp]
+        L.ep_gemm_int8_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
+        L.ep_pad_rows_int8.argtypes = [vp, i64, i64, vp, i64, vp]
+        L.ep_linear_forward_int8.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.ep_sort_tokens_scratch.argtypes = [i64, C.c_int, C.c_int, C.POINTER(sz)]
+        L.ep_sort_tokens.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp]
+        L.ep_combine_tokens.argtypes = [vp, C.c_int, vp, vp, i64, C.c_int, i64, i64, vp, vp]
+        L.ep_combine_tokens_grad.argtypes = [vp, C.c_int, vp, vp, vp, i64, C.c_int, i64, i64, vp, vp, vp]
         L.ep_handle_check.argtypes = [vp, vp]
         L.ep_release.argtypes = [vp]
         L.ep_release.restype = None
@@ -433,6 +444,244 @@ def gemm_fp8(xq, xs, wq, ws, bias=None, stream=None):
     return y
 
 
+def _need_rows(t, name: str, dtypes):
+    """_need for a 2-D matrix whose rows may be further apart than they are long."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    rows, cols = t.shape
+    apart = t.stride(0) if rows > 1 else cols
+    if not t.is_cuda or (cols > 1 and t.stride(1) != 1) or apart < cols:
+        raise ValueError(f"{name} must be on the GPU, its elements consecutive within a row and its rows disjoint")
+    if t.device.index != _torch().cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_torch().cuda.current_device()}")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be one of {', '.join(map(str, dtypes))}, got {t.dtype}")
+    return rows, cols, apart
+
+
+def _ptr(t):
+    return None if t is None else C.c_void_p(t.data_ptr())
+
+
+def _float_types():
+    torch = _torch()
+    return torch.bfloat16, torch.float16, torch.float32
+
+
+def quantize_rows_int8(x, stream=None):
+    """Per-row INT8 codes of BF16, FP16 or FP32 rows [M, K] (rows may be further apart than K) and their
+    fp32 scales: scale = max |x| / 127, codes = x / scale rounded to nearest even, exactly. A row with an
+    infinity or a NaN gets codes 0 and scale NaN. On `stream` (default: the current stream; another
+    stream first waits for the current one)."""
+    torch = _torch()
+    M, K, ldx = _need_rows(x, "x", _float_types())
+    s, other = _run_on(stream)
+    with torch.cuda.stream(s):
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        sc = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check(lib().ep_quantize_rows_int8(_ptr(x), _dtype_code(x.dtype), M, K, ldx, _ptr(q), _ptr(sc),
+                                       C.c_void_p(s.cuda_stream)), "ep_quantize_rows_int8")
+    _used_on(s, other, x)
+    return q, sc
+
+
+def pad_rows_int8(codes, stream=None):
+    """INT8 codes [..., K] in new memory with K rounded up to a multiple of 16, zeros behind: the layout
+    the INT8 products read. They call this for codes that lack it; a program with such a weight lays
+    it out once and keeps it (and pads the activations' codes to the same width)."""
+    torch = _torch()
+    _need(codes, "codes", torch.int8)
+    K = codes.shape[-1]
+    rows, ld = codes[..., 0].numel() if K else 0, (K + 15) // 16 * 16
+    s, other = _run_on(stream)
+    with torch.cuda.stream(s):
+        out = torch.empty((*codes.shape[:-1], ld), dtype=torch.int8, device=codes.device)
+    _check(lib().ep_pad_rows_int8(_ptr(codes), rows, K, _ptr(out), ld, C.c_void_p(s.cuda_stream)), "ep_pad_rows_int8")
+    _used_on(s, other, codes)
+    return out
+
+
+def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype, stream):
+    torch = _torch()
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in _float_types():
+        raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+    if xq.dim() != 2 or wq.dim() != (2 if offsets is None else 3):
+        raise ValueError("xq must be [rows, K] and wq " + ("[N, K]" if offsets is None else "[experts, N, K]"))
+    M, K = xq.shape
+    lead = tuple(wq.shape[:-1])
+    _need(xq, "xq", torch.int8)
+    _need(wq, "wq", torch.int8, shape=(*lead, K))
+    _need(xs, "xs", torch.float32, shape=(M,))
+    _need(ws, "ws", torch.float32, shape=lead)
+    if bias is not None:
+        _need(bias, "bias", torch.bfloat16, shape=lead)
+    if offsets is not None:
+        _need(offsets, "offsets", torch.int32, shape=(lead[0] + 1,))
+    s, other = _run_on(stream)
+    _used_on(s, other, xq, xs, wq, ws, bias, offsets)
+    with torch.cuda.stream(s):
+        if K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16:
+            xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
+        y = torch.empty((M, lead[-1]), dtype=out_dtype, device=xq.device)
+        tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), C.c_void_p(s.cuda_stream))
+        if offsets is None:
+            _check(lib().ep_gemm_int8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, lead[-1], xq.shape[1], *tail),
+                   "ep_gemm_int8")
+        else:
+            _check(lib().ep_gemm_int8_experts(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), lead[0], M,
+                                              lead[-1], xq.shape[1], *tail), "ep_gemm_int8_experts")
+    return y
+
+
+def gemm_int8(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
+    """Y = diag(xs) Xq Wq^T diag(ws) (+ bias) from INT8 codes xq [M, K] and wq [N, K] with a scale per
+    token xs [M] and per channel ws [N] (quantize_rows_int8; a weight's codes and scales come from
+    Handle.decompress(torch.int8)); exact int32 sums, output BF16 (default), FP16 or FP32. K a multiple
+    of 16 and 16-byte aligned codes are read in place, others are laid out first (pad_rows_int8). On
+    `stream` (default: the current stream; another stream first waits for the current one)."""
+    return _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype, stream)
+
+
+def gemm_int8_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream=None):
+    """gemm_int8 with a weight per expert, in one launch: rows offsets[e] ... offsets[e + 1] - 1 of xq
+    [R, K] meet wq[e] ([experts, N, K], scales ws and bias [experts, N]); rows behind the last expert's
+    come out zero. offsets: int32 on the GPU, as sort_tokens gives them (ascending from 0, at most R;
+    they are not read on the host)."""
+    return _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype, stream)
+
+
+# ------------------------------------------------------------------------------------ expert routing
+def _sort_raw(x, ids, n_experts, s):
+    torch = _torch()
+    T, k = ids.shape
+    _, H, ldx = _need_rows(x, "x", tuple(_torch_dtype(c) for c in (F32, BF16, F16, F8E4M3, I8, U8)))
+    need = C.c_size_t()
+    _check(lib().ep_sort_tokens_scratch(T, k, n_experts, C.byref(need)), "ep_sort_tokens")
+    rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
+    pos = torch.empty((T, k), dtype=torch.int32, device=x.device)
+    scratch = torch.empty(need.value, dtype=torch.uint8, device=x.device) if need.value else None
+    _check(lib().ep_sort_tokens(_ptr(x), _dtype_code(x.dtype), T, H, ldx, _ptr(ids), ids.element_size(), k, n_experts,
+                                _ptr(rows), _ptr(offsets), _ptr(pos), _ptr(scratch), C.c_void_p(s.cuda_stream)),
+           "ep_sort_tokens")
+    return rows, offsets, pos
+
+
+def _combine_raw(ys, pos, weights, s):
+    torch = _torch()
+    T, k = pos.shape
+    R, H = ys.shape
+    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+    _check(lib().ep_combine_tokens(_ptr(ys), _dtype_code(ys.dtype), _ptr(pos), _ptr(weights), T, k, H, R, _ptr(y),
+                                   C.c_void_p(s.cuda_stream)), "ep_combine_tokens")
+    return y
+
+
+_routing = None
+
+
+def _routing_functions():
+    """The autograd functions of sort_tokens and combine_tokens (torch is imported on first use). Their
+    gradients run on the stream the forward ran on, which autograd makes current."""
+    global _routing
+    if _routing is None:
+        torch = _torch()
+        once = torch.autograd.function.once_differentiable
+
+        class SortTokens(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, x, ids, n_experts):
+                rows, offsets, pos = _sort_raw(x, ids, n_experts, torch.cuda.current_stream())
+                ctx.save_for_backward(pos)
+                ctx.mark_non_differentiable(offsets, pos)
+                return rows, offsets, pos
+
+            @staticmethod
+            @once
+            def backward(ctx, d_rows, *_):
+                # a token's gradient is the sum of its rows'; dropped choices have no part in it
+                (pos,) = ctx.saved_tensors
+                return _combine_raw(d_rows.contiguous(), pos, None, torch.cuda.current_stream()), None, None
+
+        class CombineTokens(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, ys, pos, weights):
+                want_w = weights is not None and ctx.needs_input_grad[2]
+                ctx.save_for_backward(ys if want_w else None, pos, weights)
+                ctx.rows = ys.shape[0]
+                return _combine_raw(ys, pos, weights, torch.cuda.current_stream())
+
+            @staticmethod
+            @once
+            def backward(ctx, dy):
+                ys, pos, weights = ctx.saved_tensors
+                dy = dy.contiguous()
+                T, k = pos.shape
+                H = dy.shape[1]
+                d_ys = torch.empty((ctx.rows, H), dtype=dy.dtype, device=dy.device) if ctx.needs_input_grad[0] else None
+                d_w = torch.empty((T, k), dtype=torch.float32, device=dy.device) if ys is not None else None
+                _check(lib().ep_combine_tokens_grad(_ptr(ys), _dtype_code(dy.dtype), _ptr(pos), _ptr(weights), _ptr(dy),
+                                                    T, k, H, ctx.rows, _ptr(d_ys), _ptr(d_w),
+                                                    C.c_void_p(torch.cuda.current_stream().cuda_stream)),
+                       "ep_combine_tokens_grad")
+                return d_ys, None, d_w
+
+        _routing = SortTokens, CombineTokens
+    return _routing
+
+
+def sort_tokens(x, expert_ids, n_experts: int, stream=None):
+    """Tokens sorted by the experts they chose. x: [T, H] (any element type; rows may be further apart
+    than H), expert_ids: [T, k] int32 or int64; a number outside 0 ... n_experts - 1 drops the choice.
+    Returns (rows [T k, H], offsets [n_experts + 1] int32, pos [T, k] int32): expert e has rows offsets[e]
+    ... offsets[e + 1] - 1, in the order of the choices; choice (t, j) is row pos[t, j], or dropped, with
+    pos[t, j] = -1 - row of a zero row behind the last expert's. Differentiable in x; the host waits for
+    nothing. On `stream` (default: the current stream; another stream first waits for the current one)."""
+    torch = _torch()
+    if expert_ids.dim() != 2 or expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError("expert_ids must be an int32 or int64 tensor of shape [tokens, choices]")
+    _need(expert_ids, "expert_ids", expert_ids.dtype)
+    if x.dim() != 2 or x.shape[0] != expert_ids.shape[0]:
+        raise ValueError(f"x must have shape [{expert_ids.shape[0]}, H], got {tuple(x.shape)}")
+    s, other = _run_on(stream)
+    with torch.cuda.stream(s):
+        if torch.is_grad_enabled() and x.requires_grad:
+            out = _routing_functions()[0].apply(x, expert_ids, int(n_experts))
+        else:
+            out = _sort_raw(x, expert_ids, int(n_experts), s)
+    _used_on(s, other, x, expert_ids)
+    return out
+
+
+def combine_tokens(ys, pos, weights=None, stream=None):
+    """The experts' rows summed back per token: y[t] = sum over j of weights[t, j] ys[pos[t, j]] in fp32,
+    rounded once to the rows' type; dropped choices are left out, and without weights they are 1. ys:
+    [T k, H] BF16, FP16 or FP32 (more rows are allowed where no gradient is wanted), pos: sort_tokens'
+    positions [T, k], weights: fp32 [T, k]. Differentiable in ys and weights. On `stream` (default: the
+    current stream; another stream first waits for the current one)."""
+    torch = _torch()
+    if ys.dim() != 2 or ys.dtype not in _float_types():
+        raise ValueError(f"ys must be a bfloat16, float16 or float32 matrix, got {ys.dtype} of shape {tuple(ys.shape)}")
+    _need(ys, "ys", ys.dtype)
+    if pos.dim() != 2:
+        raise ValueError("pos must have shape [tokens, choices]")
+    _need(pos, "pos", torch.int32)
+    if weights is not None:
+        _need(weights, "weights", torch.float32, shape=tuple(pos.shape))
+    grad = torch.is_grad_enabled() and (ys.requires_grad or (weights is not None and weights.requires_grad))
+    if grad and ys.shape[0] != pos.numel():
+        raise ValueError(f"the gradient takes one row per choice: ys has {ys.shape[0]} rows for {pos.numel()} choices")
+    s, other = _run_on(stream)
+    with torch.cuda.stream(s):
+        if grad:
+            y = _routing_functions()[1].apply(ys, pos, weights)
+        else:
+            y = _combine_raw(ys, pos, weights, s)
+    _used_on(s, other, ys, pos, weights)
+    return y
+
+
 class CompressedLinear:
     """Linear layer that keeps only the compressed weight and decodes it on every forward
     ("EntroPack PyTorch Guide", section "Replace one linear layer before a whole model").
@@ -446,13 +695,15 @@ class CompressedLinear:
     out_features <= 4096; else the library's own).
     compute="fp8": the weight is decoded to FP8 E4M3 with its row scales and the activations are
     quantized per row; the codes meet in the FP8 MFMA, fused in the same cases, else on slices.
+    compute="int8": the weight is decoded slice by slice to INT8 with its row scales, the activations
+    are quantized per row (quantize_rows_int8), and the codes meet in the INT8 MFMA (gemm_int8).
 
     The forward takes BF16 activations. Other dtypes are refused unless cast=True is passed, so a
     precision change is never silent ("Diagnose compression failures in the correct order")."""
 
     def __init__(self, stream: bytes, bias=None, compute: str = "bf16"):
-        if compute not in ("bf16", "fp8"):
-            raise ValueError("compute must be 'bf16' or 'fp8'")
+        if compute not in ("bf16", "fp8", "int8"):
+            raise ValueError("compute must be 'bf16', 'fp8' or 'int8'")
         self.stream = stream
         self.handle = Handle(stream)
         self.out_features, self.in_features = self.handle.shape
@@ -511,9 +762,9 @@ class CompressedLinear:
             x2 = x.reshape(rows, shp[-1]).to(torch.bfloat16).contiguous()
             y = torch.empty((x2.shape[0], self.out_features), dtype=torch.bfloat16, device=x.device)
             bp = C.c_void_p(self.bias.data_ptr()) if self.bias is not None else None
-            fn = lib().ep_linear_forward_fp8 if self.compute == "fp8" else lib().ep_linear_forward
-            _check(fn(self.handle.ptr, C.c_void_p(x2.data_ptr()), x2.shape[0], bp, C.c_void_p(y.data_ptr()),
-                      C.c_void_p(s.cuda_stream)), "ep_linear_forward" + ("_fp8" if self.compute == "fp8" else ""))
+            name = "ep_linear_forward" + ("" if self.compute == "bf16" else "_" + self.compute)
+            _check(getattr(lib(), name)(self.handle.ptr, C.c_void_p(x2.data_ptr()), x2.shape[0], bp,
+                                        C.c_void_p(y.data_ptr()), C.c_void_p(s.cuda_stream)), name)
         _used_on(s, other, x2, self.bias)   # x (or its converted copy) is read on s after this returns
         return y.reshape(*shp[:-1], self.out_features)
 
@@ -532,7 +783,7 @@ def linear_forward_many(layers, x, stream=None):
     if not layers:
         return []
     fp8 = layers[0].compute == "fp8"
-    if len(layers) > 32 or any(l.compute != layers[0].compute for l in layers):
+    if len(layers) > 32 or any(l.compute != layers[0].compute or l.compute == "int8" for l in layers):
         return [l(x, stream=stream) for l in layers]
     K = layers[0].in_features
     shp = x.shape

@@ -17,7 +17,9 @@
 #include "ep_internal.h"
 #include "fused.h"
 #include "gemm.h"
+#include "int8.h"
 #include "kernels.h"
+#include "route.h"
 #include "static_scratch.h"
 
 struct ep_handle {
@@ -408,6 +410,43 @@ ep_status linear_forward(const ep_handle* w, const void* dev_x, int64_t M, const
     }
     he = ws.queued();
     return he == hipSuccess ? EP_OK : hip_fail(he, "recording the workspace event");
+}
+
+// Checks and launch of the INT8 products (experts = 0: one weight for all rows).
+ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const int32_t* offsets,
+                    int experts, int64_t M, int64_t N, int64_t K, const void* bias, ep_dtype out, void* y, hipStream_t s) {
+    if (M < 0 || N < 0 || K < 0) return fail(EP_EINVAL, "negative size");
+    if (out != EP_BF16 && out != EP_F16 && out != EP_F32)
+        return fail(EP_EUNSUPPORTED, "the INT8 product writes BF16, F16 or F32");
+    if (K % 16) return fail(EP_EINVAL, "K must be a multiple of 16 (ep_pad_rows_int8 lays other rows out)");
+    if (K > ep::kI8MaxK) return fail(EP_ERANGE, "K above 131071: the int32 sums could overflow");
+    if (M == 0 || N == 0) return EP_OK;
+    if ((K > 0 && (!xq || !wq)) || !xs || !ws || !y) return fail(EP_EINVAL, "null pointer");
+    if (M > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "M and N must be below 2^31");
+    if ((reinterpret_cast<uintptr_t>(xq) | reinterpret_cast<uintptr_t>(wq)) & 15)
+        return fail(EP_EINVAL, "X and W codes must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(y) & (out == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "Y is not aligned to its elements");
+    const ep::GemmI8Args g{xq, xs, wq, ws, static_cast<const uint16_t*>(bias), y, offsets, (int)M, (int)N, (int)K,
+                           (int)K, (int)K, (int)N, experts, out};
+    const hipError_t e = ep::launch_gemm_i8(g, s);
+    if (e == hipErrorInvalidValue) return fail(EP_ERANGE, "M x N is too large for one launch");
+    return e == hipSuccess ? EP_OK : hip_fail(e, "int8 gemm launch");
+}
+
+ep_status check_choices(int64_t T, int k, int E) {
+    if (T < 0 || k < 0) return fail(EP_EINVAL, "negative size");
+    if (E < 1 || E > ep::kRouteMaxExperts) return fail(EP_ERANGE, "the number of experts must be 1 ... 1024");
+    if (k > 0 && T > INT32_MAX / k) return fail(EP_ERANGE, "T k must be below 2^31");
+    return EP_OK;
+}
+
+ep_status check_combine(ep_dtype dtype, int64_t T, int k, int64_t H, int64_t R) {
+    if (T < 0 || k < 0 || H < 0 || R < 0) return fail(EP_EINVAL, "negative size");
+    if (dtype != EP_BF16 && dtype != EP_F16 && dtype != EP_F32)
+        return fail(EP_EUNSUPPORTED, "tokens are summed in BF16, F16 or F32 rows");
+    if (R > INT32_MAX || (k > 0 && T > INT32_MAX / k)) return fail(EP_ERANGE, "R and T k must be below 2^31");
+    if (H > 0 && ((R > 0 && H > (INT64_MAX / 8) / R) || (T > 0 && H > (INT64_MAX / 8) / T))) return fail(EP_ERANGE, "the rows are too large");
+    return EP_OK;
 }
 
 }  // namespace
@@ -957,6 +996,183 @@ ep_status ep_linear_forward_fp8(const ep_handle* w, const void* dev_x, int64_t M
         }
         e = ws.queued();
         return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
+    });
+}
+
+ep_status ep_quantize_rows_int8(const void* dev_x, ep_dtype src, int64_t M, int64_t K, int64_t ldx, int8_t* dev_q,
+                                float* dev_scale, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (M < 0 || K < 0) return fail(EP_EINVAL, "negative size");
+        if (src != EP_BF16 && src != EP_F16 && src != EP_F32)
+            return fail(EP_EUNSUPPORTED, "the INT8 quantizer takes BF16, F16 or F32 rows");
+        if (M == 0) return EP_OK;
+        if (M > INT32_MAX || K > INT32_MAX) return fail(EP_ERANGE, "M and K must be below 2^31");
+        if (ldx < K) return fail(EP_EINVAL, "rows of X overlap (ldx < K)");
+        if (ldx > (INT64_MAX / 8) / M) return fail(EP_ERANGE, "X is too large");
+        if ((K > 0 && (!dev_x || !dev_q)) || !dev_scale) return fail(EP_EINVAL, "null pointer");
+        if (reinterpret_cast<uintptr_t>(dev_x) & (src == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "X is not aligned to its elements");
+        hipError_t e = ep::launch_quantize_rows_i8(dev_x, src, (int)M, (int)K, ldx, dev_q, dev_scale,
+                                                   static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "quantize launch");
+    });
+}
+
+ep_status ep_gemm_int8(const int8_t* dev_xq, const float* dev_xs, const int8_t* dev_wq, const float* dev_ws, int64_t M,
+                       int64_t N, int64_t K, const void* dev_bias, ep_dtype out, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        return gemm_int8(dev_xq, dev_xs, dev_wq, dev_ws, nullptr, 0, M, N, K, dev_bias, out, dev_y,
+                         static_cast<hipStream_t>(hip_stream));
+    });
+}
+
+ep_status ep_gemm_int8_experts(const int8_t* dev_xq, const float* dev_xs, const int8_t* dev_wq, const float* dev_ws,
+                               const int32_t* dev_offsets, int E, int64_t R, int64_t N, int64_t K, const void* dev_bias,
+                               ep_dtype out, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (E < 1 || E > ep::kRouteMaxExperts) return fail(EP_ERANGE, "the number of experts must be 1 ... 1024");
+        if (R > 0 && N > 0 && !dev_offsets) return fail(EP_EINVAL, "null offsets");
+        return gemm_int8(dev_xq, dev_xs, dev_wq, dev_ws, dev_offsets, E, R, N, K, dev_bias, out, dev_y,
+                         static_cast<hipStream_t>(hip_stream));
+    });
+}
+
+ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_t* dev_dst, int64_t ld, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (rows < 0 || K < 0) return fail(EP_EINVAL, "negative size");
+        if (ld < K || ld % 16) return fail(EP_EINVAL, "ld must be a multiple of 16, at least K");
+        if (rows == 0 || ld == 0) return EP_OK;
+        if (ld > INT32_MAX || rows > INT64_MAX / ld) return fail(EP_ERANGE, "the matrix is too large");
+        if (rows * (ld / 16) > 0xFFFFFE00ll) return fail(EP_ERANGE, "the matrix is too large for one call");
+        if ((K > 0 && !dev_src) || !dev_dst) return fail(EP_EINVAL, "null pointer");
+        if (reinterpret_cast<uintptr_t>(dev_dst) & 15) return fail(EP_EINVAL, "dst must be 16-byte aligned");
+        hipError_t e = ep::launch_pad_rows_i8(dev_src, rows, (int)K, dev_dst, (int)ld, static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "pad launch");
+    });
+}
+
+ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t M, const void* dev_bias, void* dev_y,
+                                 void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (!w) return fail(EP_EINVAL, "null handle");
+        if (ep_status st = on_its_device(w); st != EP_OK) return st;
+        if (w->view.mode != EP_MODE_LOSSY_E8) return fail(EP_EUNSUPPORTED, "the linear forward takes a lossy stream");
+        const int64_t N = w->view.rows, K = w->view.cols;
+        if (M < 0) return fail(EP_EINVAL, "negative M");
+        if (M == 0 || N == 0) return EP_OK;
+        if (!dev_y || (K > 0 && !dev_x)) return fail(EP_EINVAL, "null pointer");
+        if (M > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "M and out_features must be below 2^31");
+        if (K % 16) return fail(EP_EINVAL, "in_features must be a multiple of 16 for the INT8 forward");
+        if (K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131071: the int32 sums could overflow");
+        if (reinterpret_cast<uintptr_t>(dev_x) & 15) return fail(EP_EINVAL, "X must be 16-byte aligned");
+        hipStream_t s = static_cast<hipStream_t>(hip_stream);
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        if (K == 0) {
+            // in_features 0: an empty sum, Y = bias (or zeros)
+            e = ep::launch_gemv_finish(nullptr, 0, static_cast<const uint16_t*>(dev_bias), static_cast<uint16_t*>(dev_y), M, N,
+                                       s);
+            return e == hipSuccess ? EP_OK : hip_fail(e, "empty product launch");
+        }
+        const int tr = w->view.tile_rows;
+        int64_t slice = (int64_t)(kSliceBytes / (size_t)K) / tr * tr;
+        if (slice < tr) slice = tr;
+        if (slice > N) slice = (N + tr - 1) / tr * tr;
+        // workspace: X codes [M][K] | X scales [M] | weight codes [slice][K] | weight scales [slice]
+        const size_t o_xs = up((size_t)M * (size_t)K, 256), o_wq = up(o_xs + 4 * (size_t)M, 256);
+        const size_t o_ws = up(o_wq + (size_t)slice * (size_t)K, 256), need = o_ws + 4 * (size_t)slice;
+        WsLease ws;
+        if ((e = ws_acquire(dev, s, need, &ws)) != hipSuccess)
+            return hip_fail(e, "hipMalloc for the linear forward workspace");
+        uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+        int8_t* xq = reinterpret_cast<int8_t*>(ws8);
+        float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+        int8_t* wq = reinterpret_cast<int8_t*>(ws8 + o_wq);
+        float* wsc = reinterpret_cast<float*>(ws8 + o_ws);
+        e = ep::launch_quantize_rows_i8(dev_x, EP_BF16, (int)M, (int)K, K, xq, xs, s);
+        if (e != hipSuccess) return hip_fail(e, "quantize launch");
+        const ep::MatDesc full = desc_for(w, ep::CT_I8, wq, wsc);
+        for (int64_t r0 = 0; r0 < N; r0 += slice) {
+            const int64_t rows = std::min<int64_t>(slice, N - r0);
+            ep::MatDesc d = full;                  // rows r0 .. r0 + rows of the weight
+            d.index += (size_t)(r0 / tr) * w->view.tiles_c;
+            d.row_scale += r0;
+            d.row_qmax += r0;
+            d.rows = (uint32_t)rows;
+            e = ep::launch_group(&d, 1, s);
+            if (e != hipSuccess) return hip_fail(e, "slice decode launch");
+            ep::GemmI8Args g{xq, xs, wq, wsc, dev_bias ? static_cast<const uint16_t*>(dev_bias) + r0 : nullptr,
+                             static_cast<uint16_t*>(dev_y) + r0, nullptr, (int)M, (int)rows, (int)K, (int)K, (int)K, (int)N,
+                             0, EP_BF16};
+            e = ep::launch_gemm_i8(g, s);
+            if (e != hipSuccess) return hip_fail(e, "slice int8 gemm launch");
+        }
+        e = ws.queued();
+        return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
+    });
+}
+
+ep_status ep_sort_tokens_scratch(int64_t T, int k, int E, size_t* bytes) {
+    return guarded([&]() -> ep_status {
+        if (!bytes) return fail(EP_EINVAL, "null pointer");
+        if (ep_status st = check_choices(T, k, E); st != EP_OK) return st;
+        *bytes = ep::sort_tokens_scratch(T, k, E);
+        return EP_OK;
+    });
+}
+
+ep_status ep_sort_tokens(const void* dev_x, ep_dtype dtype, int64_t T, int64_t H, int64_t ldx, const void* dev_ids,
+                         int id_bytes, int k, int E, void* dev_rows, int32_t* dev_offsets, int32_t* dev_pos,
+                         void* dev_scratch, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (ep_status st = check_choices(T, k, E); st != EP_OK) return st;
+        const int es = ep::element_bytes(dtype);
+        if (es <= 0) return fail(EP_EUNSUPPORTED, "unknown element type");
+        if (H < 0) return fail(EP_EINVAL, "negative size");
+        if (ldx < H) return fail(EP_EINVAL, "rows of X overlap (ldx < H)");
+        const int64_t n = T * k;
+        if (H > 0 && (n > (INT64_MAX / 8) / H || (T > 0 && ldx > (INT64_MAX / 8) / T))) return fail(EP_ERANGE, "the rows are too large");
+        if (id_bytes != 4 && id_bytes != 8) return fail(EP_EINVAL, "expert numbers must be int32 or int64");
+        if (!dev_offsets || (n > 0 && (!dev_ids || !dev_pos))) return fail(EP_EINVAL, "null pointer");
+        if (n > 0 && H > 0 && dev_rows && !dev_x) return fail(EP_EINVAL, "null pointer");
+        if (ep::sort_tokens_scratch(T, k, E) > 0 && !dev_scratch) return fail(EP_EINVAL, "null scratch");
+        if ((reinterpret_cast<uintptr_t>(dev_x) | reinterpret_cast<uintptr_t>(dev_rows)) & (uintptr_t)(es - 1))
+            return fail(EP_EINVAL, "X or the rows are not aligned to their elements");
+        const ep::RouteArgs r{dev_ids, id_bytes, T, k, E, dev_offsets, dev_pos};
+        hipError_t e = ep::launch_sort_tokens(r, dev_x, ldx * es, H * es, dev_rows, dev_scratch,
+                                              static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "token sort launch");
+    });
+}
+
+ep_status ep_combine_tokens(const void* dev_ys, ep_dtype dtype, const int32_t* dev_pos, const float* dev_w, int64_t T,
+                            int k, int64_t H, int64_t R, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (ep_status st = check_combine(dtype, T, k, H, R); st != EP_OK) return st;
+        if (T == 0 || H == 0) return EP_OK;
+        if (!dev_y || (k > 0 && !dev_pos) || (R > 0 && !dev_ys)) return fail(EP_EINVAL, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(dev_ys) | reinterpret_cast<uintptr_t>(dev_y)) & (dtype == EP_F32 ? 3 : 1))
+            return fail(EP_EINVAL, "the rows are not aligned to their elements");
+        const ep::CombineArgs c{dev_ys, dev_pos, dev_w, T, H, R, k, dtype};
+        hipError_t e = ep::launch_combine_tokens(c, dev_y, static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "token sum launch");
+    });
+}
+
+ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32_t* dev_pos, const float* dev_w,
+                                 const void* dev_dy, int64_t T, int k, int64_t H, int64_t R, void* dev_d_ys,
+                                 float* dev_d_w, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (ep_status st = check_combine(dtype, T, k, H, R); st != EP_OK) return st;
+        if (R != T * k) return fail(EP_EINVAL, "the gradient takes one row per choice (R = T k)");
+        if (T == 0 || k == 0 || (!dev_d_ys && !dev_d_w)) return EP_OK;
+        if (!dev_pos || (H > 0 && (!dev_dy || (dev_d_w && !dev_ys)))) return fail(EP_EINVAL, "null pointer");
+        if ((reinterpret_cast<uintptr_t>(dev_ys) | reinterpret_cast<uintptr_t>(dev_dy) |
+             reinterpret_cast<uintptr_t>(dev_d_ys)) & (dtype == EP_F32 ? 3 : 1))
+            return fail(EP_EINVAL, "the rows are not aligned to their elements");
+        const ep::CombineArgs c{dev_ys, dev_pos, dev_w, T, H, R, k, dtype};
+        hipError_t e = ep::launch_combine_tokens_grad(c, dev_dy, dev_d_ys, dev_d_w, static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "token sum gradient launch");
     });
 }
 

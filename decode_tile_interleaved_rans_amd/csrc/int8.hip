@@ -1,0 +1,594 @@
+// gfx950 INT8 row quantizer and INT8 matrix products: Y[m][n] = sx[m] sw[n] sum_k X[m][k] W[n][k]
+// (+ bias[n]), int32 sums on the matrix cores (v_mfma_i32_16x16x64_i8), fp32 epilogue. The weight is
+// the INT8 container of the decoder (codes and one scale per output channel), the activations carry
+// one scale per row, so both scales leave the sum and the sum itself is exact: any split or order
+// of K gives the same bits.
+//
+// Operand lane layout (v_mfma_i32_16x16x64_i8, checked on the device): lane l supplies 16 codes of
+// A row l % 16 and of B column l % 16, K group l / 16, and receives C[4 (l / 16) + i][l % 16],
+// i < 4. A and B take the same 16 K positions per lane, so equal k meet whatever the order. W is
+// the A operand and X the B operand: a lane then holds four consecutive output columns of one row.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "entropack.h"
+#include "int8.h"
+#include "kernels.h"
+
+namespace ep {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned short u16x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int64_t kMaxThreads = 0xFFFFFFFFll;   // of a grid
+constexpr uint32_t kOob = 0x80000000u;      // an offset past every resource: the load returns 0
+
+__device__ __forceinline__ uint16_t to_bf16(float v) {
+    return (uint16_t)(__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v, 0.0f}, bf16x2)) & 0xFFFFu);
+}
+__device__ __forceinline__ uint16_t to_f16(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+
+// ------------------------------------------------------------------------------- row quantizer
+// a = max |x| over the row (raised to 2^-100 when smaller, unless zero), scale = a / 127 (fp32),
+// code = 127 x / a rounded to nearest, ties to even, decided exactly. A zero row gets scale 0 and
+// codes 0; a row with an infinity or a NaN gets scale NaN and codes 0, so that every product with
+// it is NaN instead of a plausible number.
+//
+// The quotient is formed as x (127 / a), off by at most 1.5e-5 at 127 (two roundings); where it
+// falls within 5e-5 of a rounding border f + 1/2 the code is decided by comparing 254 |x| with
+// (2 f + 1) a in fp64, where both products are exact (at most 32 bits).
+//
+// One row per block of 256 threads or, for short rows, per wave; the row stays in registers between
+// the maximum and the codes (CH chunks of 8 elements per thread; CH = 0 reads it twice), so it is
+// read once from memory.
+constexpr float kMagic = 12582912.0f;       // 1.5 * 2^23: v + kMagic holds rne(v) in its low mantissa bits
+
+template <int SRC> struct Elem { typedef uint16_t type; };
+template <> struct Elem<EP_F32> { typedef uint32_t type; };
+
+template <int SRC>
+__device__ __forceinline__ float elem_value(uint32_t bits) {
+    if constexpr (SRC == EP_F32) return __uint_as_float(bits);
+    if constexpr (SRC == EP_BF16) return __uint_as_float(bits << 16);
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+template <int SRC> __device__ __forceinline__ uint32_t abs_bits(uint32_t b) { return b & (SRC == EP_F32 ? 0x7FFFFFFFu : 0x7FFFu); }
+template <int SRC> constexpr uint32_t inf_bits() { return SRC == EP_F32 ? 0x7F800000u : SRC == EP_BF16 ? 0x7F80u : 0x7C00u; }
+
+// Eight consecutive elements; one at a time (V = 1) where rows are not 16-byte aligned.
+template <int SRC, int V>
+struct Chunk {
+    typename Elem<SRC>::type e[V];
+};
+template <int SRC, int V>
+__device__ __forceinline__ Chunk<SRC, V> load_chunk(const typename Elem<SRC>::type* x) {
+    Chunk<SRC, V> c;
+    if constexpr (V == 8) {
+        const uint4* p = reinterpret_cast<const uint4*>(x);
+        constexpr int n = (int)sizeof(Chunk<SRC, V>) / 16;
+        uint4 v[n];
+#pragma unroll
+        for (int i = 0; i < n; ++i) v[i] = p[i];
+        __builtin_memcpy(&c, v, sizeof c);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c.e[i] = x[i];
+    }
+    return c;
+}
+
+template <int SRC, int V>
+__device__ __forceinline__ uint32_t chunk_max(const Chunk<SRC, V>& c, uint32_t a) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const uint32_t b = abs_bits<SRC>(c.e[i]);
+        a = a > b ? a : b;
+    }
+    return a;
+}
+
+// The codes of a chunk, one byte each (low byte first).
+template <int SRC, int V>
+__device__ __forceinline__ void chunk_codes(const Chunk<SRC, V>& c, float inv, float amax, uint32_t* out) {
+    uint32_t m[V];
+    bool close = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const float t = elem_value<SRC>(c.e[i]) * inv;
+        const float r = t + kMagic;
+        m[i] = __float_as_uint(r);
+        close |= fabsf(t - (r - kMagic)) > 0.49995f;
+    }
+    if (close) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            // floor f of the magnitude, then 127 |x| / a against the border f + 1/2: both products exact
+            const float x = elem_value<SRC>(c.e[i]), f = floorf(fabsf(x * inv));
+            if (fabsf(fabsf(x * inv) - f - 0.5f) > 5e-5f) continue;
+            const double l = 254.0 * (double)fabsf(x), r = (double)(2.0f * f + 1.0f) * (double)amax;
+            const int n = (int)f, q = l > r || (l == r && (n & 1)) ? n + 1 : n;
+            m[i] = (uint32_t)(x < 0.0f ? -q : q);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < (V + 3) / 4; ++i) {
+        uint32_t w = 0;
+#pragma unroll
+        for (int j = 0; j < 4 && 4 * i + j < V; ++j) w |= (m[4 * i + j] & 0xFFu) << (8 * j);
+        out[i] = w;
+    }
+}
+
+// TPR threads per row (64 or 256), V elements per chunk (8 or 1), CH chunks per thread held in registers.
+template <int SRC, int TPR, int V, int CH>
+__global__ __launch_bounds__(256) void quantize_rows_i8(const void* Xv, int M, int K, int64_t ldx, int8_t* Q, float* S) {
+    typedef typename Elem<SRC>::type T;
+    __shared__ uint32_t wmax[4];
+    const int t = threadIdx.x % TPR;
+    // m is uniform in the block for TPR 256 (block barriers below), in the wave for TPR 64; a grid may
+    // have at most 2^32 - 1 threads, so the blocks stride over the rows
+    for (int64_t m = (int64_t)blockIdx.x * (256 / TPR) + threadIdx.x / TPR; m < M; m += (int64_t)gridDim.x * (256 / TPR)) {
+        const T* x = static_cast<const T*>(Xv) + m * ldx;
+        int8_t* q = Q + m * K;
+        constexpr int R = CH > 0 ? CH : 1;
+        Chunk<SRC, V> v[R];
+        uint32_t a = 0;
+        if constexpr (CH > 0) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int k = V * (t + TPR * c);
+                if (k < K) v[c] = load_chunk<SRC, V>(x + k);
+                else
+#pragma unroll
+                    for (int i = 0; i < V; ++i) v[c].e[i] = 0;
+            }
+#pragma unroll
+            for (int c = 0; c < CH; ++c) a = chunk_max<SRC, V>(v[c], a);
+        } else {
+            for (int k = V * t; k < K; k += V * TPR) a = chunk_max<SRC, V>(load_chunk<SRC, V>(x + k), a);
+        }
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            const uint32_t b = (uint32_t)__shfl_xor((int)a, o);
+            a = a > b ? a : b;
+        }
+        if constexpr (TPR == 256) {
+            if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = a;
+            __syncthreads();
+            a = wmax[0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i) a = a > wmax[i] ? a : wmax[i];
+            __syncthreads();                                       // wmax is free for the next row
+        }
+        float amax = elem_value<SRC>(a);
+        const bool bad = a >= inf_bits<SRC>();
+        if (a == 0 || bad) {
+            if (t == 0) S[m] = bad ? __builtin_nanf("") : 0.0f;
+            for (int k = t; k < K; k += TPR) q[k] = 0;
+            continue;
+        }
+        amax = fmaxf(amax, 0x1p-100f);
+        if (t == 0) S[m] = amax / 127.0f;
+        const float inv = 127.0f / amax;
+        auto store = [&](int k, const Chunk<SRC, V>& c) {
+            uint32_t o[(V + 3) / 4];
+            chunk_codes<SRC, V>(c, inv, amax, o);
+            if constexpr (V == 8) *reinterpret_cast<uint2*>(q + k) = make_uint2(o[0], o[1]);
+            else q[k] = (int8_t)o[0];
+        };
+        if constexpr (CH > 0) {
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                const int k = V * (t + TPR * c);
+                if (k < K) store(k, v[c]);
+            }
+        } else {
+            for (int k = V * t; k < K; k += V * TPR) store(k, load_chunk<SRC, V>(x + k));
+        }
+    }
+}
+
+template <int SRC, int TPR, int V, int CH>
+hipError_t quantize_go(const void* X, int M, int K, int64_t ldx, int8_t* Q, float* S, hipStream_t stream) {
+    const int64_t groups = ((int64_t)M + 256 / TPR - 1) / (256 / TPR);
+    const unsigned blocks = (unsigned)(groups < (1 << 20) ? groups : 1 << 20);
+    hipLaunchKernelGGL((quantize_rows_i8<SRC, TPR, V, CH>), dim3(blocks), dim3(256), 0, stream, X, M, K, ldx, Q, S);
+    return hipGetLastError();
+}
+
+template <int SRC>
+hipError_t quantize_src(const void* X, int M, int K, int64_t ldx, int8_t* Q, float* S, hipStream_t stream) {
+    const size_t es = sizeof(typename Elem<SRC>::type);
+    const bool vec = K % 8 == 0 && ((size_t)ldx * es) % 16 == 0 && !(reinterpret_cast<uintptr_t>(X) & 15) &&
+                     !(reinterpret_cast<uintptr_t>(Q) & 7);
+    if (!vec) return K <= 1024 ? quantize_go<SRC, 64, 1, 0>(X, M, K, ldx, Q, S, stream)
+                               : quantize_go<SRC, 256, 1, 0>(X, M, K, ldx, Q, S, stream);
+    if (K <= 512) return quantize_go<SRC, 64, 8, 1>(X, M, K, ldx, Q, S, stream);
+    if (K <= 1024) return quantize_go<SRC, 64, 8, 2>(X, M, K, ldx, Q, S, stream);
+    if (K <= 2048) return quantize_go<SRC, 256, 8, 1>(X, M, K, ldx, Q, S, stream);
+    if (K <= 4096) return quantize_go<SRC, 256, 8, 2>(X, M, K, ldx, Q, S, stream);
+    if (K <= 8192) return quantize_go<SRC, 256, 8, 4>(X, M, K, ldx, Q, S, stream);
+    if (K <= 16384) return quantize_go<SRC, 256, 8, 8>(X, M, K, ldx, Q, S, stream);
+    return quantize_go<SRC, 256, 8, 0>(X, M, K, ldx, Q, S, stream);
+}
+
+// ------------------------------------------------------------------------------- rows to 16 bytes
+// Codes whose rows are not 16-byte aligned (K % 16, or a base address inside a row) are copied once
+// to rows of K rounded up to 16 with zeros behind; the zeros add nothing to the sums.
+__global__ __launch_bounds__(256) void pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* dst, int ld) {
+    const int cpr = ld / 16;
+    const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (c >= rows * cpr) return;
+    const int64_t r = c / cpr;
+    const int k0 = 16 * (int)(c % cpr);
+    const uint8_t* s = reinterpret_cast<const uint8_t*>(src) + r * (int64_t)K + k0;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        w[i] = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (k0 + 4 * i + j < K) w[i] |= (uint32_t)s[4 * i + j] << (8 * j);
+    }
+    *reinterpret_cast<uint4*>(dst + r * (int64_t)ld + k0) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ------------------------------------------------------------------------------- tile of a block
+// The output tile of a block: rows [m0, m0 + BM) up to m_end, columns [n0, n0 + BN), of expert e
+// (0 without experts). e == experts stands for the rows behind the last expert's, which are zeroed;
+// `any` is false for a block without a tile (the grid holds the largest tile count that the row
+// count allows, since the split over the experts is known to the device only).
+struct TileAt {
+    int m0, m_end, n0, e;
+    bool any;
+};
+
+// Rows of expert e (e == experts: the rows behind), clamped to [0, M] so that no offset can lead
+// out of the buffers.
+__device__ __forceinline__ void expert_rows(const GemmI8Args& g, int e, int* a, int* b) {
+    const int lo = g.offsets[e], hi = e < g.experts ? g.offsets[e + 1] : g.M;
+    *a = lo < 0 ? 0 : lo < g.M ? lo : g.M;
+    *b = hi < *a ? *a : hi < g.M ? hi : g.M;
+}
+
+// Every wave looks the tile up on its own: 64 experts at a time, one per lane, a running sum of
+// their tile counts over the lanes.
+template <int BM>
+__device__ __forceinline__ TileAt expert_tile(const GemmI8Args& g, int tm) {
+    const int lane = threadIdx.x & 63;
+    int before = 0;
+    TileAt t{0, 0, 0, 0, false};
+    for (int e0 = 0; e0 <= g.experts; e0 += 64) {
+        int a = 0, b = 0;
+        if (e0 + lane <= g.experts) expert_rows(g, e0 + lane, &a, &b);
+        const int cnt = (b - a + BM - 1) / BM;
+        int sum = cnt;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(sum, o);
+            if (lane >= o) sum += v;
+        }
+        const int mine = before + sum - cnt;                   // tiles before this lane's expert
+        const uint64_t hit = __ballot(tm >= mine && tm < mine + cnt);
+        if (hit) {
+            const int l = __builtin_ctzll(hit);
+            t.e = __builtin_amdgcn_readfirstlane(e0 + l);
+            t.m0 = __builtin_amdgcn_readfirstlane(__shfl(a, l) + BM * (tm - __shfl(mine, l)));
+            t.m_end = __builtin_amdgcn_readfirstlane(__shfl(b, l));
+            t.any = true;
+            return t;
+        }
+        before += __shfl(sum, 63);
+    }
+    return t;
+}
+
+// Four consecutive outputs of a row (columns n .. n + 3 of n_end), converted and stored; `vec` when
+// rows of Y are aligned to four elements.
+template <typename F>
+__device__ __forceinline__ void store_out(void* Y, int out, int64_t at, const float* v, int count, bool vec, F) {
+    if (out == EP_F32) {
+        float* y = static_cast<float*>(Y) + at;
+        if (vec && count == 4) *reinterpret_cast<f32x4*>(y) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+            for (int i = 0; i < count; ++i) y[i] = v[i];
+        return;
+    }
+    uint16_t h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = out == EP_BF16 ? to_bf16(v[i]) : to_f16(v[i]);
+    uint16_t* y = static_cast<uint16_t*>(Y) + at;
+    if (vec && count == 4)
+        *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+    else
+        for (int i = 0; i < count; ++i) y[i] = h[i];
+}
+
+// The epilogue of one 16 x 16 part: the lane's four sums of output row m, columns n .. n + 3.
+__device__ __forceinline__ void finish4(const GemmI8Args& g, const TileAt& t, int m, int n, i32x4 acc, float sx, bool vec) {
+    if (m >= t.m_end || n >= g.N) return;
+    const int count = g.N - n < 4 ? g.N - n : 4;
+    const float* sw = g.sw + (int64_t)t.e * g.N + n;
+    const uint16_t* bias = g.bias ? g.bias + (int64_t)t.e * g.N + n : nullptr;
+    float v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int j = i < count ? i : 0;
+        v[i] = (float)acc[i] * sw[j] * sx;
+        if (bias) v[i] += __uint_as_float((uint32_t)bias[j] << 16);
+    }
+    store_out(g.Y, g.out, (int64_t)m * g.ldy + n, v, count, vec, 0);
+}
+
+__device__ __forceinline__ void zero_rows(const GemmI8Args& g, const TileAt& t, int bm, int bn) {
+    const int rows = t.m_end - t.m0 < bm ? t.m_end - t.m0 : bm, cols = g.N - t.n0 < bn ? g.N - t.n0 : bn;
+    for (int i = threadIdx.x; i < rows * cols; i += blockDim.x) {
+        const int64_t at = (int64_t)(t.m0 + i / cols) * g.ldy + t.n0 + i % cols;
+        if (g.out == EP_F32) static_cast<float*>(g.Y)[at] = 0.0f;
+        else static_cast<uint16_t*>(g.Y)[at] = 0;
+    }
+}
+
+__device__ __forceinline__ bool vec_out(const GemmI8Args& g) {
+    return g.ldy % 4 == 0 && !(reinterpret_cast<uintptr_t>(g.Y) & (g.out == EP_F32 ? 15 : 7));
+}
+
+// Rows [r0, r0 + ROWS) up to r_end of a row-major code matrix as a buffer resource: rows past r_end
+// read as zero.
+template <int ROWS>
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, int ld, int64_t r0, int64_t r_end) {
+    const int64_t left = r_end - r0;
+    const int n = (int)(left < ROWS ? left : ROWS);
+    const int bytes = __builtin_amdgcn_readfirstlane((n > 0 ? n : 0) * ld);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t*>(src + r0 * ld), 0, bytes, 0x00020000);
+}
+
+// ------------------------------------------------------------------------------- tiled product
+// A block of WGM x WGN waves owns a BM x BN tile of Y and walks K in steps of 128 codes. Both operand
+// tiles go straight from global memory into LDS (buffer_load ... lds, 16 bytes per lane, 8 rows of
+// 128 bytes per instruction), two stages: the loads of step k + 1 run while step k multiplies. The
+// eight 16-byte chunks of a row are swizzled: chunk c of row r sits at slot c ^ ((r / 2) % 8), so that
+// the 16 lanes of a fragment read (16 consecutive rows, one chunk) cover all banks.
+__device__ __forceinline__ int chunk_swizzle(int r) { return (r >> 1) & 7; }
+
+template <int ROWS, int NW>
+__device__ __forceinline__ void dma_rows(__amdgpu_buffer_rsrc_t rs, int ld, int k0, int K, uint8_t* lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int rr = lane >> 3;
+#pragma unroll
+    for (int j = 0; j < ROWS / 8 / NW; ++j) {
+        const int g = wave + NW * j;
+        const int k = k0 + 16 * ((lane & 7) ^ chunk_swizzle(8 * g + rr));
+        const uint32_t off = (uint32_t)((8 * g + rr) * ld + k) | ((uint32_t)((K - 1 - k) >> 31) & kOob);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + 1024 * g), 16, off, 0, 0, 0);
+    }
+}
+
+template <int BM, int BN, int WGM, int WGN, bool EXPERTS>
+__global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
+    constexpr int NW = WGM * WGN;
+    constexpr int TI = BM / WGM / 16, TJ = BN / WGN / 16;
+    constexpr int kStage = (BM + BN) * 128;
+    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+    const int tiles_n = (g.N + BN - 1) / BN;
+    TileAt t;
+    if constexpr (EXPERTS) {
+        t = expert_tile<BM>(g, (int)blockIdx.x / tiles_n);
+        if (!t.any) return;
+        t.n0 = __builtin_amdgcn_readfirstlane(((int)blockIdx.x % tiles_n) * BN);
+        if (t.e == g.experts) {
+            zero_rows(g, t, BM, BN);
+            return;
+        }
+    } else {
+        const int tiles_m = (g.M + BM - 1) / BM, nblk = tiles_m * tiles_n;
+        int b = blockIdx.x;
+        if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
+        constexpr int G = 4;
+        const int per_group = G * tiles_n, first_m = (b / per_group) * G;
+        const int gsize = tiles_m - first_m < G ? tiles_m - first_m : G;
+        t.m0 = __builtin_amdgcn_readfirstlane((first_m + (b % per_group) % gsize) * BM);
+        t.n0 = __builtin_amdgcn_readfirstlane(((b % per_group) / gsize) * BN);
+        t.m_end = g.M;
+        t.e = 0;
+    }
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc<BM>(g.X, g.ldx, t.m0, t.m_end);
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc<BN>(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
+
+    i32x4 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+
+    dma_rows<BM, NW>(rx, g.ldx, 0, g.K, lds);
+    dma_rows<BN, NW>(rw, g.ldw, 0, g.K, lds + BM * 128);
+    __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): this wave's loads landed
+    __syncthreads();
+    const int nk = (g.K + 127) / 128;
+    for (int kt = 0; kt < nk; ++kt) {
+        uint8_t* cur = lds + (kt & 1) * kStage;
+        if (kt + 1 < nk) {
+            uint8_t* nxt = lds + ((kt + 1) & 1) * kStage;
+            dma_rows<BM, NW>(rx, g.ldx, (kt + 1) * 128, g.K, nxt);
+            dma_rows<BN, NW>(rw, g.ldw, (kt + 1) * 128, g.K, nxt + BM * 128);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            i32x4 a[TI], b[TJ];
+            const int kc = 4 * ks + (lane >> 4);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                const int r = wm + 16 * i + (lane & 15);
+                a[i] = *reinterpret_cast<const i32x4*>(cur + r * 128 + ((kc ^ chunk_swizzle(r)) << 4));
+            }
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) {
+                const int r = wn + 16 * j + (lane & 15);
+                b[j] = *reinterpret_cast<const i32x4*>(cur + BM * 128 + r * 128 + ((kc ^ chunk_swizzle(r)) << 4));
+            }
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+        }
+        __builtin_amdgcn_s_waitcnt(0x0F70);                  // vmcnt(0): the next stage's loads landed
+        __syncthreads();                                     // ... for every wave; this stage is free
+    }
+
+    const bool vec = vec_out(g);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const int m = t.m0 + wm + 16 * i + (lane & 15);
+        const float sx = m < t.m_end ? g.sx[m] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) finish4(g, t, m, t.n0 + wn + 16 * j + 4 * (lane >> 4), acc[i][j], sx, vec);
+    }
+}
+
+// ------------------------------------------------------------------------------- few rows
+// For a few rows of X (a decoding step): W streams once from memory straight into MFMA registers, no
+// LDS staging. A block owns 16 output columns; its 8 waves split K in chunks of 128 codes, four
+// chunks of loads in flight each, every wave multiplying MT tiles of 16 rows; the int32 partial sums
+// meet in LDS.
+constexpr int kSkinnyWaves = 8;
+constexpr int kSkinnyUnroll = 4;
+
+template <int MT, bool EXPERTS>
+__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_i8(GemmI8Args g) {
+    __shared__ __align__(16) int red[kSkinnyWaves][MT][256];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int r = lane & 15, kq = lane >> 4;
+    const int tiles_n = (g.N + 15) / 16;
+    TileAt t{0, g.M, 0, 0, true};
+    if constexpr (EXPERTS) {
+        t = expert_tile<16 * MT>(g, (int)blockIdx.x / tiles_n);
+        if (!t.any) return;
+        t.n0 = ((int)blockIdx.x % tiles_n) * 16;
+        if (t.e == g.experts) {
+            zero_rows(g, t, 16 * MT, 16);
+            return;
+        }
+    } else {
+        t.n0 = (int)blockIdx.x * 16;
+    }
+    const __amdgpu_buffer_rsrc_t rw = rows_rsrc<16>(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
+    const __amdgpu_buffer_rsrc_t rx = rows_rsrc<16 * MT>(g.X, g.ldx, t.m0, t.m_end);
+    const uint32_t woff = (uint32_t)r * g.ldw;
+    i32x4 acc[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
+    const int nkc = (g.K + 127) / 128;
+    for (int kb = wave; kb < nkc; kb += kSkinnyWaves * kSkinnyUnroll) {
+        i32x4 bw[kSkinnyUnroll][2], ax[kSkinnyUnroll][MT][2];
+#pragma unroll
+        for (int u = 0; u < kSkinnyUnroll; ++u) {
+            const int kc = kb + u * kSkinnyWaves;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = kc * 128 + 64 * h + 16 * kq;
+                const bool in = k < g.K;
+                bw[u][h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? woff + (uint32_t)k : kOob, 0, 0));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint32_t xo = (uint32_t)(mt * 16 + r) * g.ldx + (uint32_t)k;
+                    ax[u][mt][h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo : kOob, 0, 0));
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kSkinnyUnroll; ++u)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                    acc[mt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bw[u][h], ax[u][mt][h], acc[mt], 0, 0, 0);
+    }
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) *reinterpret_cast<i32x4*>(&red[wave][mt][4 * lane]) = acc[mt];
+    __syncthreads();
+    const bool vec = vec_out(g);
+    for (int p = threadIdx.x; p < MT * 64; p += 64 * kSkinnyWaves) {
+        const int mt = p >> 6, l = p & 63;
+        i32x4 v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < kSkinnyWaves; ++w) v += *reinterpret_cast<const i32x4*>(&red[w][mt][4 * l]);
+        const int m = t.m0 + mt * 16 + (l & 15);
+        finish4(g, t, m, t.n0 + 4 * (l >> 4), v, m < t.m_end ? g.sx[m] : 0.0f, vec);
+    }
+}
+
+// Tiles of BM rows that M rows split over the experts can need: every range adds at most one partly
+// filled tile (the rows behind the last expert's are a range of their own).
+int64_t row_tiles(const GemmI8Args& g, int bm) {
+    if (!g.experts) return ((int64_t)g.M + bm - 1) / bm;
+    const int64_t most = (int64_t)g.M / bm + g.experts + 1;
+    return most < g.M ? most : g.M;
+}
+
+template <int BM, int BN, int WGM, int WGN>
+hipError_t tiled_go(const GemmI8Args& g, hipStream_t stream) {
+    const int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
+    if (blocks * (64 * WGM * WGN) > kMaxThreads) return hipErrorInvalidValue;
+    if (g.experts)
+        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN), 0, stream, g);
+    else
+        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN), 0, stream, g);
+    return hipGetLastError();
+}
+
+template <int MT>
+hipError_t skinny_go(const GemmI8Args& g, hipStream_t stream) {
+    const int64_t blocks = row_tiles(g, 16 * MT) * (((int64_t)g.N + 15) / 16);
+    if (blocks * (64 * kSkinnyWaves) > kMaxThreads) return hipErrorInvalidValue;
+    if (g.experts)
+        hipLaunchKernelGGL((gemm_skinny_i8<MT, true>), dim3((unsigned)blocks), dim3(64 * kSkinnyWaves), 0, stream, g);
+    else
+        hipLaunchKernelGGL((gemm_skinny_i8<MT, false>), dim3((unsigned)blocks), dim3(64 * kSkinnyWaves), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows_i8(const void* X, int src, int M, int K, int64_t ldx, int8_t* Q, float* S,
+                                   hipStream_t stream) {
+    if (M <= 0) return hipSuccess;
+    switch (src) {
+        case EP_F32: return quantize_src<EP_F32>(X, M, K, ldx, Q, S, stream);
+        case EP_BF16: return quantize_src<EP_BF16>(X, M, K, ldx, Q, S, stream);
+        case EP_F16: return quantize_src<EP_F16>(X, M, K, ldx, Q, S, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* dst, int ld, hipStream_t stream) {
+    const int64_t chunks = rows * (ld / 16);
+    if (chunks <= 0) return hipSuccess;
+    if (chunks > kMaxThreads - 256) return hipErrorInvalidValue;
+    hipLaunchKernelGGL(pad_rows_i8, dim3((unsigned)((chunks + 255) / 256)), dim3(256), 0, stream, src, rows, K, dst, ld);
+    return hipGetLastError();
+}
+
+hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
+    if (g.M <= 0 || g.N <= 0) return hipSuccess;
+    // rows that meet one weight: all of them, or an expert's share
+    const int64_t per = g.experts ? ((int64_t)g.M + g.experts - 1) / g.experts : g.M;
+    if (per <= 16) return skinny_go<1>(g, stream);
+    if (per <= 32) return skinny_go<2>(g, stream);
+    if (per <= 64) return skinny_go<4>(g, stream);
+    auto tiles = [&](int bm, int bn) { return (((int64_t)g.M + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn); };
+    if (tiles(256, 256) >= device_cus()) return tiled_go<256, 256, 2, 4>(g, stream);
+    if (tiles(128, 128) >= 2L * device_cus()) return tiled_go<128, 128, 2, 2>(g, stream);
+    return tiled_go<64, 64, 2, 2>(g, stream);
+}
+
+}  // namespace ep

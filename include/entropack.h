@@ -332,6 +332,117 @@ ep_status ep_quantize_rows_fp8(const void* dev_x, int64_t M, int64_t K, uint8_t*
 ep_status ep_gemm_fp8(const uint8_t* dev_xq, const float* dev_xs, const uint8_t* dev_wq, const float* dev_ws,
                       int64_t M, int64_t N, int64_t K, const void* dev_bias, void* dev_y, void* hip_stream);
 
+/* INT8 row quantizer: per-row codes and fp32 scales of activation rows, the counterpart of the INT8
+ * weight container (codes and one scale per output channel).
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
+ * Abstract (INT8 among the containers the decode fills); the activation rule is this library's.
+ * a = max |x| over the row (raised to 2^-100 when smaller, unless zero), scale = fp32(a / 127), code =
+ * 127 x / a rounded to nearest, ties to even, decided exactly (-127 ... 127). A zero row gets scale 0
+ * and codes 0; a row holding an infinity or a NaN gets scale NaN and codes 0, so that products with it
+ * are NaN. dev_x: M rows of K elements of src (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise),
+ * rows ldx >= K elements apart, any alignment of the element; dev_q: [M][K] codes, dev_scale: [M] fp32.
+ * M and K below 2^31 (EP_ERANGE). Fastest with K % 8 == 0 and 16-byte aligned rows. Asynchronous on
+ * hip_stream; allocates nothing. */
+ep_status ep_quantize_rows_int8(const void* dev_x, ep_dtype src, int64_t M, int64_t K, int64_t ldx, int8_t* dev_q,
+                                float* dev_scale, void* hip_stream);
+
+/* INT8 GEMM with a scale per token and per channel: Y[m][n] = xs[m] ws[n] sum_k xq[m][k] wq[n][k]
+ * (+ bias[n]). The sum is formed in int32 and exact, so the result does not depend on its order; it is
+ * then multiplied by ws[n], by xs[m] and biased in fp32 and rounded once to the output type.
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
+ * Abstract (the INT8 container); "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory
+ * Checks", section "Replace one linear layer before a whole model".
+ * xq [M][K] and wq [N][K] int8 codes (16-byte aligned), xs [M] and ws [N] fp32, bias [N] bf16 or NULL, Y
+ * [M][N] elements of out (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise). Requires K % 16 == 0
+ * (EP_EINVAL; ep_pad_rows_int8 lays other rows out) and K <= 131071 (EP_ERANGE: longer sums could leave
+ * int32); M and N below 2^31 (EP_ERANGE). The library's own kernels; asynchronous on hip_stream;
+ * allocates nothing. */
+ep_status ep_gemm_int8(const int8_t* dev_xq, const float* dev_xs, const int8_t* dev_wq, const float* dev_ws, int64_t M,
+                       int64_t N, int64_t K, const void* dev_bias, ep_dtype out, void* dev_y, void* hip_stream);
+
+/* ep_gemm_int8 with a weight per expert: rows [offsets[e], offsets[e + 1]) of xq (ep_sort_tokens' order)
+ * are multiplied by expert e's weight, each row the same bits as ep_gemm_int8 with that weight.
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
+ * Abstract (the INT8 container). One launch for the experts of a layer is this library's scheduling,
+ * not a step of the method.
+ * xq [R][K], xs [R], wq [E][N][K], ws [E][N], offsets [E + 1] int32 in device memory, ascending, offsets[0]
+ * = 0, offsets[E] <= R (read by the kernels: nothing is copied to the host; offsets outside 0 ... R are
+ * clamped, so a wrong one gives wrong rows but no access out of bounds); bias [E][N] bf16 or NULL; Y
+ * [R][N] of out. Rows from offsets[E] on are set to zero. E in 1 ... 1024 (EP_ERANGE otherwise); other
+ * checks as ep_gemm_int8. Asynchronous on hip_stream; allocates nothing. */
+ep_status ep_gemm_int8_experts(const int8_t* dev_xq, const float* dev_xs, const int8_t* dev_wq, const float* dev_ws,
+                               const int32_t* dev_offsets, int E, int64_t R, int64_t N, int64_t K, const void* dev_bias,
+                               ep_dtype out, void* dev_y, void* hip_stream);
+
+/* Codes laid out for ep_gemm_int8: dst [rows][ld] = src [rows][K] (contiguous, any alignment) with zeros
+ * in columns K ... ld - 1, which add nothing to the sums. ld >= K, ld % 16 == 0 and dst 16-byte aligned
+ * (EP_EINVAL); K and ld below 2^31 (EP_ERANGE).
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
+ * Abstract (the INT8 container, whose rows may have any length). Asynchronous on hip_stream. */
+ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_t* dev_dst, int64_t ld, void* hip_stream);
+
+/* INT8 variant of ep_linear_forward: Y = diag(xs) Xq Wq^T diag(ws) (+ bias), BF16 output. The weight is
+ * decoded into the INT8 container with its per-row scales, slice by slice in the workspace as in
+ * ep_linear_forward, the activations are quantized per row as ep_quantize_rows_int8 does, and both meet
+ * in ep_gemm_int8's kernels.
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
+ * Abstract (decoding fused into the computation that uses the weight, the INT8 container); "EntroPack
+ * PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one linear layer
+ * before a whole model".
+ * dev_x: [M][K] bf16, 16-byte aligned (may be NULL when K == 0); dev_bias: [N] bf16 or NULL; dev_y: [M][N]
+ * bf16. K == 0 gives Y = bias (or zeros). Requires a lossy stream and K % 16 == 0 (EP_EINVAL), K <=
+ * 131071, M and N below 2^31 (EP_ERANGE). Workspace rules of ep_linear_forward. Asynchronous on
+ * hip_stream. */
+ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t M, const void* dev_bias, void* dev_y,
+                                 void* hip_stream);
+
+/* Tokens sorted by the experts they chose (the input order of ep_gemm_int8_experts, and of compressed
+ * layers run expert by expert).
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
+ * linear layer before a whole model" (compressed layers inside a model's forward). Routing rows to layers
+ * is this library's scheduling, not a step of the method.
+ *   ids: [T][k] expert numbers, int32 or int64 (id_bytes 4 or 8); a number outside 0 ... E - 1 marks a
+ *        dropped choice. The same expert twice in a token gives two rows.
+ *   x: T rows of H elements of dtype (any ep_dtype), rows ldx >= H elements apart.
+ *   rows: out [T k][H]: choices ordered by expert, within an expert by t k + j; rows of dropped choices,
+ *        behind the experts', are zero. NULL: offsets and pos only.
+ *   offsets: out [E + 1] int32: expert e has rows [offsets[e], offsets[e + 1]).
+ *   pos: out [T][k] int32: the row of choice (t, j), or -1 - row for a dropped one.
+ * scratch: ep_sort_tokens_scratch(T, k, E) bytes of device memory, 4-byte aligned (NULL when that is 0), read
+ * and written by this call's kernels only. E in 1 ... 1024, T k below 2^31 (EP_ERANGE). Same bits on every
+ * call. Asynchronous on hip_stream; allocates nothing, copies nothing to the host. */
+ep_status ep_sort_tokens(const void* dev_x, ep_dtype dtype, int64_t T, int64_t H, int64_t ldx, const void* dev_ids,
+                         int id_bytes, int k, int E, void* dev_rows, int32_t* dev_offsets, int32_t* dev_pos,
+                         void* dev_scratch, void* hip_stream);
+
+/* Bytes of device scratch ep_sort_tokens needs in *bytes. Source: "EntroPack PyTorch Guide: Lossless
+ * Weights, Bitrates and Memory Checks", section "Measure memory with clear boundaries" (temporary
+ * buffers of a call are part of its memory). */
+ep_status ep_sort_tokens_scratch(int64_t T, int k, int E, size_t* bytes);
+
+/* The experts' rows summed back per token: Y[t] = sum over j of w[t][j] ys[pos[t][j]], in the order of j,
+ * fp32 sums rounded once; dropped choices (negative positions) are left out, whatever their rows hold.
+ * With w NULL the weights are 1 (the gradient of ep_sort_tokens' rows).
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
+ * linear layer before a whole model" (compressed layers inside a model's forward). Routing rows to layers
+ * is this library's scheduling, not a step of the method.
+ *   ys: [R][H] of dtype (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise); pos: [T][k] int32 (a row
+ * of R or more is left out like a dropped one); w: [T][k] fp32 or NULL; y: [T][H] of dtype. Asynchronous on
+ * hip_stream. */
+ep_status ep_combine_tokens(const void* dev_ys, ep_dtype dtype, const int32_t* dev_pos, const float* dev_w, int64_t T,
+                            int k, int64_t H, int64_t R, void* dev_y, void* hip_stream);
+
+/* Gradients of ep_combine_tokens: d_ys [R][H] (dtype) gets w[t][j] dy[t] in row pos[t][j] and zeros in the
+ * rows of dropped choices; d_w [T][k] (fp32) = <dy[t], ys[pos[t][j]]>, 0 for a dropped choice, fp32 sums in a
+ * fixed order. d_ys or d_w may be NULL (not wanted); ys may be NULL when d_w is. The positions must be
+ * those of ep_sort_tokens for these T and k (every row named once), and R = T k (EP_EINVAL otherwise).
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
+ * linear layer before a whole model" (a compressed layer inside a model; its routing may be trained).
+ * Asynchronous on hip_stream. */
+ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32_t* dev_pos, const float* dev_w,
+                                 const void* dev_dy, int64_t T, int k, int64_t H, int64_t R, void* dev_d_ys,
+                                 float* dev_d_w, void* hip_stream);
+
 /* Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Test
  * saved artifacts and reloads before deployment" (a failed step must stop with a clear error);
  * reading R12 (every lane ends at its initial state: a free integrity check).

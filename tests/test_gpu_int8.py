@@ -1,0 +1,349 @@
+"""The INT8 products on the GPU: the row quantizer, the product with a scale per token and per channel,
+the same per expert, and the compressed linear layer's INT8 forward.
+
+References are computed in 64 bits. The quantizer must give the same codes and scales bit for bit: its
+rounding is decided exactly, and 127 x / a in fp64 can neither reach nor leave a rounding border (127 x
+is exact, and a quotient of two fp32 numbers that is not on a border is at least 2^-33 of itself away
+from it). The products' int32 sums are exact, so an output differs from the reference by fp32 steps
+only: the sum's conversion, two scale products and the bias, each at most 2^-24 relative, then the
+output type's rounding (half of finfo.eps)."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import decode_tile_interleaved_rans_amd as ep
+from decode_tile_interleaved_rans_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = [torch.bfloat16, torch.float16, torch.float32]
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def reference_codes(x):
+    x64 = x.double()
+    a = x64.abs().amax(1, keepdim=True)
+    a = torch.where(a > 0, a.clamp_min(2.0 ** -100), a)
+    q = torch.where(a > 0, 127.0 * x64 / torch.where(a > 0, a, 1.0), 0.0).round()
+    return q.to(torch.int8), (a[:, 0] / 127.0).float()
+
+
+def same_codes(x):
+    q, s = ep.quantize_rows_int8(x)
+    wq, ws = reference_codes(x)
+    assert q.dtype == torch.int8 and s.dtype == torch.float32
+    assert torch.equal(s, ws)
+    assert torch.equal(q, wq), f"{(q != wq).sum().item()} codes differ"
+    return q, s
+
+
+# ------------------------------------------------------------------------------------ quantizer
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,K", [(1, 1), (1, 8), (3, 17), (5, 64), (2, 513), (7, 1000), (4, 1024), (3, 1025), (2, 2048),
+                                 (9, 4096), (1, 8192), (2, 10240), (3, 16384), (2, 16392), (2, 20001), (300, 24)])
+def test_quantizer_codes(M, K, dtype):
+    g = gen(M * 1000 + K)
+    x = torch.randn((M, K), generator=g, device="cuda") * torch.exp(torch.randn((M, 1), generator=g, device="cuda"))
+    same_codes(x.to(dtype))
+
+
+@pytest.mark.parametrize("K", [24, 1027, 4096])
+def test_quantizer_at_rounding_borders(K):
+    # ties ((k + 1/2) a / 127 exactly) and the fp32 neighbours of every border, rows of differing maximum
+    rng = np.random.default_rng(K)
+    rows = []
+    for a in [127.0, 127.0 * 2 ** -30, 1.0, 3.0, 0.7, 1e30, 1e-20, 3.4e38]:
+        a = np.float32(a)
+        k = rng.integers(-127, 127, K)
+        x = ((k + 0.5) * (float(a) / 127.0)).astype(np.float32)
+        step = rng.integers(-2, 3, K)
+        for _ in range(2):
+            x = np.where(step > 0, np.nextafter(x, np.float32(np.inf)), np.where(step < 0, np.nextafter(x, np.float32(-np.inf)), x))
+            step = step - np.sign(step)
+        x[0] = a
+        rows.append(np.clip(x, -a, a))
+    x = torch.from_numpy(np.stack(rows).astype(np.float32)).cuda()
+    same_codes(x)
+    for t in (torch.bfloat16, torch.float16):
+        same_codes(x[:5].to(t))                               # the rows that fp16 can hold
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("K", [40, 1001, 4096])
+def test_quantizer_special_rows(K, dtype):
+    x = torch.randn((8, K), generator=gen(3), device="cuda").to(dtype)
+    tiny = torch.finfo(dtype).smallest_normal / 64 if dtype != torch.float32 else 2.0 ** -149
+    x[1] = 0
+    x[2, K // 2] = float("nan")
+    x[3, K - 1] = float("inf")
+    x[4, 0] = float("-inf")
+    x[5] = 0
+    x[5, 3] = tiny                                            # a subnormal row maximum
+    x[6] = -0.0
+    x[7, 1] = torch.finfo(dtype).max
+    q, s = ep.quantize_rows_int8(x)
+    fine = torch.tensor([0, 1, 5, 6, 7], device="cuda")
+    wq, ws = reference_codes(x[fine])
+    assert torch.equal(q[fine], wq) and torch.equal(s[fine], ws)
+    for r in (2, 3, 4):
+        assert torch.isnan(s[r]) and not q[r].any()
+    assert s[1] == 0 and s[6] == 0
+
+
+def test_quantizer_row_strides_and_offsets():
+    base = torch.randn((20, 3000), generator=gen(4), device="cuda").to(torch.bfloat16)
+    for x in (base[:, 8:1032], base[:, 3:1000], base[::2, :512], base[4:5, 1:9], base[:, :1]):
+        q, s = ep.quantize_rows_int8(x)
+        wq, ws = reference_codes(x)
+        assert torch.equal(q, wq) and torch.equal(s, ws)
+
+
+# ------------------------------------------------------------------------------------ product
+def operands(M, N, K, seed, full=False):
+    g = gen(seed)
+    lim = 128 if full else 127
+    xq = torch.randint(-lim, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-lim, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.exp(torch.randn(M, generator=g, device="cuda")) * 1e-3
+    ws = torch.exp(torch.randn(N, generator=g, device="cuda")) * 1e-3
+    b = torch.randn(N, generator=g, device="cuda").to(torch.bfloat16)
+    return xq, xs, wq, ws, b
+
+
+def product64(xq, wq):
+    return torch.mm(xq.double(), wq.double().t().contiguous())
+
+
+def check_product(y, acc, xs, ws, b):
+    v = acc * xs.double()[:, None] * ws.double()[None, :]
+    ref = v if b is None else v + b.double()
+    fp32 = 4 * U * (v.abs() + (0 if b is None else b.double().abs()))
+    half = torch.finfo(y.dtype).eps / 2
+    tiny = 2.0 ** -25 if y.dtype == torch.float16 else 2.0 ** -134       # half a subnormal step
+    tol = fp32 + half * (ref.abs() + fp32) + tiny
+    err = (y.double() - ref).abs()
+    assert (err <= tol).all(), f"largest excess {(err - tol).max().item():.3g} at {int((err - tol).argmax())}"
+
+
+SHAPES = [(1, 1, 16), (1, 17, 32), (2, 64, 128), (5, 100, 144), (16, 48, 1024), (17, 33, 4112), (31, 130, 256), (33, 20, 512),
+          (64, 257, 2048), (65, 63, 640), (100, 500, 96), (128, 128, 128), (200, 1000, 1040), (257, 300, 16), (130, 4100, 272),
+          (700, 1300, 400), (1030, 2050, 256), (4100, 4099, 144)]
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("M,N,K", SHAPES)
+def test_product(M, N, K, out):
+    xq, xs, wq, ws, b = operands(M, N, K, M + N + K)
+    acc = product64(xq, wq)
+    check_product(ep.gemm_int8(xq, xs, wq, ws, out_dtype=out), acc, xs, ws, None)
+    check_product(ep.gemm_int8(xq, xs, wq, ws, b, out_dtype=out), acc, xs, ws, b)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 5, 1), (3, 70, 15), (40, 33, 17), (90, 65, 127), (300, 401, 1001)])
+def test_product_of_any_width(M, N, K):
+    xq, xs, wq, ws, b = operands(M, N, K, K)
+    check_product(ep.gemm_int8(xq, xs, wq, ws, b), product64(xq, wq), xs, ws, b)
+    # codes laid out once by the program give the same bits
+    xp, wp = ep.pad_rows_int8(xq), ep.pad_rows_int8(wq)
+    assert xp.shape[1] % 16 == 0 and torch.equal(xp[:, :K], xq) and not xp[:, K:].any()
+    assert torch.equal(ep.gemm_int8(xp, xs, wp, ws, b), ep.gemm_int8(xq, xs, wq, ws, b))
+
+
+def test_product_misaligned_codes():
+    xq, xs, wq, ws, b = operands(50, 70, 256, 7)
+    flat = torch.zeros(50 * 256 + 3, dtype=torch.int8, device="cuda")
+    off = flat[3:].view(50, 256)
+    off.copy_(xq)
+    assert torch.equal(ep.gemm_int8(off, xs, wq, ws, b), ep.gemm_int8(xq, xs, wq, ws, b))
+
+
+@pytest.mark.parametrize("M", [1, 40, 300])
+def test_longest_sum_does_not_overflow(M):
+    # every product 2^14: the largest sum an int8 row of 131056 codes can reach, and its negative
+    K = 131056
+    xq = torch.full((M, K), -128, dtype=torch.int8, device="cuda")
+    wq = torch.full((20, K), -128, dtype=torch.int8, device="cuda")
+    wq[1] = 127
+    xs, ws = torch.ones(M, device="cuda"), torch.ones(20, device="cuda")
+    y = ep.gemm_int8(xq, xs, wq, ws, out_dtype=torch.float32)
+    assert (y[:, 0] == float(np.float32(K * 16384))).all() and (y[:, 1] == float(np.float32(-K * 128 * 127))).all()
+
+
+@pytest.mark.parametrize("M", [1, 20, 70, 300])
+def test_empty_sum_and_empty_sides(M):
+    xq, xs, wq, ws, b = operands(M, 40, 16, 1)
+    e = torch.empty
+    y = ep.gemm_int8(e((M, 0), dtype=torch.int8, device="cuda"), xs, e((40, 0), dtype=torch.int8, device="cuda"), ws, b)
+    assert torch.equal(y, b.expand(M, 40))
+    assert ep.gemm_int8(xq[:0], xs[:0], wq, ws).shape == (0, 40)
+    assert ep.gemm_int8(xq, xs, wq[:0], ws[:0]).shape == (M, 0)
+
+
+def test_bad_rows_stay_bad():
+    # a row with a NaN has scale NaN: its outputs are NaN and no other row's are
+    x = torch.randn((70, 128), generator=gen(6), device="cuda").to(torch.bfloat16)
+    x[13, 5] = float("nan")
+    x[44, 0] = float("inf")
+    _, _, wq, ws, _ = operands(1, 90, 128, 8)
+    q, s = ep.quantize_rows_int8(x)
+    y = ep.gemm_int8(q, s, wq, ws)
+    nan = torch.isnan(y)
+    assert nan[13].all() and nan[44].all() and int(nan.sum()) == 180
+
+
+def test_rows_do_not_depend_on_their_batch():
+    # exact sums: a row's outputs are the same bits whatever the other rows and the kernel chosen
+    xq, xs, wq, ws, b = operands(4200, 1100, 528, 12)
+    y = ep.gemm_int8(xq, xs, wq, ws, b)
+    for M in (1, 16, 20, 64, 65, 300, 1500):
+        assert torch.equal(ep.gemm_int8(xq[:M], xs[:M], wq, ws, b), y[:M]), M
+
+
+# ------------------------------------------------------------------------------------ experts
+def expert_case(counts, N, K, R, seed):
+    E = len(counts)
+    g = gen(seed)
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    xq = torch.randint(-127, 128, (R, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (E, N, K), generator=g, device="cuda", dtype=torch.int8)
+    xs = torch.exp(torch.randn(R, generator=g, device="cuda")) * 1e-3
+    ws = torch.exp(torch.randn((E, N), generator=g, device="cuda")) * 1e-3
+    b = torch.randn((E, N), generator=g, device="cuda").to(torch.bfloat16)
+    return off, xq, xs, wq, ws, b
+
+
+COUNTS = [[1], [0], [0, 3, 0], [16, 17, 1, 0, 64], [5] * 100, [0] * 70 + [9] + [0] * 200, [300, 0, 1, 129], [1000, 7, 513, 64],
+          [2500, 2600], [40] * 60]
+
+
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}x{sum(c)}")
+@pytest.mark.parametrize("N,K", [(100, 144), (520, 512)])
+def test_experts(counts, N, K, out):
+    R = sum(counts) + 21                                      # rows behind the last expert's
+    off, xq, xs, wq, ws, b = expert_case(counts, N, K, R, sum(counts) + N)
+    for bias in (None, b):
+        y = ep.gemm_int8_experts(xq, xs, wq, ws, off, bias, out_dtype=out)
+        assert not y[sum(counts):].any()
+        a = 0
+        for e, c in enumerate(counts):
+            if c:
+                check_product(y[a:a + c], product64(xq[a:a + c], wq[e]), xs[a:a + c], ws[e], None if bias is None else b[e])
+                assert torch.equal(y[a:a + c], ep.gemm_int8(xq[a:a + c], xs[a:a + c], wq[e], ws[e],
+                                                            None if bias is None else b[e], out_dtype=out))
+            a += c
+
+
+def test_experts_any_width_and_no_rows():
+    off, xq, xs, wq, ws, b = expert_case([3, 0, 40], 33, 75, 43, 5)
+    y = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)
+    check_product(y[:3], product64(xq[:3], wq[0]), xs[:3], ws[0], b[0])
+    check_product(y[3:], product64(xq[3:], wq[2]), xs[3:], ws[2], b[2])
+    assert ep.gemm_int8_experts(xq[:0], xs[:0], wq, ws, torch.zeros_like(off), b).shape == (0, 33)
+
+
+def test_experts_wrong_offsets_stay_inside():
+    # offsets out of range or order give wrong rows, never an access outside: rows that are written
+    # belong to the result and everything around it keeps its values
+    off, xq, xs, wq, ws, b = expert_case([8, 8, 8], 64, 128, 24, 9)
+    for bad in ([0, 100, 5, 24], [0, -7, 12, 9], [0, 24, 24, 2 ** 31 - 1], [-2 ** 31, 0, 0, 0]):
+        o = torch.tensor(bad, dtype=torch.int64, device="cuda").to(torch.int32)
+        assert ep.gemm_int8_experts(xq, xs, wq, ws, o, b).shape == (24, 64)
+    torch.cuda.synchronize()
+
+
+def test_experts_take_new_offsets_in_a_captured_graph():
+    off, xq, xs, wq, ws, b = expert_case([10, 0, 30, 8], 200, 256, 64, 15)
+    y = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)           # warm up
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)
+    for counts in ([10, 0, 30, 8], [0, 0, 0, 0], [64, 0, 0, 0], [1, 1, 1, 61], [16, 16, 16, 16]):
+        off.copy_(torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32))
+        xq.copy_(torch.roll(xq, 1, 0))
+        graph.replay()
+        want = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)    # eager work between replays
+        torch.cuda.synchronize()
+        assert torch.equal(y, want), counts
+
+
+def test_large_result_offsets():
+    # more than 2^31 bytes and more than 2^31 / 2 elements of output: 64-bit addresses in the epilogue
+    M, N, K = 70000, 32768, 16
+    xq, xs, wq, ws, _ = operands(M, N, K, 3)
+    y = ep.gemm_int8(xq, xs, wq, ws)
+    for r in (0, 32768, 65535, M - 100):
+        check_product(y[r:r + 100], product64(xq[r:r + 100], wq), xs[r:r + 100], ws, None)
+    del y
+
+
+def test_other_stream():
+    xq, xs, wq, ws, b = operands(300, 400, 512, 31)
+    x = torch.randn((300, 512), generator=gen(32), device="cuda").to(torch.bfloat16)
+    want_y, (want_q, want_s) = ep.gemm_int8(xq, xs, wq, ws, b), ep.quantize_rows_int8(x)
+    s = torch.cuda.Stream()
+    for _ in range(3):
+        big = torch.randn((4096, 4096), device="cuda")
+        big = big @ big                                        # keeps the current stream busy
+        x2 = x + 0                                             # made on it
+        y = ep.gemm_int8(xq + 0, xs, wq, ws, b, stream=s)
+        q, sc = ep.quantize_rows_int8(x2, stream=s)
+        del x2
+        s.synchronize()
+        assert torch.equal(y, want_y) and torch.equal(q, want_q) and torch.equal(sc, want_s)
+
+
+# ------------------------------------------------------------------------------------ compressed layer
+@pytest.mark.parametrize("layout", [0, ep.ROW_LAYOUT])
+@pytest.mark.parametrize("M", [1, 16, 33, 64, 65, 300])
+def test_compressed_forward(M, layout):
+    N, K = 300, 1040
+    s, _ = ep.compress(W.student_t(N, K, 5), 4.5, dtype=ep.BF16, layout=layout, prob_bits=11)
+    bias = torch.randn(N, generator=gen(5), device="cuda").to(torch.bfloat16)
+    layer = ep.CompressedLinear(s, bias, compute="int8")
+    xb = W.activations(M, K, 6)
+    x = torch.from_numpy(xb.view(np.int16)).view(torch.bfloat16).cuda()
+    y = layer(x)
+    layer.handle.check()
+    cq, cs = oracle.decompress(s, oracle.I8)
+    xq, xs = reference_codes(x)
+    wq, ws = torch.from_numpy(cq.view(np.int8)).cuda(), torch.from_numpy(cs).cuda()   # the oracle returns bytes
+    check_product(y, product64(xq, wq), xs, ws, bias)
+    # the same bits as the parts called one by one
+    dq, ds = layer.handle.decompress(torch.int8)
+    assert torch.equal(dq, wq) and torch.equal(ds, ws)
+    assert torch.equal(y, ep.gemm_int8(*ep.quantize_rows_int8(x), dq, ds, bias))
+    assert torch.equal(ep.linear_forward_many([layer, layer], x)[1], y)
+
+
+def test_compressed_forward_on_two_slices():
+    # a weight of more than one 128 MiB slice, 128 MiB / K rows each
+    N, K, M = 9000, 16384, 70
+    w = W.gpu_student_t(N, K, 3)
+    s, _ = ep.compress_device(w, 3.0, layout=ep.ROW_LAYOUT, prob_bits=11)
+    layer = ep.CompressedLinear(s, compute="int8")
+    x = torch.randn((M, K), generator=gen(8), device="cuda").to(torch.bfloat16)
+    dq, ds = layer.handle.decompress(torch.int8)
+    assert torch.equal(layer(x), ep.gemm_int8(*ep.quantize_rows_int8(x), dq, ds))
+
+
+def test_c_abi_refusals_reach_python():
+    L = ep.lib()
+    x = torch.zeros((4, 32), dtype=torch.int8, device="cuda")
+    f = torch.zeros(4, device="cuda")
+    y = torch.zeros((4, 4), device="cuda")
+    p = lambda t, o=0: C.c_void_p(t.data_ptr() + o)
+    st = C.c_void_p(0)
+    assert L.ep_gemm_int8(p(x), p(f), p(x, 4), p(f), 4, 3, 16, None, ep.F32, p(y), st) == -1     # W misaligned
+    assert L.ep_gemm_int8(p(x), p(f), p(x), p(f), 4, 4, 32, None, ep.F32, p(y, 2), st) == -1     # Y misaligned
+    assert L.ep_quantize_rows_int8(p(f, 2), ep.F32, 1, 1, 1, p(x), p(f), st) == -1

@@ -459,8 +459,24 @@ def _need_rows(t, name: str, dtypes):
     return rows, cols, apart
 
 
+def _on_stream(stream, call, *tensors):
+    """call() with `stream` current, ordered as _run_on and _used_on order it. The calls below run on
+    the current stream without a stream object or context of their own, which would cost a small
+    call more time (9 us) than its kernel takes."""
+    s, other = _run_on(stream)
+    _used_on(s, other, *tensors)
+    with _torch().cuda.stream(s):
+        return call()
+
+
+def _current_raw():
+    """The current stream of the current device, as the C ABI takes it."""
+    torch = _torch()
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+
+
 def _ptr(t):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _float_types():
@@ -473,15 +489,14 @@ def quantize_rows_int8(x, stream=None):
     fp32 scales: scale = max |x| / 127, codes = x / scale rounded to nearest even, exactly. A row with an
     infinity or a NaN gets codes 0 and scale NaN. On `stream` (default: the current stream; another
     stream first waits for the current one)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: quantize_rows_int8(x), x)
     torch = _torch()
     M, K, ldx = _need_rows(x, "x", _float_types())
-    s, other = _run_on(stream)
-    with torch.cuda.stream(s):
-        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
-        sc = torch.empty(M, dtype=torch.float32, device=x.device)
-    _check(lib().ep_quantize_rows_int8(_ptr(x), _dtype_code(x.dtype), M, K, ldx, _ptr(q), _ptr(sc),
-                                       C.c_void_p(s.cuda_stream)), "ep_quantize_rows_int8")
-    _used_on(s, other, x)
+    q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+    sc = torch.empty(M, dtype=torch.float32, device=x.device)
+    _check(lib().ep_quantize_rows_int8(_ptr(x), _dtype_code(x.dtype), M, K, ldx, _ptr(q), _ptr(sc), _current_raw()),
+           "ep_quantize_rows_int8")
     return q, sc
 
 
@@ -489,19 +504,20 @@ def pad_rows_int8(codes, stream=None):
     """INT8 codes [..., K] in new memory with K rounded up to a multiple of 16, zeros behind: the layout
     the INT8 products read. They call this for codes that lack it; a program with such a weight lays
     it out once and keeps it (and pads the activations' codes to the same width)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: pad_rows_int8(codes), codes)
     torch = _torch()
     _need(codes, "codes", torch.int8)
+    if codes.dim() < 1:
+        raise ValueError("codes must have rows")
     K = codes.shape[-1]
-    rows, ld = codes[..., 0].numel() if K else 0, (K + 15) // 16 * 16
-    s, other = _run_on(stream)
-    with torch.cuda.stream(s):
-        out = torch.empty((*codes.shape[:-1], ld), dtype=torch.int8, device=codes.device)
-    _check(lib().ep_pad_rows_int8(_ptr(codes), rows, K, _ptr(out), ld, C.c_void_p(s.cuda_stream)), "ep_pad_rows_int8")
-    _used_on(s, other, codes)
+    rows, ld = codes.numel() // K if K else 0, (K + 15) // 16 * 16
+    out = torch.empty((*codes.shape[:-1], ld), dtype=torch.int8, device=codes.device)
+    _check(lib().ep_pad_rows_int8(_ptr(codes), rows, K, _ptr(out), ld, _current_raw()), "ep_pad_rows_int8")
     return out
 
 
-def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype, stream):
+def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype):
     torch = _torch()
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in _float_types():
@@ -518,19 +534,16 @@ def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype, stream):
         _need(bias, "bias", torch.bfloat16, shape=lead)
     if offsets is not None:
         _need(offsets, "offsets", torch.int32, shape=(lead[0] + 1,))
-    s, other = _run_on(stream)
-    _used_on(s, other, xq, xs, wq, ws, bias, offsets)
-    with torch.cuda.stream(s):
-        if K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16:
-            xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
-        y = torch.empty((M, lead[-1]), dtype=out_dtype, device=xq.device)
-        tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), C.c_void_p(s.cuda_stream))
-        if offsets is None:
-            _check(lib().ep_gemm_int8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, lead[-1], xq.shape[1], *tail),
-                   "ep_gemm_int8")
-        else:
-            _check(lib().ep_gemm_int8_experts(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), lead[0], M,
-                                              lead[-1], xq.shape[1], *tail), "ep_gemm_int8_experts")
+    if K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16:
+        xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
+        K = xq.shape[1]
+    y = torch.empty((M, lead[-1]), dtype=out_dtype, device=xq.device)
+    tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), _current_raw())
+    if offsets is None:
+        _check(lib().ep_gemm_int8(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, lead[-1], K, *tail), "ep_gemm_int8")
+    else:
+        _check(lib().ep_gemm_int8_experts(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), lead[0], M, lead[-1], K,
+                                          *tail), "ep_gemm_int8_experts")
     return y
 
 
@@ -540,7 +553,9 @@ def gemm_int8(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
     Handle.decompress(torch.int8)); exact int32 sums, output BF16 (default), FP16 or FP32. K a multiple
     of 16 and 16-byte aligned codes are read in place, others are laid out first (pad_rows_int8). On
     `stream` (default: the current stream; another stream first waits for the current one)."""
-    return _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype, stream)
+    if stream is not None:
+        return _on_stream(stream, lambda: _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype), xq, xs, wq, ws, bias)
+    return _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype)
 
 
 def gemm_int8_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream=None):
@@ -548,33 +563,36 @@ def gemm_int8_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream
     [R, K] meet wq[e] ([experts, N, K], scales ws and bias [experts, N]); rows behind the last expert's
     come out zero. offsets: int32 on the GPU, as sort_tokens gives them (ascending from 0, at most R;
     they are not read on the host)."""
-    return _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype, stream)
+    if stream is not None:
+        return _on_stream(stream, lambda: _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype),
+                          xq, xs, wq, ws, offsets, bias)
+    return _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype)
 
 
 # ------------------------------------------------------------------------------------ expert routing
-def _sort_raw(x, ids, n_experts, s):
+def _sort_raw(x, ids, n_experts):
     torch = _torch()
     T, k = ids.shape
-    _, H, ldx = _need_rows(x, "x", tuple(_torch_dtype(c) for c in (F32, BF16, F16, F8E4M3, I8, U8)))
+    _, H, ldx = _need_rows(x, "x", (torch.bfloat16, torch.float16, torch.float32, torch.int8, torch.uint8,
+                                    torch.float8_e4m3fn))
     need = C.c_size_t()
     _check(lib().ep_sort_tokens_scratch(T, k, n_experts, C.byref(need)), "ep_sort_tokens")
-    rows = torch.empty((T * k, H), dtype=x.dtype, device=x.device)
-    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=x.device)
-    pos = torch.empty((T, k), dtype=torch.int32, device=x.device)
-    scratch = torch.empty(need.value, dtype=torch.uint8, device=x.device) if need.value else None
+    dev = x.device
+    rows = torch.empty((T * k, H), dtype=x.dtype, device=dev)
+    offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=dev)
+    pos = torch.empty((T, k), dtype=torch.int32, device=dev)
+    scratch = torch.empty(need.value, dtype=torch.uint8, device=dev) if need.value else None
     _check(lib().ep_sort_tokens(_ptr(x), _dtype_code(x.dtype), T, H, ldx, _ptr(ids), ids.element_size(), k, n_experts,
-                                _ptr(rows), _ptr(offsets), _ptr(pos), _ptr(scratch), C.c_void_p(s.cuda_stream)),
-           "ep_sort_tokens")
+                                _ptr(rows), _ptr(offsets), _ptr(pos), _ptr(scratch), _current_raw()), "ep_sort_tokens")
     return rows, offsets, pos
 
 
-def _combine_raw(ys, pos, weights, s):
-    torch = _torch()
+def _combine_raw(ys, pos, weights):
     T, k = pos.shape
     R, H = ys.shape
-    y = torch.empty((T, H), dtype=ys.dtype, device=ys.device)
+    y = _torch().empty((T, H), dtype=ys.dtype, device=ys.device)
     _check(lib().ep_combine_tokens(_ptr(ys), _dtype_code(ys.dtype), _ptr(pos), _ptr(weights), T, k, H, R, _ptr(y),
-                                   C.c_void_p(s.cuda_stream)), "ep_combine_tokens")
+                                   _current_raw()), "ep_combine_tokens")
     return y
 
 
@@ -591,18 +609,16 @@ def _routing_functions():
 
         class SortTokens(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, ids, n_experts):
-                rows, offsets, pos = _sort_raw(x, ids, n_experts, torch.cuda.current_stream())
+            def forward(ctx, x, rows, pos):
                 ctx.save_for_backward(pos)
-                ctx.mark_non_differentiable(offsets, pos)
-                return rows, offsets, pos
+                return rows.view_as(rows)
 
             @staticmethod
             @once
-            def backward(ctx, d_rows, *_):
+            def backward(ctx, d_rows):
                 # a token's gradient is the sum of its rows'; dropped choices have no part in it
                 (pos,) = ctx.saved_tensors
-                return _combine_raw(d_rows.contiguous(), pos, None, torch.cuda.current_stream()), None, None
+                return _combine_raw(d_rows.contiguous(), pos, None), None, None
 
         class CombineTokens(torch.autograd.Function):
             @staticmethod
@@ -610,7 +626,7 @@ def _routing_functions():
                 want_w = weights is not None and ctx.needs_input_grad[2]
                 ctx.save_for_backward(ys if want_w else None, pos, weights)
                 ctx.rows = ys.shape[0]
-                return _combine_raw(ys, pos, weights, torch.cuda.current_stream())
+                return _combine_raw(ys, pos, weights)
 
             @staticmethod
             @once
@@ -622,8 +638,7 @@ def _routing_functions():
                 d_ys = torch.empty((ctx.rows, H), dtype=dy.dtype, device=dy.device) if ctx.needs_input_grad[0] else None
                 d_w = torch.empty((T, k), dtype=torch.float32, device=dy.device) if ys is not None else None
                 _check(lib().ep_combine_tokens_grad(_ptr(ys), _dtype_code(dy.dtype), _ptr(pos), _ptr(weights), _ptr(dy),
-                                                    T, k, H, ctx.rows, _ptr(d_ys), _ptr(d_w),
-                                                    C.c_void_p(torch.cuda.current_stream().cuda_stream)),
+                                                    T, k, H, ctx.rows, _ptr(d_ys), _ptr(d_w), _current_raw()),
                        "ep_combine_tokens_grad")
                 return d_ys, None, d_w
 
@@ -639,19 +654,17 @@ def sort_tokens(x, expert_ids, n_experts: int, stream=None):
     pos[t, j] = -1 - row of a zero row behind the last expert's. Differentiable in x; the host waits for
     nothing. On `stream` (default: the current stream; another stream first waits for the current one)."""
     torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: sort_tokens(x, expert_ids, n_experts), x, expert_ids)
     if expert_ids.dim() != 2 or expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be an int32 or int64 tensor of shape [tokens, choices]")
     _need(expert_ids, "expert_ids", expert_ids.dtype)
     if x.dim() != 2 or x.shape[0] != expert_ids.shape[0]:
         raise ValueError(f"x must have shape [{expert_ids.shape[0]}, H], got {tuple(x.shape)}")
-    s, other = _run_on(stream)
-    with torch.cuda.stream(s):
-        if torch.is_grad_enabled() and x.requires_grad:
-            out = _routing_functions()[0].apply(x, expert_ids, int(n_experts))
-        else:
-            out = _sort_raw(x, expert_ids, int(n_experts), s)
-    _used_on(s, other, x, expert_ids)
-    return out
+    rows, offsets, pos = _sort_raw(x, expert_ids, n_experts)
+    if x.requires_grad and torch.is_grad_enabled():
+        rows = _routing_functions()[0].apply(x, rows, pos)
+    return rows, offsets, pos
 
 
 def combine_tokens(ys, pos, weights=None, stream=None):
@@ -661,6 +674,8 @@ def combine_tokens(ys, pos, weights=None, stream=None):
     positions [T, k], weights: fp32 [T, k]. Differentiable in ys and weights. On `stream` (default: the
     current stream; another stream first waits for the current one)."""
     torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: combine_tokens(ys, pos, weights), ys, pos, weights)
     if ys.dim() != 2 or ys.dtype not in _float_types():
         raise ValueError(f"ys must be a bfloat16, float16 or float32 matrix, got {ys.dtype} of shape {tuple(ys.shape)}")
     _need(ys, "ys", ys.dtype)
@@ -668,18 +683,12 @@ def combine_tokens(ys, pos, weights=None, stream=None):
         raise ValueError("pos must have shape [tokens, choices]")
     _need(pos, "pos", torch.int32)
     if weights is not None:
-        _need(weights, "weights", torch.float32, shape=tuple(pos.shape))
-    grad = torch.is_grad_enabled() and (ys.requires_grad or (weights is not None and weights.requires_grad))
-    if grad and ys.shape[0] != pos.numel():
-        raise ValueError(f"the gradient takes one row per choice: ys has {ys.shape[0]} rows for {pos.numel()} choices")
-    s, other = _run_on(stream)
-    with torch.cuda.stream(s):
-        if grad:
-            y = _routing_functions()[1].apply(ys, pos, weights)
-        else:
-            y = _combine_raw(ys, pos, weights, s)
-    _used_on(s, other, ys, pos, weights)
-    return y
+        _need(weights, "weights", torch.float32, shape=pos.shape)
+    if torch.is_grad_enabled() and (ys.requires_grad or (weights is not None and weights.requires_grad)):
+        if ys.shape[0] != pos.numel():
+            raise ValueError(f"the gradient takes one row per choice: ys has {ys.shape[0]} rows for {pos.numel()} choices")
+        return _routing_functions()[1].apply(ys, pos, weights)
+    return _combine_raw(ys, pos, weights)
 
 
 class CompressedLinear:

@@ -289,41 +289,77 @@ __device__ __forceinline__ TileAt expert_tile(const GemmI8Args& g, int tm) {
     return t;
 }
 
-// Four consecutive outputs of a row (columns n .. n + 3 of n_end), converted and stored; `vec` when
-// rows of Y are aligned to four elements.
-template <typename F>
-__device__ __forceinline__ void store_out(void* Y, int out, int64_t at, const float* v, int count, bool vec, F) {
-    if (out == EP_F32) {
-        float* y = static_cast<float*>(Y) + at;
-        if (vec && count == 4) *reinterpret_cast<f32x4*>(y) = f32x4{v[0], v[1], v[2], v[3]};
-        else
-            for (int i = 0; i < count; ++i) y[i] = v[i];
-        return;
-    }
-    uint16_t h[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = out == EP_BF16 ? to_bf16(v[i]) : to_f16(v[i]);
-    uint16_t* y = static_cast<uint16_t*>(Y) + at;
-    if (vec && count == 4)
-        *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
-    else
-        for (int i = 0; i < count; ++i) y[i] = h[i];
-}
-
-// The epilogue of one 16 x 16 part: the lane's four sums of output row m, columns n .. n + 3.
-__device__ __forceinline__ void finish4(const GemmI8Args& g, const TileAt& t, int m, int n, i32x4 acc, float sx, bool vec) {
-    if (m >= t.m_end || n >= g.N) return;
-    const int count = g.N - n < 4 ? g.N - n : 4;
-    const float* sw = g.sw + (int64_t)t.e * g.N + n;
-    const uint16_t* bias = g.bias ? g.bias + (int64_t)t.e * g.N + n : nullptr;
+// The output of four sums of one row (columns n .. n + count - 1 of a lane), scaled, biased, rounded once
+// and stored; `vec` when rows of Y are aligned to four elements.
+template <int OUT>
+__device__ __forceinline__ void store4(void* Y, int64_t at, i32x4 acc, const float* sw, float sx, const float* bias, int count,
+                                       bool vec) {
     float v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int j = i < count ? i : 0;
-        v[i] = (float)acc[i] * sw[j] * sx;
-        if (bias) v[i] += __uint_as_float((uint32_t)bias[j] << 16);
+        v[i] = (float)acc[i] * sw[i] * sx;
+        if (bias) v[i] += bias[i];
     }
-    store_out(g.Y, g.out, (int64_t)m * g.ldy + n, v, count, vec, 0);
+    if constexpr (OUT == EP_F32) {
+        float* y = static_cast<float*>(Y) + at;
+        if (vec && count == 4) *reinterpret_cast<f32x4*>(y) = f32x4{v[0], v[1], v[2], v[3]};
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) y[i] = v[i];
+    } else {
+        uint16_t h[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = OUT == EP_BF16 ? to_bf16(v[i]) : to_f16(v[i]);
+        uint16_t* y = static_cast<uint16_t*>(Y) + at;
+        if (vec && count == 4)
+            *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | (uint32_t)h[1] << 16, h[2] | (uint32_t)h[3] << 16);
+        else
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) y[i] = h[i];
+    }
+}
+
+// Scales and biases of a lane's four columns from n on (count of them inside the matrix).
+__device__ __forceinline__ void load_columns(const GemmI8Args& g, int e, int n, int count, float* sw, float* bias) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t c = (int64_t)e * g.N + n + i;
+        sw[i] = i < count ? g.sw[c] : 0.0f;
+        if (g.bias) bias[i] = i < count ? __uint_as_float((uint32_t)g.bias[c] << 16) : 0.0f;
+    }
+}
+
+// The epilogue of a wave's TI x TJ parts of 16 x 16: rows m0 + 16 i + lane % 16, columns n0 + 16 j + 4 (lane / 16).
+template <int OUT, int TI, int TJ>
+__device__ __forceinline__ void store_tile(const GemmI8Args& g, const TileAt& t, int m0, int n0, const i32x4 (&acc)[TI][TJ],
+                                           bool vec) {
+    const int lane = threadIdx.x & 63;
+    float sx[TI];
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const int m = m0 + 16 * i + (lane & 15);
+        sx[i] = m < t.m_end ? g.sx[m] : 0.0f;
+    }
+    float sw[TJ][4], bias[TJ][4];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+        const int n = n0 + 16 * j + 4 * (lane >> 4);
+        load_columns(g, t.e, n, g.N - n < 4 ? g.N - n : 4, sw[j], bias[j]);
+    }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const int m = m0 + 16 * i + (lane & 15);
+        if (m >= t.m_end) continue;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const int n = n0 + 16 * j + 4 * (lane >> 4);
+            if (n >= g.N) continue;
+            store4<OUT>(g.Y, (int64_t)m * g.ldy + n, acc[i][j], sw[j], sx[i], g.bias ? bias[j] : nullptr,
+                        g.N - n < 4 ? g.N - n : 4, vec);
+        }
+    }
 }
 
 __device__ __forceinline__ void zero_rows(const GemmI8Args& g, const TileAt& t, int bm, int bn) {
@@ -352,21 +388,69 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 // ------------------------------------------------------------------------------- tiled product
 // A block of WGM x WGN waves owns a BM x BN tile of Y and walks K in steps of 128 codes. Both operand
 // tiles go straight from global memory into LDS (buffer_load ... lds, 16 bytes per lane, 8 rows of
-// 128 bytes per instruction), two stages: the loads of step k + 1 run while step k multiplies. The
-// eight 16-byte chunks of a row are swizzled: chunk c of row r sits at slot c ^ ((r / 2) % 8), so that
-// the 16 lanes of a fragment read (16 consecutive rows, one chunk) cover all banks.
+// 128 bytes per instruction), two stages. The eight 16-byte chunks of a row are swizzled: chunk c of
+// row r sits at slot c ^ ((r / 2) % 8), so that the 16 lanes of a fragment read (16 consecutive rows,
+// one chunk) cover all banks.
+//
+// A step has two halves of 64 codes with a fragment set each. While the MFMAs of one half run, the
+// wave reads the other set: the second half's behind the first half's MFMAs, the next step's first
+// half behind the second half's. So no MFMA waits for LDS, and the one barrier of a step sits between
+// the halves: by then every wave has read all of this stage (it may be overwritten: the loads of step
+// k + 2 start there) and the loads of step k + 1, in flight for a whole step, have landed.
 __device__ __forceinline__ int chunk_swizzle(int r) { return (r >> 1) & 7; }
 
+// One operand tile of ROWS rows: the lane's byte offset in its first row group, and the loads of step k0.
+// The row groups of a wave are 8 NW rows apart, so the swizzle (period 16 rows) is that of the first one.
 template <int ROWS, int NW>
-__device__ __forceinline__ void dma_rows(__amdgpu_buffer_rsrc_t rs, int ld, int k0, int K, uint8_t* lds) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int rr = lane >> 3;
+struct Dma {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t row_off;           // of the wave's first row group
+    int chunk;                  // K chunk that the lane's slot holds
+    uint32_t group_step;        // bytes between the wave's row groups
+    __device__ __forceinline__ void init(const int8_t* src, int ld, int64_t r0, int64_t r_end) {
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+        const int r = 8 * wave + (lane >> 3);
+        rs = rows_rsrc<ROWS>(src, ld, r0, r_end);
+        row_off = (uint32_t)(r * ld);
+        chunk = 16 * ((lane & 7) ^ chunk_swizzle(r));
+        group_step = (uint32_t)(8 * NW * ld);
+    }
+    __device__ __forceinline__ void load(int k0, int K, uint8_t* lds) const {
+        static_assert(NW % 2 == 0, "the swizzle repeats every two row groups");
+        const int wave = threadIdx.x >> 6, k = k0 + chunk;
+        const uint32_t at = row_off + ((uint32_t)k | ((uint32_t)((K - 1 - k) >> 31) & kOob));   // past K reads zero
 #pragma unroll
-    for (int j = 0; j < ROWS / 8 / NW; ++j) {
-        const int g = wave + NW * j;
-        const int k = k0 + 16 * ((lane & 7) ^ chunk_swizzle(8 * g + rr));
-        const uint32_t off = (uint32_t)((8 * g + rr) * ld + k) | ((uint32_t)((K - 1 - k) >> 31) & kOob);
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + 1024 * g), 16, off, 0, 0, 0);
+        for (int j = 0; j < ROWS / 8 / NW; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + 1024 * (wave + NW * j)), 16, at + j * group_step, 0, 0, 0);
+    }
+};
+
+// Fragments of T 16-row parts from row r0 of an operand tile, K half h (64 codes) of a stage.
+template <int T>
+__device__ __forceinline__ void read_frags(const uint8_t* tile, int r0, int h, i32x4 (&f)[T]) {
+    const int lane = threadIdx.x & 63, r = r0 + (lane & 15);
+    const uint8_t* p = tile + r * 128 + (((4 * h + (lane >> 4)) ^ chunk_swizzle(r)) << 4);
+#pragma unroll
+    for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const i32x4*>(p + 16 * 128 * i);
+}
+
+template <int TI, int TJ>
+__device__ __forceinline__ void multiply(const i32x4 (&x)[TI], const i32x4 (&w)[TJ], i32x4 (&acc)[TI][TJ]) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[j], x[i], acc[i][j], 0, 0, 0);
+}
+
+// Scheduling order of a half step: `many` memory instructions of the kind `mask` (0x100 LDS reads, 0x20
+// global loads) spread evenly over `mfmas` MFMAs.
+template <int MANY, int MFMAS, int MASK, int I = 0>
+__device__ __forceinline__ void interleave() {
+    if constexpr (I < MANY) {
+        __builtin_amdgcn_sched_group_barrier(MASK, 1, 0);
+        constexpr int n = MFMAS * (I + 1) / MANY - MFMAS * I / MANY;
+        if constexpr (n > 0) __builtin_amdgcn_sched_group_barrier(0x8, n, 0);
+        interleave<MANY, MFMAS, MASK, I + 1>();
     }
 }
 
@@ -398,10 +482,12 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
         t.m_end = g.M;
         t.e = 0;
     }
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int wave = threadIdx.x >> 6;
     const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc<BM>(g.X, g.ldx, t.m0, t.m_end);
-    const __amdgpu_buffer_rsrc_t rw = rows_rsrc<BN>(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
+    Dma<BM, NW> dx;
+    Dma<BN, NW> dw;
+    dx.init(g.X, g.ldx, t.m0, t.m_end);
+    dw.init(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
 
     i32x4 acc[TI][TJ];
 #pragma unroll
@@ -409,50 +495,41 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-    dma_rows<BM, NW>(rx, g.ldx, 0, g.K, lds);
-    dma_rows<BN, NW>(rw, g.ldw, 0, g.K, lds + BM * 128);
+    const int nk = (g.K + 127) / 128;
+    dx.load(0, g.K, lds);
+    dw.load(0, g.K, lds + BM * 128);
     __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): this wave's loads landed
     __syncthreads();
-    const int nk = (g.K + 127) / 128;
+    dx.load(128, g.K, lds + kStage);                         // loads past K write zeros, so no step has a tail
+    dw.load(128, g.K, lds + kStage + BM * 128);
+    i32x4 x0[TI], w0[TJ], x1[TI], w1[TJ];
+    read_frags<TI>(lds, wm, 0, x0);
+    read_frags<TJ>(lds + BM * 128, wn, 0, w0);
     for (int kt = 0; kt < nk; ++kt) {
         uint8_t* cur = lds + (kt & 1) * kStage;
-        if (kt + 1 < nk) {
-            uint8_t* nxt = lds + ((kt + 1) & 1) * kStage;
-            dma_rows<BM, NW>(rx, g.ldx, (kt + 1) * 128, g.K, nxt);
-            dma_rows<BN, NW>(rw, g.ldw, (kt + 1) * 128, g.K, nxt + BM * 128);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            i32x4 a[TI], b[TJ];
-            const int kc = 4 * ks + (lane >> 4);
-#pragma unroll
-            for (int i = 0; i < TI; ++i) {
-                const int r = wm + 16 * i + (lane & 15);
-                a[i] = *reinterpret_cast<const i32x4*>(cur + r * 128 + ((kc ^ chunk_swizzle(r)) << 4));
-            }
-#pragma unroll
-            for (int j = 0; j < TJ; ++j) {
-                const int r = wn + 16 * j + (lane & 15);
-                b[j] = *reinterpret_cast<const i32x4*>(cur + BM * 128 + r * 128 + ((kc ^ chunk_swizzle(r)) << 4));
-            }
-#pragma unroll
-            for (int i = 0; i < TI; ++i)
-#pragma unroll
-                for (int j = 0; j < TJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(b[j], a[i], acc[i][j], 0, 0, 0);
-        }
-        __builtin_amdgcn_s_waitcnt(0x0F70);                  // vmcnt(0): the next stage's loads landed
-        __syncthreads();                                     // ... for every wave; this stage is free
+        uint8_t* nxt = lds + ((kt + 1) & 1) * kStage;
+        __builtin_amdgcn_sched_barrier(0);
+        read_frags<TI>(cur, wm, 1, x1);
+        read_frags<TJ>(cur + BM * 128, wn, 1, w1);
+        multiply<TI, TJ>(x0, w0, acc);
+        interleave<TI + TJ, TI * TJ, 0x100>();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0): all read, next stage landed
+        __syncthreads();
+        read_frags<TI>(nxt, wm, 0, x0);
+        read_frags<TJ>(nxt + BM * 128, wn, 0, w0);
+        dx.load(128 * (kt + 2), g.K, cur);
+        dw.load(128 * (kt + 2), g.K, cur + BM * 128);
+        multiply<TI, TJ>(x1, w1, acc);
+        interleave<TI + TJ, TI * TJ / 2, 0x100>();
+        interleave<(BM + BN) / 8 / NW, TI * TJ / 2, 0x20>();
     }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                      // no load may still write LDS when the block ends
 
     const bool vec = vec_out(g);
-#pragma unroll
-    for (int i = 0; i < TI; ++i) {
-        const int m = t.m0 + wm + 16 * i + (lane & 15);
-        const float sx = m < t.m_end ? g.sx[m] : 0.0f;
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) finish4(g, t, m, t.n0 + wn + 16 * j + 4 * (lane >> 4), acc[i][j], sx, vec);
-    }
+    if (g.out == EP_BF16) store_tile<EP_BF16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+    else if (g.out == EP_F16) store_tile<EP_F16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+    else store_tile<EP_F32, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
 }
 
 // ------------------------------------------------------------------------------- few rows
@@ -522,8 +599,15 @@ __global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_i8(GemmI8Args g
         i32x4 v = {0, 0, 0, 0};
 #pragma unroll
         for (int w = 0; w < kSkinnyWaves; ++w) v += *reinterpret_cast<const i32x4*>(&red[w][mt][4 * l]);
-        const int m = t.m0 + mt * 16 + (l & 15);
-        finish4(g, t, m, t.n0 + 4 * (l >> 4), v, m < t.m_end ? g.sx[m] : 0.0f, vec);
+        const int m = t.m0 + mt * 16 + (l & 15), n = t.n0 + 4 * (l >> 4);
+        if (m >= t.m_end || n >= g.N) continue;
+        const int count = g.N - n < 4 ? g.N - n : 4;
+        float sw[4], bias[4];
+        load_columns(g, t.e, n, count, sw, bias);
+        const float* b = g.bias ? bias : nullptr;
+        if (g.out == EP_BF16) store4<EP_BF16>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
+        else if (g.out == EP_F16) store4<EP_F16>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
+        else store4<EP_F32>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
     }
 }
 

@@ -388,7 +388,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 // ------------------------------------------------------------------------------- tiled product
 // A block of WGM x WGN waves owns a BM x BN tile of Y and walks K in steps of 128 codes. Both operand
 // tiles go straight from global memory into LDS (buffer_load ... lds, 16 bytes per lane, 8 rows of
-// 128 bytes per instruction), two stages. The eight 16-byte chunks of a row are swizzled: chunk c of
+// 128 bytes per instruction), in a ring of S stages. The eight 16-byte chunks of a row are swizzled: chunk c of
 // row r sits at slot c ^ ((r / 2) % 8), so that the 16 lanes of a fragment read (16 consecutive rows,
 // one chunk) cover all banks.
 //
@@ -396,32 +396,43 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 // wave reads the other set: the second half's behind the first half's MFMAs, the next step's first
 // half behind the second half's. So no MFMA waits for LDS, and the one barrier of a step sits between
 // the halves: by then every wave has read all of this stage (it may be overwritten: the loads of step
-// k + 2 start there) and the loads of step k + 1, in flight for a whole step, have landed.
+// k + S start there) and the loads of step k + 1, in flight for S - 1 steps, have landed.
+//
+// KS groups of WGM x WGN waves work on one tile, each on its own 128 codes of a step of 128 KS: more
+// waves hide the latency of small tiles, without a workspace. Their int32 sums are added through LDS.
 __device__ __forceinline__ int chunk_swizzle(int r) { return (r >> 1) & 7; }
 
 // One operand tile of ROWS rows: the lane's byte offset in its first row group, and the loads of step k0.
 // The row groups of a wave are 8 NW rows apart, so the swizzle (period 16 rows) is that of the first one.
+// Every wave issues the same number of loads, which the waits count: a wave without a row group of its
+// own loads zeros (an offset past the resource) into the spare KiB behind the ring.
 template <int ROWS, int NW>
 struct Dma {
+    static constexpr int kLoads = (ROWS / 8 + NW - 1) / NW;
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row_off;           // of the wave's first row group
     int chunk;                  // K chunk that the lane's slot holds
     uint32_t group_step;        // bytes between the wave's row groups
-    __device__ __forceinline__ void init(const int8_t* src, int ld, int64_t r0, int64_t r_end) {
-        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __device__ __forceinline__ void init(const int8_t* src, int ld, int64_t r0, int64_t r_end, int wave) {
+        const int lane = threadIdx.x & 63;
         const int r = 8 * wave + (lane >> 3);
         rs = rows_rsrc<ROWS>(src, ld, r0, r_end);
         row_off = (uint32_t)(r * ld);
         chunk = 16 * ((lane & 7) ^ chunk_swizzle(r));
         group_step = (uint32_t)(8 * NW * ld);
     }
-    __device__ __forceinline__ void load(int k0, int K, uint8_t* lds) const {
-        static_assert(NW % 2 == 0, "the swizzle repeats every two row groups");
-        const int wave = threadIdx.x >> 6, k = k0 + chunk;
+    __device__ __forceinline__ void load(int k0, int K, uint8_t* lds, uint8_t* spare, int wave) const {
+        static_assert(NW % 2 == 0 && (ROWS / 8 % NW == 0 || ROWS / 8 < NW), "whole row groups, a swizzle of two of them");
+        const int k = k0 + chunk;
         const uint32_t at = row_off + ((uint32_t)k | ((uint32_t)((K - 1 - k) >> 31) & kOob));   // past K reads zero
+        if constexpr (ROWS / 8 < NW) {
+            const bool mine = wave < ROWS / 8;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(mine ? lds + 1024 * wave : spare), 16, mine ? at : kOob, 0, 0, 0);
+        } else {
 #pragma unroll
-        for (int j = 0; j < ROWS / 8 / NW; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + 1024 * (wave + NW * j)), 16, at + j * group_step, 0, 0, 0);
+            for (int j = 0; j < kLoads; ++j)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(lds + 1024 * (wave + NW * j)), 16, at + j * group_step, 0, 0, 0);
+        }
     }
 };
 
@@ -454,12 +465,25 @@ __device__ __forceinline__ void interleave() {
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, bool EXPERTS>
-__global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
-    constexpr int NW = WGM * WGN;
+// s_waitcnt vmcnt(n) lgkmcnt(0)
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+    static_assert(N < 64, "vmcnt has six bits");
+    __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0070);
+}
+
+template <int BM, int BN, int WGM, int WGN, int S, int KS, bool EXPERTS>
+__global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
+    constexpr int NW = WGM * WGN;                            // waves of a K group
     constexpr int TI = BM / WGM / 16, TJ = BN / WGN / 16;
     constexpr int kStage = (BM + BN) * 128;
-    __shared__ __align__(1024) uint8_t lds[2 * kStage];
+    constexpr int kLoads = Dma<BM, NW>::kLoads + Dma<BN, NW>::kLoads;       // per wave and stage
+    constexpr bool kSpare = BM / 8 < NW || BN / 8 < NW;
+    constexpr int kRing = S * kStage;                        // of a K group
+    constexpr int kSums = (KS - 1) * BM * BN * 4;
+    static_assert(kSums <= KS * kRing, "the sums of the other K groups reuse the rings");
+    __shared__ __align__(1024) uint8_t smem[KS * kRing + (kSpare ? 1024 : 0)];
+    uint8_t* spare = smem + KS * kRing;
     const int tiles_n = (g.N + BN - 1) / BN;
     TileAt t;
     if constexpr (EXPERTS) {
@@ -482,12 +506,14 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
         t.m_end = g.M;
         t.e = 0;
     }
-    const int wave = threadIdx.x >> 6;
+    const int wave = (threadIdx.x >> 6) % NW;
+    const int kg = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / NW);   // K group of the wave
+    uint8_t* lds = smem + kg * kRing;
     const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
     Dma<BM, NW> dx;
     Dma<BN, NW> dw;
-    dx.init(g.X, g.ldx, t.m0, t.m_end);
-    dw.init(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
+    dx.init(g.X, g.ldx, t.m0, t.m_end, wave);
+    dw.init(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N, wave);
 
     i32x4 acc[TI][TJ];
 #pragma unroll
@@ -495,120 +521,64 @@ __global__ __launch_bounds__(64 * WGM * WGN) void gemm_i8(GemmI8Args g) {
 #pragma unroll
         for (int j = 0; j < TJ; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
 
-    const int nk = (g.K + 127) / 128;
-    dx.load(0, g.K, lds);
-    dw.load(0, g.K, lds + BM * 128);
-    __builtin_amdgcn_s_waitcnt(0x0F70);                      // vmcnt(0): this wave's loads landed
+    const int nk = (g.K + 128 * KS - 1) / (128 * KS);
+    int k0 = 128 * kg;                                       // of the next loads
+#pragma unroll
+    for (int p = 0; p < S; ++p) {                            // loads past K write zeros, so no step has a tail
+        dx.load(k0, g.K, lds + p * kStage, spare, wave);
+        dw.load(k0, g.K, lds + p * kStage + BM * 128, spare, wave);
+        k0 += 128 * KS;
+    }
+    wait_loads<(S - 1) * kLoads>();                          // this wave's part of the first stage landed
     __syncthreads();
-    dx.load(128, g.K, lds + kStage);                         // loads past K write zeros, so no step has a tail
-    dw.load(128, g.K, lds + kStage + BM * 128);
     i32x4 x0[TI], w0[TJ], x1[TI], w1[TJ];
     read_frags<TI>(lds, wm, 0, x0);
     read_frags<TJ>(lds + BM * 128, wn, 0, w0);
+    uint8_t* cur = lds;
     for (int kt = 0; kt < nk; ++kt) {
-        uint8_t* cur = lds + (kt & 1) * kStage;
-        uint8_t* nxt = lds + ((kt + 1) & 1) * kStage;
+        uint8_t* nxt = cur + kStage == lds + kRing ? lds : cur + kStage;
         __builtin_amdgcn_sched_barrier(0);
         read_frags<TI>(cur, wm, 1, x1);
         read_frags<TJ>(cur + BM * 128, wn, 1, w1);
         multiply<TI, TJ>(x0, w0, acc);
         interleave<TI + TJ, TI * TJ, 0x100>();
         __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0x0070);                  // vmcnt(0) lgkmcnt(0): all read, next stage landed
+        wait_loads<(S - 2) * kLoads>();                      // all of this stage read, the next one landed
         __syncthreads();
+        dx.load(k0, g.K, cur, spare, wave);
+        dw.load(k0, g.K, cur + BM * 128, spare, wave);
+        k0 += 128 * KS;
         read_frags<TI>(nxt, wm, 0, x0);
         read_frags<TJ>(nxt + BM * 128, wn, 0, w0);
-        dx.load(128 * (kt + 2), g.K, cur);
-        dw.load(128 * (kt + 2), g.K, cur + BM * 128);
         multiply<TI, TJ>(x1, w1, acc);
+        interleave<kLoads, TI * TJ / 2, 0x20>();
         interleave<TI + TJ, TI * TJ / 2, 0x100>();
-        interleave<(BM + BN) / 8 / NW, TI * TJ / 2, 0x20>();
+        cur = nxt;
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);                      // no load may still write LDS when the block ends
+    if constexpr (KS > 1) {
+        __syncthreads();                                     // every group is done with its ring
+        i32x4* sums = reinterpret_cast<i32x4*>(smem) + (wave * TI * TJ) * 64 + (threadIdx.x & 63);
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) sums[((kg - 1) * NW * TI * TJ + i * TJ + j) * 64] = acc[i][j];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int q = 0; q < KS - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) acc[i][j] += sums[(q * NW * TI * TJ + i * TJ + j) * 64];
+    }
 
     const bool vec = vec_out(g);
     if (g.out == EP_BF16) store_tile<EP_BF16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
     else if (g.out == EP_F16) store_tile<EP_F16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
     else store_tile<EP_F32, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
-}
-
-// ------------------------------------------------------------------------------- few rows
-// For a few rows of X (a decoding step): W streams once from memory straight into MFMA registers, no
-// LDS staging. A block owns 16 output columns; its 8 waves split K in chunks of 128 codes, four
-// chunks of loads in flight each, every wave multiplying MT tiles of 16 rows; the int32 partial sums
-// meet in LDS.
-constexpr int kSkinnyWaves = 8;
-constexpr int kSkinnyUnroll = 4;
-
-template <int MT, bool EXPERTS>
-__global__ __launch_bounds__(64 * kSkinnyWaves) void gemm_skinny_i8(GemmI8Args g) {
-    __shared__ __align__(16) int red[kSkinnyWaves][MT][256];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int r = lane & 15, kq = lane >> 4;
-    const int tiles_n = (g.N + 15) / 16;
-    TileAt t{0, g.M, 0, 0, true};
-    if constexpr (EXPERTS) {
-        t = expert_tile<16 * MT>(g, (int)blockIdx.x / tiles_n);
-        if (!t.any) return;
-        t.n0 = ((int)blockIdx.x % tiles_n) * 16;
-        if (t.e == g.experts) {
-            zero_rows(g, t, 16 * MT, 16);
-            return;
-        }
-    } else {
-        t.n0 = (int)blockIdx.x * 16;
-    }
-    const __amdgpu_buffer_rsrc_t rw = rows_rsrc<16>(g.W + (int64_t)t.e * g.N * g.ldw, g.ldw, t.n0, g.N);
-    const __amdgpu_buffer_rsrc_t rx = rows_rsrc<16 * MT>(g.X, g.ldx, t.m0, t.m_end);
-    const uint32_t woff = (uint32_t)r * g.ldw;
-    i32x4 acc[MT];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = i32x4{0, 0, 0, 0};
-    const int nkc = (g.K + 127) / 128;
-    for (int kb = wave; kb < nkc; kb += kSkinnyWaves * kSkinnyUnroll) {
-        i32x4 bw[kSkinnyUnroll][2], ax[kSkinnyUnroll][MT][2];
-#pragma unroll
-        for (int u = 0; u < kSkinnyUnroll; ++u) {
-            const int kc = kb + u * kSkinnyWaves;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = kc * 128 + 64 * h + 16 * kq;
-                const bool in = k < g.K;
-                bw[u][h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, in ? woff + (uint32_t)k : kOob, 0, 0));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    const uint32_t xo = (uint32_t)(mt * 16 + r) * g.ldx + (uint32_t)k;
-                    ax[u][mt][h] = __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, in ? xo : kOob, 0, 0));
-                }
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < kSkinnyUnroll; ++u)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-                    acc[mt] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bw[u][h], ax[u][mt][h], acc[mt], 0, 0, 0);
-    }
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) *reinterpret_cast<i32x4*>(&red[wave][mt][4 * lane]) = acc[mt];
-    __syncthreads();
-    const bool vec = vec_out(g);
-    for (int p = threadIdx.x; p < MT * 64; p += 64 * kSkinnyWaves) {
-        const int mt = p >> 6, l = p & 63;
-        i32x4 v = {0, 0, 0, 0};
-#pragma unroll
-        for (int w = 0; w < kSkinnyWaves; ++w) v += *reinterpret_cast<const i32x4*>(&red[w][mt][4 * l]);
-        const int m = t.m0 + mt * 16 + (l & 15), n = t.n0 + 4 * (l >> 4);
-        if (m >= t.m_end || n >= g.N) continue;
-        const int count = g.N - n < 4 ? g.N - n : 4;
-        float sw[4], bias[4];
-        load_columns(g, t.e, n, count, sw, bias);
-        const float* b = g.bias ? bias : nullptr;
-        if (g.out == EP_BF16) store4<EP_BF16>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
-        else if (g.out == EP_F16) store4<EP_F16>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
-        else store4<EP_F32>(g.Y, (int64_t)m * g.ldy + n, v, sw, g.sx[m], b, count, vec);
-    }
 }
 
 // Tiles of BM rows that M rows split over the experts can need: every range adds at most one partly
@@ -619,25 +589,14 @@ int64_t row_tiles(const GemmI8Args& g, int bm) {
     return most < g.M ? most : g.M;
 }
 
-template <int BM, int BN, int WGM, int WGN>
+template <int BM, int BN, int WGM, int WGN, int S, int KS>
 hipError_t tiled_go(const GemmI8Args& g, hipStream_t stream) {
     const int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
-    if (blocks * (64 * WGM * WGN) > kMaxThreads) return hipErrorInvalidValue;
+    if (blocks * (64 * WGM * WGN * KS) > kMaxThreads) return hipErrorInvalidValue;
     if (g.experts)
-        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN), 0, stream, g);
+        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
     else
-        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN), 0, stream, g);
-    return hipGetLastError();
-}
-
-template <int MT>
-hipError_t skinny_go(const GemmI8Args& g, hipStream_t stream) {
-    const int64_t blocks = row_tiles(g, 16 * MT) * (((int64_t)g.N + 15) / 16);
-    if (blocks * (64 * kSkinnyWaves) > kMaxThreads) return hipErrorInvalidValue;
-    if (g.experts)
-        hipLaunchKernelGGL((gemm_skinny_i8<MT, true>), dim3((unsigned)blocks), dim3(64 * kSkinnyWaves), 0, stream, g);
-    else
-        hipLaunchKernelGGL((gemm_skinny_i8<MT, false>), dim3((unsigned)blocks), dim3(64 * kSkinnyWaves), 0, stream, g);
+        hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, S, KS, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -662,17 +621,51 @@ hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* ds
     return hipGetLastError();
 }
 
+// Tile of a product with one weight. A step of 128 K columns takes a block about the time below, whatever
+// M, N and K (measured with one block per CU; small tiles are bound by the latency and the rate of the
+// loads from L2, the largest by the MFMAs), so the estimate is rounds of tiles over the CUs times steps
+// times that. It picks, e.g., 256 x 256 for 4096 x 8192 x 8192 (211 us; 128 x 128: 266), 128 x 128 for
+// 512 x 8192 x 8192 (42; 64 x 64: 59), 128 x 64 for 333 x 5003 x 3856 (22; 128 x 128: 24, 64 x 64: 26),
+// 32 x 64 for 64 x 8192 x 8192 (20; 64 x 64: 24), 16 x 64 for 1 x 11520 x 3840 (11) and 16 x 32 with two
+// K groups for 1 x 8192 x 8192 (15; 16 x 64: 16) and 1 x 4096 x 16384 (16; 16 x 64: 25).
+struct TileCost {
+    int bm, bn;
+    float step_us;
+    hipError_t (*go)(const GemmI8Args&, hipStream_t);
+};
+const TileCost kTiles[] = {
+    {256, 256, 1.65f, tiled_go<256, 256, 2, 4, 2, 1>}, {256, 128, 0.97f, tiled_go<256, 128, 4, 2, 3, 1>},
+    {128, 128, 0.65f, tiled_go<128, 128, 2, 4, 4, 1>}, {128, 64, 0.50f, tiled_go<128, 64, 2, 2, 6, 1>},
+    {64, 64, 0.375f, tiled_go<64, 64, 2, 2, 4, 1>},    {32, 64, 0.305f, tiled_go<32, 64, 1, 4, 5, 1>},
+    {32, 32, 0.245f, tiled_go<32, 32, 1, 2, 4, 2>},    {16, 64, 0.28f, tiled_go<16, 64, 1, 4, 6, 1>},
+    {16, 32, 0.235f, tiled_go<16, 32, 1, 2, 6, 2>},
+};
+constexpr float kTileUs = 1.5f;             // start and epilogue of a tile
+
 hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
-    // rows that meet one weight: all of them, or an expert's share
-    const int64_t per = g.experts ? ((int64_t)g.M + g.experts - 1) / g.experts : g.M;
-    if (per <= 16) return skinny_go<1>(g, stream);
-    if (per <= 32) return skinny_go<2>(g, stream);
-    if (per <= 64) return skinny_go<4>(g, stream);
-    auto tiles = [&](int bm, int bn) { return (((int64_t)g.M + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn); };
-    if (tiles(256, 256) >= device_cus()) return tiled_go<256, 256, 2, 4>(g, stream);
-    if (tiles(128, 128) >= 2L * device_cus()) return tiled_go<128, 128, 2, 2>(g, stream);
-    return tiled_go<64, 64, 2, 2>(g, stream);
+    if (!g.experts) {
+        const TileCost* best = nullptr;
+        float least = 0.0f;
+        for (const TileCost& t : kTiles) {
+            const int64_t tiles = (((int64_t)g.M + t.bm - 1) / t.bm) * (((int64_t)g.N + t.bn - 1) / t.bn);
+            const float us = (float)((tiles + device_cus() - 1) / device_cus()) * ((float)((g.K + 127) / 128) * t.step_us + kTileUs);
+            if (!best || us < least) best = &t, least = us;
+        }
+        return best->go(g, stream);
+    }
+    // Experts: how many rows each has is known to the device only, so the tile goes by the average, several
+    // small blocks share a CU where the weights' bytes bound the time, and a tile too large to give
+    // every CU one makes way for the next. Measured, 32 experts: 2 rows each on 16 x 64 tiles 31.5 us (4096 x
+    // 2048; 32 x 64: 31.9, 64 x 64: 33.3), 8 rows on 32 x 64 41.4 (16 x 64: 43.0), 32 rows (2048 x 4096) on
+    // 128 x 128 48.8 (64 x 64: 52.4), 512 rows on 128 x 256 186 (256 x 256: 195, 128 x 128: 198).
+    const int64_t used = g.M < g.experts ? g.M : g.experts, rows = (g.M + used - 1) / used;
+    auto fills = [&](int bm, int bn) { return used * ((rows + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn) >= device_cus(); };
+    if (rows > 64 && fills(128, 256)) return tiled_go<128, 256, 2, 4, 3, 1>(g, stream);
+    if (rows > 16 && fills(128, 128)) return tiled_go<128, 128, 2, 2, 2, 1>(g, stream);
+    if (rows > 16 && fills(128, 64)) return tiled_go<128, 64, 2, 2, 3, 1>(g, stream);
+    if (rows > 4) return tiled_go<32, 64, 1, 4, 3, 1>(g, stream);
+    return tiled_go<16, 64, 1, 4, 3, 1>(g, stream);
 }
 
 }  // namespace ep

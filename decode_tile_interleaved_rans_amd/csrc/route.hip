@@ -169,40 +169,55 @@ __global__ __launch_bounds__(kSortThreads) void place_choices(RouteArgs r, int64
 }
 
 // ------------------------------------------------------------------------------- rows of the experts
-// Copies of U bytes: each thread takes a piece of a token's vector and stores it once per choice.
-template <typename U>
+// Where piece c (U elements or bytes) of a row of n starts: the last one ends with the row and repeats part
+// of the one before it (the same values), so rows of any length and alignment move in whole pieces.
+template <int U>
+__device__ __forceinline__ int64_t piece_start(int64_t c, int64_t n) {
+    return U * c < n - U ? U * c : n - U;
+}
+
+// Each thread takes U bytes (16, or 1 for rows shorter than that) of a token's vector and stores them once
+// per choice.
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+template <int U> struct Piece { typedef u32x4 type; };
+template <> struct Piece<1> { typedef uint8_t type; };
+template <int U>
 __device__ __forceinline__ void copy_piece(const uint8_t* x, int64_t ldx, int64_t t, int64_t c, const int32_t* pos, int k,
-                                           int64_t pieces, int64_t R, U* rows) {
-    const U v = reinterpret_cast<const U*>(x + t * ldx)[c];
+                                           int64_t row_bytes, int64_t R, uint8_t* rows) {
+    const int64_t at = piece_start<U>(c, row_bytes);
+    typename Piece<U>::type v;
+    __builtin_memcpy(&v, x + t * ldx + at, U);
     for (int j = 0; j < k; ++j) {
         const int p = pos[j];
         const int64_t row = p < 0 ? -1 - (int64_t)p : p;
-        if (row < R) rows[row * pieces + c] = p < 0 ? U{} : v;
+        const typename Piece<U>::type o = v & (typename Piece<U>::type)(p < 0 ? 0u : ~0u);   // a dropped choice's row is zero
+        if (row < R) __builtin_memcpy(rows + row * row_bytes + at, &o, U);
     }
 }
 
-template <typename U>
-__global__ __launch_bounds__(256) void scatter_rows(const uint8_t* x, int64_t ldx, int64_t T, int k, int64_t pieces, int tpb,
-                                                    const int32_t* pos, int64_t R, U* rows) {
+template <int U>
+__global__ __launch_bounds__(256) void scatter_rows(const uint8_t* x, int64_t ldx, int64_t T, int k, int64_t row_bytes, int tpb,
+                                                    const int32_t* pos, int64_t R, uint8_t* rows) {
+    const int64_t pieces = (row_bytes + U - 1) / U;
     for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < T; t0 += (int64_t)gridDim.x * tpb) {
         if (tpb == 1) {
-            for (int64_t c = threadIdx.x; c < pieces; c += 256) copy_piece<U>(x, ldx, t0, c, pos + t0 * k, k, pieces, R, rows);
+            for (int64_t c = threadIdx.x; c < pieces; c += 256) copy_piece<U>(x, ldx, t0, c, pos + t0 * k, k, row_bytes, R, rows);
             continue;
         }
         const int64_t t1 = t0 + tpb < T ? t0 + tpb : T;
         const int p32 = (int)pieces;                           // tpb > 1: at most 128 pieces per token
         for (int u = threadIdx.x; u < (int)(t1 - t0) * p32; u += 256) {
             const int64_t t = t0 + u / p32;
-            copy_piece<U>(x, ldx, t, u % p32, pos + t * k, k, pieces, R, rows);
+            copy_piece<U>(x, ldx, t, u % p32, pos + t * k, k, row_bytes, R, rows);
         }
     }
 }
 
 // Up to 1024 choices: every block orders all of them by itself (a chunk of one choice per thread) and
 // copies its own tokens, so a decoding step takes one launch. Block 0 writes offsets and pos.
-template <typename U>
-__global__ __launch_bounds__(kSortThreads) void sort_small(RouteArgs r, const uint8_t* x, int64_t ldx, int64_t pieces, int tpb,
-                                                           U* rows) {
+template <int U>
+__global__ __launch_bounds__(kSortThreads) void sort_small(RouteArgs r, const uint8_t* x, int64_t ldx, int64_t row_bytes, int tpb,
+                                                           uint8_t* rows) {
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ int wave_sum[kSortWaves];
     __shared__ int32_t dst[kSortThreads];
@@ -230,9 +245,10 @@ __global__ __launch_bounds__(kSortThreads) void sort_small(RouteArgs r, const ui
     if (!rows) return;
     __syncthreads();
     const int64_t t0 = (int64_t)blockIdx.x * tpb, t1 = t0 + tpb < r.T ? t0 + tpb : r.T;
+    const int64_t pieces = (row_bytes + U - 1) / U;
     for (int64_t u = threadIdx.x; u < (t1 - t0) * pieces; u += kSortThreads) {
         const int64_t t = t0 + u / pieces;
-        copy_piece<U>(x, ldx, t, u % pieces, dst + t * r.k, r.k, pieces, n, rows);
+        copy_piece<U>(x, ldx, t, u % pieces, dst + t * r.k, r.k, row_bytes, n, rows);
     }
 }
 
@@ -254,7 +270,7 @@ __device__ __forceinline__ typename Store<DT>::type narrow(float v) {
     else return __builtin_bit_cast(uint16_t, (_Float16)v);
 }
 
-// V consecutive elements: 16 bytes, or one where rows are not 16-byte aligned.
+// V consecutive elements: 16 bytes at any alignment of the element, or one for rows shorter than that.
 template <int DT, int V>
 struct Vec {
     typename Store<DT>::type e[V];
@@ -262,25 +278,12 @@ struct Vec {
 template <int DT, int V>
 __device__ __forceinline__ Vec<DT, V> load_vec(const typename Store<DT>::type* p) {
     Vec<DT, V> v;
-    if constexpr (V * sizeof(typename Store<DT>::type) == 16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        __builtin_memcpy(&v, &u, 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) v.e[i] = p[i];
-    }
+    __builtin_memcpy(&v, p, sizeof v);
     return v;
 }
 template <int DT, int V>
 __device__ __forceinline__ void store_vec(typename Store<DT>::type* p, const Vec<DT, V>& v) {
-    if constexpr (V * sizeof(typename Store<DT>::type) == 16) {
-        uint4 u;
-        __builtin_memcpy(&u, &v, 16);
-        *reinterpret_cast<uint4*>(p) = u;
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) p[i] = v.e[i];
-    }
+    __builtin_memcpy(p, &v, sizeof v);
 }
 
 constexpr int kRowsAtOnce = 4;              // rows of a token loaded together
@@ -289,10 +292,11 @@ template <int DT, int V>
 __global__ __launch_bounds__(256) void combine_tokens(CombineArgs c, typename Store<DT>::type* y, int tpb) {
     typedef typename Store<DT>::type E;
     const E* ys = static_cast<const E*>(c.ys);
-    const int64_t pieces = c.H / V;
+    const int64_t pieces = (c.H + V - 1) / V;
     auto piece = [&](int64_t t, int64_t p) {
         const int32_t* pos = c.pos + t * c.k;
         const float* w = c.w ? c.w + t * c.k : nullptr;
+        const int64_t at = piece_start<V>(p, c.H);
         float acc[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -303,7 +307,7 @@ __global__ __launch_bounds__(256) void combine_tokens(CombineArgs c, typename St
             for (int j = 0; j < kRowsAtOnce; ++j) {
                 const int64_t row = j0 + j < c.k ? pos[j0 + j] : -1;
                 on[j] = row >= 0 && row < c.R;
-                if (on[j]) v[j] = load_vec<DT, V>(ys + row * c.H + p * V);
+                if (on[j]) v[j] = load_vec<DT, V>(ys + row * c.H + at);
             }
 #pragma unroll
             for (int j = 0; j < kRowsAtOnce; ++j) {
@@ -316,7 +320,7 @@ __global__ __launch_bounds__(256) void combine_tokens(CombineArgs c, typename St
         Vec<DT, V> o;
 #pragma unroll
         for (int i = 0; i < V; ++i) o.e[i] = narrow<DT>(acc[i]);
-        store_vec<DT, V>(y + t * c.H + p * V, o);
+        store_vec<DT, V>(y + t * c.H + at, o);
     };
     for (int64_t t0 = (int64_t)blockIdx.x * tpb; t0 < c.T; t0 += (int64_t)gridDim.x * tpb) {
         if (tpb == 1) {
@@ -329,7 +333,7 @@ __global__ __launch_bounds__(256) void combine_tokens(CombineArgs c, typename St
     }
 }
 
-// TPT threads per token (a wave, or the block). dy is read once per kRowsAtOnce choices; the dot
+// TPT threads per token (16 lanes, a wave, or the block). dy is read once per kRowsAtOnce choices; the dot
 // products are summed per thread in column order, then across the lanes and waves in a fixed order.
 template <int DT, int V, int TPT>
 __global__ __launch_bounds__(256) void combine_tokens_grad(CombineArgs c, const typename Store<DT>::type* dy,
@@ -337,8 +341,8 @@ __global__ __launch_bounds__(256) void combine_tokens_grad(CombineArgs c, const 
     typedef typename Store<DT>::type E;
     __shared__ float part[4][kRowsAtOnce];
     const E* ys = static_cast<const E*>(c.ys);
-    const int64_t pieces = c.H / V;
-    // t is uniform in the block for TPT 256 (block barriers below), in the wave for TPT 64
+    const int64_t pieces = (c.H + V - 1) / V;
+    // t is uniform in the block for TPT 256 (block barriers below), in a group of TPT lanes otherwise
     for (int64_t t = (int64_t)blockIdx.x * (256 / TPT) + threadIdx.x / TPT; t < c.T; t += (int64_t)gridDim.x * (256 / TPT)) {
         for (int j0 = 0; j0 < c.k; j0 += kRowsAtOnce) {
             int64_t row[kRowsAtOnce];
@@ -355,24 +359,27 @@ __global__ __launch_bounds__(256) void combine_tokens_grad(CombineArgs c, const 
                 dot[j] = 0.0f;
             }
             for (int64_t q = threadIdx.x % TPT; q < pieces; q += TPT) {
-                const Vec<DT, V> g = load_vec<DT, V>(dy + t * c.H + q * V);
+                const int64_t at = piece_start<V>(q, c.H);
+                const int again = (int)(q * V - at);           // elements that the piece before has counted
+                const Vec<DT, V> g = load_vec<DT, V>(dy + t * c.H + at);
                 Vec<DT, V> v[kRowsAtOnce];
                 if (d_w) {
 #pragma unroll
                     for (int j = 0; j < kRowsAtOnce; ++j)
-                        if (kept[j]) v[j] = load_vec<DT, V>(ys + row[j] * c.H + q * V);
+                        if (kept[j]) v[j] = load_vec<DT, V>(ys + row[j] * c.H + at);
                 }
 #pragma unroll
                 for (int j = 0; j < kRowsAtOnce; ++j) {
                     if (d_w && kept[j]) {
 #pragma unroll
-                        for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(widen<DT>(g.e[i]), widen<DT>(v[j].e[i]), dot[j]);
+                        for (int i = 0; i < V; ++i)
+                        if (i >= again) dot[j] = __builtin_fmaf(widen<DT>(g.e[i]), widen<DT>(v[j].e[i]), dot[j]);
                     }
                     if (d_ys && in[j]) {
                         Vec<DT, V> o;
 #pragma unroll
                         for (int i = 0; i < V; ++i) o.e[i] = kept[j] ? narrow<DT>(w[j] * widen<DT>(g.e[i])) : narrow<DT>(0.0f);
-                        store_vec<DT, V>(d_ys + row[j] * c.H + q * V, o);
+                        store_vec<DT, V>(d_ys + row[j] * c.H + at, o);
                     }
                 }
             }
@@ -380,7 +387,7 @@ __global__ __launch_bounds__(256) void combine_tokens_grad(CombineArgs c, const 
 #pragma unroll
             for (int j = 0; j < kRowsAtOnce; ++j)
 #pragma unroll
-                for (int o = 32; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
+                for (int o = (TPT < 64 ? TPT : 64) / 2; o > 0; o >>= 1) dot[j] += __shfl_xor(dot[j], o);
             if constexpr (TPT == 256) {
                 if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -392,7 +399,7 @@ __global__ __launch_bounds__(256) void combine_tokens_grad(CombineArgs c, const 
                     d_w[t * c.k + j0 + threadIdx.x] = s;
                 }
                 __syncthreads();
-            } else if ((threadIdx.x & 63) == 0) {
+            } else if (threadIdx.x % TPT == 0) {
 #pragma unroll
                 for (int j = 0; j < kRowsAtOnce; ++j)
                     if (j0 + j < c.k) d_w[t * c.k + j0 + j] = dot[j];
@@ -407,17 +414,17 @@ unsigned token_blocks(int64_t groups) { return (unsigned)(groups < (1 << 20) ? g
 // Tokens per 256-thread block: several when a token has few pieces.
 int tokens_per_block(int64_t pieces) { return pieces >= 256 || pieces <= 0 ? 1 : pieces > 128 ? 1 : (int)(256 / pieces); }
 
-template <typename U>
+template <int U>
 hipError_t sort_go(const RouteArgs& r, const void* x, int64_t ldx, int64_t row_bytes, void* rows, void* scratch,
                    hipStream_t stream) {
-    const int64_t n = r.T * r.k, pieces = row_bytes / (int64_t)sizeof(U);
+    const int64_t n = r.T * r.k, pieces = (row_bytes + U - 1) / U;
     if (n <= kSortThreads) {
         // a block's copying threads take about one 1024-piece round
         int64_t tpb = pieces > 0 ? kSortThreads / pieces : r.T;
         tpb = tpb < 1 ? 1 : tpb > r.T ? r.T : tpb;
         const unsigned blocks = n > 0 && rows && pieces > 0 ? (unsigned)((r.T + tpb - 1) / tpb) : 1u;
         hipLaunchKernelGGL(sort_small<U>, dim3(blocks), dim3(kSortThreads), sort_lds_bytes(r.E), stream, r,
-                           static_cast<const uint8_t*>(x), ldx, pieces, (int)tpb, n > 0 ? static_cast<U*>(rows) : nullptr);
+                           static_cast<const uint8_t*>(x), ldx, row_bytes, (int)tpb, n > 0 ? static_cast<uint8_t*>(rows) : nullptr);
         return hipGetLastError();
     }
     const int64_t chunks = (n + kSortThreads - 1) / kSortThreads;
@@ -433,34 +440,34 @@ hipError_t sort_go(const RouteArgs& r, const void* x, int64_t ldx, int64_t row_b
     if (e != hipSuccess || !rows || pieces <= 0) return e;
     const int tpb = tokens_per_block(pieces);
     hipLaunchKernelGGL(scatter_rows<U>, dim3(token_blocks((r.T + tpb - 1) / tpb)), dim3(256), 0, stream,
-                       static_cast<const uint8_t*>(x), ldx, r.T, r.k, pieces, tpb, (const int32_t*)r.pos, n,
-                       static_cast<U*>(rows));
+                       static_cast<const uint8_t*>(x), ldx, r.T, r.k, row_bytes, tpb, (const int32_t*)r.pos, n,
+                       static_cast<uint8_t*>(rows));
     return hipGetLastError();
 }
 
 template <int DT, int V>
 hipError_t combine_go(const CombineArgs& c, void* y, hipStream_t stream) {
-    const int tpb = tokens_per_block(c.H / V);
+    const int tpb = tokens_per_block((c.H + V - 1) / V);
     hipLaunchKernelGGL((combine_tokens<DT, V>), dim3(token_blocks((c.T + tpb - 1) / tpb)), dim3(256), 0, stream, c,
                        static_cast<typename Store<DT>::type*>(y), tpb);
     return hipGetLastError();
 }
 
-template <int DT, int V>
-hipError_t grad_go(const CombineArgs& c, const void* dy, void* d_ys, float* d_w, hipStream_t stream) {
+template <int DT, int V, int TPT>
+hipError_t grad_tpt(const CombineArgs& c, const void* dy, void* d_ys, float* d_w, hipStream_t stream) {
     typedef typename Store<DT>::type E;
-    if (c.H / V <= 128)
-        hipLaunchKernelGGL((combine_tokens_grad<DT, V, 64>), dim3(token_blocks((c.T + 3) / 4)), dim3(256), 0, stream, c,
-                           static_cast<const E*>(dy), static_cast<E*>(d_ys), d_w);
-    else
-        hipLaunchKernelGGL((combine_tokens_grad<DT, V, 256>), dim3(token_blocks(c.T)), dim3(256), 0, stream, c,
-                           static_cast<const E*>(dy), static_cast<E*>(d_ys), d_w);
+    constexpr int tpb = 256 / TPT;
+    hipLaunchKernelGGL((combine_tokens_grad<DT, V, TPT>), dim3(token_blocks((c.T + tpb - 1) / tpb)), dim3(256), 0, stream, c,
+                       static_cast<const E*>(dy), static_cast<E*>(d_ys), d_w);
     return hipGetLastError();
 }
 
-bool aligned16(const void* a, const void* b, const void* d, int64_t row_bytes) {
-    return !((reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | reinterpret_cast<uintptr_t>(d) |
-              (uintptr_t)row_bytes) & 15);
+template <int DT, int V>
+hipError_t grad_go(const CombineArgs& c, const void* dy, void* d_ys, float* d_w, hipStream_t stream) {
+    const int64_t pieces = (c.H + V - 1) / V;
+    if (pieces <= 32) return grad_tpt<DT, V, 16>(c, dy, d_ys, d_w, stream);
+    if (pieces <= 128) return grad_tpt<DT, V, 64>(c, dy, d_ys, d_w, stream);
+    return grad_tpt<DT, V, 256>(c, dy, d_ys, d_w, stream);
 }
 
 }  // namespace
@@ -471,18 +478,13 @@ size_t sort_tokens_scratch(int64_t T, int k, int E) {
 
 hipError_t launch_sort_tokens(const RouteArgs& r, const void* x, int64_t ldx_bytes, int64_t row_bytes, void* rows,
                               void* scratch, hipStream_t stream) {
-    // pieces as wide as every address allows
-    const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(rows) | (uintptr_t)ldx_bytes |
-                        (uintptr_t)row_bytes;
-    if (!(a & 15)) return sort_go<uint4>(r, x, ldx_bytes, row_bytes, rows, scratch, stream);
-    if (!(a & 3)) return sort_go<uint32_t>(r, x, ldx_bytes, row_bytes, rows, scratch, stream);
-    if (!(a & 1)) return sort_go<uint16_t>(r, x, ldx_bytes, row_bytes, rows, scratch, stream);
-    return sort_go<uint8_t>(r, x, ldx_bytes, row_bytes, rows, scratch, stream);
+    return row_bytes >= 16 ? sort_go<16>(r, x, ldx_bytes, row_bytes, rows, scratch, stream)
+                           : sort_go<1>(r, x, ldx_bytes, row_bytes, rows, scratch, stream);
 }
 
 hipError_t launch_combine_tokens(const CombineArgs& c, void* y, hipStream_t stream) {
     if (c.T <= 0 || c.H <= 0) return hipSuccess;
-    const bool v = aligned16(c.ys, y, nullptr, c.H * (c.dtype == EP_F32 ? 4 : 2));
+    const bool v = c.H >= (c.dtype == EP_F32 ? 4 : 8);
     switch (c.dtype) {
         case EP_F32: return v ? combine_go<EP_F32, 4>(c, y, stream) : combine_go<EP_F32, 1>(c, y, stream);
         case EP_BF16: return v ? combine_go<EP_BF16, 8>(c, y, stream) : combine_go<EP_BF16, 1>(c, y, stream);
@@ -493,7 +495,7 @@ hipError_t launch_combine_tokens(const CombineArgs& c, void* y, hipStream_t stre
 
 hipError_t launch_combine_tokens_grad(const CombineArgs& c, const void* dy, void* d_ys, float* d_w, hipStream_t stream) {
     if (c.T <= 0) return hipSuccess;
-    const bool v = aligned16(c.ys, dy, d_ys, c.H * (c.dtype == EP_F32 ? 4 : 2));
+    const bool v = c.H >= (c.dtype == EP_F32 ? 4 : 8);
     switch (c.dtype) {
         case EP_F32: return v ? grad_go<EP_F32, 4>(c, dy, d_ys, d_w, stream) : grad_go<EP_F32, 1>(c, dy, d_ys, d_w, stream);
         case EP_BF16: return v ? grad_go<EP_BF16, 8>(c, dy, d_ys, d_w, stream) : grad_go<EP_BF16, 1>(c, dy, d_ys, d_w, stream);

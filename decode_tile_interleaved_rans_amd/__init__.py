@@ -41,7 +41,8 @@ EXPORTS = ["ep_compress", "ep_free", "ep_stream_info", "ep_upload", "ep_handle_i
            "ep_release", "ep_last_error", "ep_version", "ep_linear_forward_fp8", "ep_quantize_rows_fp8",
            "ep_gemm_fp8", "ep_compress_device", "ep_linear_forward_noalloc", "ep_linear_forward_many",
            "ep_linear_forward_fp8_many", "ep_quantize_rows_int8", "ep_gemm_int8", "ep_gemm_int8_experts",
-           "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_sort_tokens_scratch", "ep_sort_tokens",
+           "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_linear_forward_experts",
+           "ep_sort_tokens_scratch", "ep_sort_tokens",
            "ep_combine_tokens", "ep_combine_tokens_grad"]
 
 
@@ -103,6 +104,7 @@ def lib() -> C.CDLL:
         L.ep_gemm_int8_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_pad_rows_int8.argtypes = [vp, i64, i64, vp, i64, vp]
         L.ep_linear_forward_int8.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.ep_linear_forward_experts.argtypes = [vp, C.c_int, C.c_int, vp, vp, vp, vp, vp]
         L.ep_sort_tokens_scratch.argtypes = [i64, C.c_int, C.c_int, C.POINTER(sz)]
         L.ep_sort_tokens.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp]
         L.ep_combine_tokens.argtypes = [vp, C.c_int, vp, vp, i64, C.c_int, i64, i64, vp, vp]
@@ -449,8 +451,8 @@ def _need_rows(t, name: str, dtypes):
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
     rows, cols = t.shape
-    apart = t.stride(0) if rows > 1 else cols
-    if not t.is_cuda or (cols > 1 and t.stride(1) != 1) or apart < cols:
+    apart = t.stride(0) if rows > 1 and cols > 0 else cols
+    if not t.is_cuda or (t.numel() > 0 and ((cols > 1 and t.stride(1) != 1) or apart < cols)):
         raise ValueError(f"{name} must be on the GPU, its elements consecutive within a row and its rows disjoint")
     if t.device.index != _torch().cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{_torch().cuda.current_device()}")
@@ -704,8 +706,9 @@ class CompressedLinear:
     out_features <= 4096; else the library's own).
     compute="fp8": the weight is decoded to FP8 E4M3 with its row scales and the activations are
     quantized per row; the codes meet in the FP8 MFMA, fused in the same cases, else on slices.
-    compute="int8": the weight is decoded slice by slice to INT8 with its row scales, the activations
-    are quantized per row (quantize_rows_int8), and the codes meet in the INT8 MFMA (gemm_int8).
+    compute="int8": the weight is decoded to INT8 with its row scales and the activations are quantized
+    per row (quantize_rows_int8); the codes meet in the INT8 MFMA, fused for up to 64 rows of a
+    row-layout stream, else on slices (gemm_int8); the sums are exact either way.
 
     The forward takes BF16 activations. Other dtypes are refused unless cast=True is passed, so a
     precision change is never silent ("Diagnose compression failures in the correct order")."""
@@ -819,3 +822,44 @@ def linear_forward_many(layers, x, stream=None):
                "ep_linear_forward_fp8_many" if fp8 else "ep_linear_forward_many")
     _used_on(s, other, x2, *[l.bias for l in layers])
     return [y.reshape(*shp[:-1], l.out_features) for y, l in zip(ys, layers)]
+
+
+def linear_forward_experts(layers, x, expert_ids, weights=None, stream=None):
+    """A mixture-of-experts layer of compressed experts: y[t] = sum over j of weights[t, j] layer_e(x[t]), e =
+    expert_ids[t, j], for CompressedLinear layers of one shape and compute mode; x: BF16 [T, in_features],
+    expert_ids: [T, k] int32 or int64 (a number outside 0 ... len(layers) - 1 drops the choice), weights:
+    fp32 [T, k] or None (ones). The tokens are sorted by expert (sort_tokens), each expert multiplies its
+    rows, the same bits as the layer's own forward of them, and the rows are summed back
+    (combine_tokens). Experts without tokens are not decoded, and up to 64 rows each share fused
+    launches, so the host reads the experts' row counts once: the call waits for the work queued on its
+    stream and cannot be captured into a graph. Differentiable in weights (a router over frozen experts);
+    x has to be detached, since a compressed layer has no gradient. On `stream` (default: the current
+    stream; another stream first waits for the current one)."""
+    torch = _torch()
+    layers = list(layers)
+    if not layers:
+        raise ValueError("linear_forward_experts needs at least one expert")
+    if any(l.compute != layers[0].compute or l.handle.shape != layers[0].handle.shape for l in layers):
+        raise ValueError("the experts must share their shape and compute mode")
+    N, K = layers[0].handle.shape
+    if x.dim() != 2 or x.shape[1] != K or x.dtype != torch.bfloat16:
+        raise ValueError(f"x must be a bfloat16 tensor of shape [tokens, {K}], got {x.dtype} {tuple(x.shape)}")
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("the compressed experts have no gradient in x; detach it")
+    biases = [l.bias for l in layers]
+    for b in biases:
+        if b is not None:
+            _need(b, "bias", torch.bfloat16, shape=(N,))
+    if stream is not None:
+        return _on_stream(stream, lambda: linear_forward_experts(layers, x, expert_ids, weights), x, expert_ids,
+                          weights, *biases)
+    n = len(layers)
+    rows, offsets, pos = sort_tokens(x, expert_ids, n)
+    offs = (C.c_int64 * (n + 1))(*offsets.tolist())
+    ys = torch.empty((rows.shape[0], N), dtype=torch.bfloat16, device=x.device)
+    hs = (C.c_void_p * n)(*[l.handle.ptr.value for l in layers])
+    bs = (C.c_void_p * n)(*[_ptr(b) for b in biases])
+    code = {"bf16": BF16, "fp8": F8E4M3, "int8": I8}[layers[0].compute]
+    _check(lib().ep_linear_forward_experts(hs, n, code, _ptr(rows), offs, bs, _ptr(ys), _current_raw()),
+           "ep_linear_forward_experts")
+    return combine_tokens(ys, pos, weights)

@@ -1074,6 +1074,27 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
                                        s);
             return e == hipSuccess ? EP_OK : hip_fail(e, "empty product launch");
         }
+        if (const ep::MatDesc d = desc_for(w, ep::CT_I8, nullptr, nullptr); ep::fused_many_fits(&d, 1, M)) {
+            // up to 64 activation rows in the row layout: every tile pair decoded straight into the
+            // INT8 container's codes as the B operand of the INT8 MFMA
+            // workspace: X codes [M][K] | X scales [M] | int32 partial sums
+            const int rows = (int)M, mt = ep::fused_rows_mt_of(&rows, 1);
+            const size_t o_xs = up((size_t)M * (size_t)K, 256), o_pt = up(o_xs + 4 * (size_t)M, 256);
+            WsLease ws;
+            if ((e = ws_acquire(dev, s, o_pt + ep::fused_rows_partial_bytes(d, mt), &ws)) != hipSuccess)
+                return hip_fail(e, "hipMalloc for the linear forward workspace");
+            uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+            const void* xq = ws8;
+            float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+            const float* cxs = xs;
+            float* part = reinterpret_cast<float*>(ws8 + o_pt);
+            const uint16_t* bias = static_cast<const uint16_t*>(dev_bias);
+            uint16_t* y = static_cast<uint16_t*>(dev_y);
+            e = ep::launch_quantize_rows_i8(dev_x, EP_BF16, (int)M, (int)K, K, reinterpret_cast<int8_t*>(ws8), xs, s);
+            if (e == hipSuccess) e = ep::launch_fused_rows(&d, 1, ep::CT_I8, &xq, &cxs, &rows, &part, &bias, &y, s);
+            if (e == hipSuccess) e = ws.queued();
+            return e == hipSuccess ? EP_OK : hip_fail(e, "fused INT8 decode + MFMA launch");
+        }
         const int tr = w->view.tile_rows;
         int64_t slice = (int64_t)(kSliceBytes / (size_t)K) / tr * tr;
         if (slice < tr) slice = tr;
@@ -1109,6 +1130,117 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
         }
         e = ws.queued();
         return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
+    });
+}
+
+ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dtype compute, const void* dev_x,
+                                    const int64_t* host_offsets, const void* const* dev_bias, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (count < 1 || count > ep::kRouteMaxExperts) return fail(EP_ERANGE, "the number of experts must be 1 ... 1024");
+        if (compute != EP_BF16 && compute != EP_F8E4M3 && compute != EP_I8)
+            return fail(EP_EUNSUPPORTED, "the compressed forward computes in BF16, F8E4M3 or I8");
+        if (!w || !host_offsets) return fail(EP_EINVAL, "null pointer");
+        // every expert checked before anything is queued
+        for (int i = 0; i < count; ++i) {
+            if (!w[i]) return fail(EP_EINVAL, "null handle at expert " + std::to_string(i));
+            if (ep_status st = on_its_device(w[i]); st != EP_OK) return st;
+            if (w[i]->view.mode != EP_MODE_LOSSY_E8) return fail(EP_EUNSUPPORTED, "the linear forward takes a lossy stream");
+            if (w[i]->view.cols != w[0]->view.cols || w[i]->view.rows != w[0]->view.rows)
+                return fail(EP_EINVAL, "the experts have different shapes");
+            if (host_offsets[i + 1] < host_offsets[i]) return fail(EP_EINVAL, "the offsets descend");
+        }
+        const int64_t N = w[0]->view.rows, K = w[0]->view.cols, R = host_offsets[count];
+        if (host_offsets[0] != 0) return fail(EP_EINVAL, "the offsets must start at 0");
+        if (R == 0 || N == 0) return EP_OK;
+        if (!dev_y || (K > 0 && !dev_x)) return fail(EP_EINVAL, "null pointer");
+        if (R > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "the rows and out_features must be below 2^31");
+        if (K % (compute == EP_BF16 ? 8 : 16)) return fail(EP_EINVAL, "in_features must be a multiple of 8 (16 in FP8 and INT8)");
+        if (compute == EP_I8 && K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131071: the int32 sums could overflow");
+        if (reinterpret_cast<uintptr_t>(dev_x) & 15) return fail(EP_EINVAL, "X must be 16-byte aligned");
+        hipStream_t s = static_cast<hipStream_t>(hip_stream);
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+        const int ct = (int)compute;
+        const uint16_t* x = static_cast<const uint16_t*>(dev_x);
+        uint16_t* y = static_cast<uint16_t*>(dev_y);
+        // experts of 1 to 64 rows in the row layout share fused launches: groups of one probability
+        // precision, at most kMaxGroup experts and kExpertPartials bytes of partial sums each
+        constexpr size_t kExpertPartials = 256u << 20;
+        std::vector<char> done((size_t)count, 0);
+        std::vector<std::vector<int>> groups;
+        std::vector<ep::MatDesc> ds((size_t)count);
+        size_t part_bytes = 0;
+        for (int bits = 10; bits <= 12 && K > 0; ++bits) {
+            size_t bytes = 0;
+            bool open = false;
+            for (int i = 0; i < count; ++i) {
+                const int64_t M = host_offsets[i + 1] - host_offsets[i];
+                ds[i] = desc_for(w[i], ct, nullptr, nullptr);
+                if (M == 0 || ds[i].prob_bits != bits || !ep::fused_many_fits(&ds[i], 1, M)) continue;
+                const size_t need = up(ep::fused_rows_partial_bytes(ds[i], 4), 256);   // for the most M tiles
+                if (!open || groups.back().size() == ep::kMaxGroup || bytes + need > kExpertPartials) {
+                    groups.emplace_back();
+                    bytes = 0;
+                    open = true;
+                }
+                groups.back().push_back(i);
+                done[i] = 1;
+                bytes += need;
+                part_bytes = std::max(part_bytes, bytes);
+            }
+        }
+        if (!groups.empty()) {
+            // workspace: X codes [R][K] | X scales [R] (FP8, INT8) | a group's partial sums
+            const bool codes = compute != EP_BF16;
+            const size_t o_xs = codes ? up((size_t)R * (size_t)K, 256) : 0, o_pt = codes ? up(o_xs + 4 * (size_t)R, 256) : 0;
+            WsLease ws;
+            if ((e = ws_acquire(dev, s, o_pt + part_bytes, &ws)) != hipSuccess)
+                return hip_fail(e, "hipMalloc for the linear forward workspace");
+            uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+            float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+            if (compute == EP_I8)
+                e = ep::launch_quantize_rows_i8(x, EP_BF16, (int)R, (int)K, K, reinterpret_cast<int8_t*>(ws8), xs, s);
+            else if (codes)
+                e = ep::launch_quantize_rows_f8(x, (int)R, (int)K, (int)K, ws8, (int)K, xs, s);
+            if (e != hipSuccess) return hip_fail(e, "quantize launch");
+            for (const std::vector<int>& gr : groups) {
+                const int n = (int)gr.size();
+                std::vector<ep::MatDesc> gd;
+                std::vector<const void*> gx;
+                std::vector<const float*> gs;
+                std::vector<int> gm;
+                std::vector<float*> gp;
+                std::vector<const uint16_t*> gb;
+                std::vector<uint16_t*> gy;
+                size_t o = o_pt;
+                for (int i : gr) {
+                    const int64_t r0 = host_offsets[i];
+                    gd.push_back(ds[i]);
+                    gx.push_back(codes ? static_cast<const void*>(ws8 + (size_t)r0 * (size_t)K) : x + r0 * K);
+                    gs.push_back(xs + r0);
+                    gm.push_back((int)(host_offsets[i + 1] - r0));
+                    gp.push_back(reinterpret_cast<float*>(ws8 + o));
+                    gb.push_back(dev_bias ? static_cast<const uint16_t*>(dev_bias[i]) : nullptr);
+                    gy.push_back(y + r0 * N);
+                    o += up(ep::fused_rows_partial_bytes(ds[i], 4), 256);
+                }
+                e = ep::launch_fused_rows(gd.data(), n, ct, gx.data(), gs.data(), gm.data(), gp.data(), gb.data(), gy.data(), s);
+                if (e != hipSuccess) return hip_fail(e, "grouped expert decode + MFMA launch");
+            }
+            if ((e = ws.queued()) != hipSuccess) return hip_fail(e, "recording the workspace event");
+        }
+        // the others: each its own forward
+        for (int i = 0; i < count; ++i) {
+            const int64_t r0 = host_offsets[i], M = host_offsets[i + 1] - r0;
+            if (M == 0 || done[i]) continue;
+            const void* b = dev_bias ? dev_bias[i] : nullptr;
+            const ep_status st = compute == EP_BF16     ? linear_forward(w[i], x + r0 * K, M, b, y + r0 * N, s, false)
+                                 : compute == EP_F8E4M3 ? ep_linear_forward_fp8(w[i], x + r0 * K, M, b, y + r0 * N, hip_stream)
+                                                        : ep_linear_forward_int8(w[i], x + r0 * K, M, b, y + r0 * N, hip_stream);
+            if (st != EP_OK) return st;
+        }
+        return EP_OK;
     });
 }
 

@@ -62,4 +62,16 @@ hipError_t launch_fused_many_f8(const MatDesc* ms, int count, const uint8_t* xq,
 hipError_t launch_fused_f8(const MatDesc& m, const uint8_t* xq, const float* xs, int64_t M, float* part,
                            const uint16_t* bias, uint16_t* y, hipStream_t stream);
 
+// The fused decode + MFMA product of up to kMaxGroup row-layout matrices that take activation rows of
+// their own (1 to 64 each), in one decode launch and one finishing launch: matrix i multiplies x[i]
+// (ct CT_BF16: bf16 [M_i][cols]; CT_F8E4M3, CT_I8: codes [M_i][cols] with scales xs[i] [M_i], cols % 16 ==
+// 0), writes its partial sums to parts[i] (fused_rows_partial_bytes with mt = fused_rows_mt_of of the group)
+// and Y_i (+ bias[i], bf16 or null) to y[i] (bf16 [M_i][rows_i]). BF16 and FP8: the same bits as launch_fused
+// and launch_fused_f8 of that matrix alone. INT8 (int32 partials, exact): the same bits as the decoded
+// codes multiplied by launch_gemm_i8. One probability precision; each matrix fused_many_fits.
+int fused_rows_mt_of(const int* M, int count);
+size_t fused_rows_partial_bytes(const MatDesc& m, int mt);
+hipError_t launch_fused_rows(const MatDesc* ms, int count, int ct, const void* const* x, const float* const* xs, const int* M,
+                             float* const* parts, const uint16_t* const* bias, uint16_t* const* y, hipStream_t stream);
+
 }  // namespace ep

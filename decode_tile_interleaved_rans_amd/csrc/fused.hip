@@ -10,6 +10,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "decode_core.h"
 #include "fused.h"
@@ -298,8 +299,9 @@ __global__ __launch_bounds__(64 * WAVES) void decode_mfma_f8(GroupArgs g) {
 // so the partials and the finishing sums are the same. (Loading the activations of 2 or 4 steps
 // at once, so that whole 128-byte lines are requested together, measured no faster.)
 typedef long i64_t;
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 
-template <int N, int MT, bool F8>
+template <int N, int MT, int CT>
 __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Tile& t, uint64_t pair,
                                           __amdgpu_buffer_rsrc_t rs, __amdgpu_buffer_rsrc_t rx) {
     const float h = M.step * 0.5f;
@@ -307,16 +309,18 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
     const uint32_t f0 = coset[0].x, f1 = coset[1].x;
     const int lo0 = (int32_t)coset[0].y >> 16;
     PairRows P;
-    begin_pair<F8 ? CT_F8E4M3 : CT_BF16, true>(M, rs, pair, true, t, P);
+    begin_pair<CT, true>(M, rs, pair, true, t, P);
+    constexpr bool F8 = CT == CT_F8E4M3, I8 = CT == CT_I8;
+    const bool divide = I8 && __any(P.k_l != 1u);   // INT8 rows whose largest |q| is at most 127 store q itself
     const float alpha = h * P.sc_l;                 // the lane's row (scale 0 past the matrix)
     const int lane = threadIdx.x & 63, qg = lane >> 4, n = lane & 15;
     const uint32_t K = M.cols;
     const uint32_t c0 = (uint32_t)(pair % M.pairs_c) * 512u + (uint32_t)(qg >> 1) * 256u + 8u * (uint32_t)(qg & 1);
     const uint32_t keep = t.valid ? 0xFFFFFFFFu : 0u;
-    constexpr uint32_t kEs = F8 ? 1u : 2u;          // activation bytes per element
-    f32x4_t acc[MT];
+    constexpr uint32_t kEs = F8 || I8 ? 1u : 2u;          // activation bytes per element
+    typename std::conditional<I8, i32x4_t, f32x4_t>::type acc[MT];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) acc[mt] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int mt = 0; mt < MT; ++mt) acc[mt] = {0, 0, 0, 0};
     for (int s = 0; s < 16; ++s) {
         const uint32_t kc = c0 + 16u * (uint32_t)s;
         // columns past K read as zero (K % 8 == 0: a block is wholly inside or outside), and so do
@@ -326,7 +330,7 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
             const uint32_t off = (((uint32_t)(16 * mt + n) * K + kc) * kEs) | oob;
-            if constexpr (F8) {
+            if constexpr (F8 || I8) {
                 const uint2 v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rx, off, 0, 0));
                 ax[mt] = make_uint4(v.x, v.y, 0u, 0u);
             } else {
@@ -338,19 +342,21 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
         refill(t);
         const uint32_t base = (uint32_t)b << N;
         const uint2* ent_b = T.ent + b * 256;
-        float q[8];
+        float q[8];                                 // INT8: the coordinate's bit pattern (int32)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint2 e;
             const uint2* ent_j = ent_b + 2 * j * 256;
             rans_steps<N, 1>(&t, (2 * j) << N, &base, &ent_j, &e);
             refill_all<1>(&t);
-            q[j] = hi16_to_f32(e.y);
+            if constexpr (I8) q[j] = __int_as_float((int32_t)e.y >> 16);
+            else q[j] = hi16_to_f32(e.y);
             if ((M.esc_tables >> (2 * j)) & 3u) {
                 const bool esc = (int32_t)e.x < 0;
                 if (__ballot(esc)) {
                     const uint32_t w = take_words(t, esc);
-                    if (esc) q[j] = (float)(int32_t)(int16_t)(2 * (int32_t)(int16_t)w + b);
+                    const int32_t v = (int32_t)(int16_t)(2 * (int32_t)(int16_t)w + b);
+                    if (esc) q[j] = I8 ? __int_as_float(v) : (float)v;
                 }
             }
         }
@@ -370,6 +376,29 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
             for (int mt = 0; mt < MT; ++mt)
                 acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(
                     __builtin_bit_cast(i64_t, make_uint2(ax[mt].x, ax[mt].y)), bop, acc[mt], 0, 0, 0);
+        } else if constexpr (I8) {
+            // the INT8 container's values (round-half-away(q / k), as the decode kernel stores them)
+            int32_t v[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __float_as_int(q[j]);
+            if (divide) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint32_t m = (uint32_t)(v[j] < 0 ? -v[j] : v[j]);
+                    const int32_t d = (int32_t)__umulhi(2u * m + P.k_l, P.magic_l);
+                    v[j] = P.k_l == 1u ? v[j] : v[j] < 0 ? -d : d;
+                }
+            }
+            uint32_t bw[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)             // the low bytes of four values, in order
+                bw[i] = (__builtin_amdgcn_perm((uint32_t)v[4 * i + 1], (uint32_t)v[4 * i], 0x0c0c0400u) |
+                         __builtin_amdgcn_perm((uint32_t)v[4 * i + 3], (uint32_t)v[4 * i + 2], 0x04000c0cu)) & keep;
+            const i64_t bop = __builtin_bit_cast(i64_t, make_uint2(bw[0], bw[1]));
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+                acc[mt] = __builtin_amdgcn_mfma_i32_16x16x32_i8(__builtin_bit_cast(i64_t, make_uint2(ax[mt].x, ax[mt].y)), bop,
+                                                                acc[mt], 0, 0, 0);
         } else {
             uint4 bw;
             bw.x = pack_bf16(q[0] * alpha, q[1] * alpha) & keep;
@@ -383,14 +412,14 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
         }
     }
     end_tile(t);
-    // partials [pair][mt][q][n][i] (fp32): 1 KiB per M tile, one 16-byte store per lane
+    // partials [pair][mt][q][n][i] (fp32; INT8: int32): 1 KiB per M tile, one 16-byte store per lane
     float* part = static_cast<float*>(M.out) + pair * (uint64_t)(MT * 256);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
-        *reinterpret_cast<f32x4_t*>(part + ((mt * 4 + qg) * 16 + n) * 4) = acc[mt];
+        *reinterpret_cast<f32x4_t*>(part + ((mt * 4 + qg) * 16 + n) * 4) = __builtin_bit_cast(f32x4_t, acc[mt]);
 }
 
-template <int N, int MT, bool F8>
+template <int N, int MT, int CT>
 __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows(GroupArgs g) {
     extern __shared__ __align__(16) uint8_t smem[];
     const MatDesc& M = g.m[0];
@@ -409,7 +438,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows(GroupArgs g) {
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const __amdgpu_buffer_rsrc_t rs = payload_rsrc(M);
     const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<uint16_t*>(M.gemv_x), 0, (int)((size_t)M.gemv_m * M.cols * (F8 ? 1 : 2)), 0x00020000);
+        const_cast<uint16_t*>(M.gemv_x), 0, (int)((size_t)M.gemv_m * M.cols * (CT == CT_BF16 ? 2 : 1)), 0x00020000);
     // pairs in column-major order: the 16 waves of a block take the same 512 columns of 16
     // consecutive tile rows, so their activation loads are the same lines at about the same time
     // and the L1 serves them once (in row-major order each wave had its own columns, and with four
@@ -417,7 +446,7 @@ __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows(GroupArgs g) {
     const uint32_t tiles_r = (M.rows + 15u) / 16u;
     for (uint64_t p = p0 + (uint64_t)wave; p < p1; p += kWaves) {
         const uint32_t pc = (uint32_t)p / tiles_r, tr = (uint32_t)p % tiles_r;
-        rows_pair<N, MT, F8>(M, T, t, (uint64_t)tr * M.pairs_c + pc, rs, rx);
+        rows_pair<N, MT, CT>(M, T, t, (uint64_t)tr * M.pairs_c + pc, rs, rx);
     }
     if (t.err) atomicOr(M.err, t.err);
 }
@@ -471,6 +500,46 @@ __global__ __launch_bounds__(256) void fused_finish(const float* part, const uin
 }
 
 
+// The finishing sums of several matrices that took rows of their own (blockIdx.y: the matrix), as
+// fused_finish and fused_finish_f8 form them; INT8: the int32 partials, whose sum is exact, times the
+// row's scale (alpha_r k_r, as the decode kernel stores it) and the token's.
+struct FinishMany {
+    struct One {
+        const float* part;
+        const float* sx;            // scales of its activation rows (FP8, INT8)
+        const float* row_scale;
+        const uint16_t* row_qmax;
+        const uint16_t* bias;
+        uint16_t* y;
+        float step;
+        int Mrows, Nrows, pairs_c;
+    } m[kMaxGroup];
+};
+
+template <int MT, int CT>
+__global__ __launch_bounds__(256) void fused_finish_many(FinishMany f) {
+    const FinishMany::One& o = f.m[blockIdx.y];
+    const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (e >= (int64_t)o.Mrows * o.Nrows) return;
+    const int m = (int)(e / o.Nrows), col = (int)(e % o.Nrows);
+    const int tr = col >> 4, n = col & 15;
+    const int mt = m >> 4, qg = (m >> 2) & 3, i = m & 3;
+    const float* p = o.part + (uint64_t)tr * o.pairs_c * (MT * 256) + ((mt * 4 + qg) * 16 + n) * 4 + i;
+    float v;
+    if constexpr (CT == CT_I8) {
+        int32_t sum = 0;
+        for (int pc = 0; pc < o.pairs_c; ++pc) sum += __float_as_int(p[(uint64_t)pc * (MT * 256)]);
+        const uint32_t qm = o.row_qmax[col], k = qm > 127u ? (qm + 126u) / 127u : 1u;
+        const float alpha = (o.step * 0.5f) * o.row_scale[col];
+        v = (float)sum * (alpha * (float)k) * o.sx[m];
+    } else {
+        v = sum_partials<MT>(p, o.pairs_c);
+        if constexpr (CT == CT_F8E4M3) v = v * o.row_scale[col] * o.sx[m];
+    }
+    if (o.bias) v += __uint_as_float((uint32_t)o.bias[col] << 16);
+    o.y[e] = (uint16_t)(__builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{v, 0.0f}, bf16x2)) & 0xFFFFu);
+}
+
 template <int N, int MT>
 hipError_t launch_mfma_n(const GroupArgs& g, uint64_t blocks, hipStream_t stream) {
     constexpr int W = N == 12 ? 8 : 12;
@@ -521,7 +590,7 @@ hipError_t launch_mfma_mt(const GroupArgs& g, uint64_t blocks, hipStream_t strea
 // pairs than the CU's wave slots, or one whose last round of pairs is mostly empty, shares its
 // rounds with the others instead of ending on a pair's latency. Same probability precision N and
 // input width for all matrices.
-template <int N, int MT, bool F8>
+template <int N, int MT, int CT>
 __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows_many(GroupArgs g) {
     extern __shared__ __align__(16) uint8_t smem[];
     if ((uint32_t)(size_t)(lds_u8*)smem != 0u) {
@@ -545,65 +614,65 @@ __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows_many(GroupArgs g
         init_lane(t, smem + lds_table_bytes(M.n_tables, M.prob_bits, true), 0);
         const __amdgpu_buffer_rsrc_t rs = payload_rsrc(M);
         const __amdgpu_buffer_rsrc_t rx = __builtin_amdgcn_make_buffer_rsrc(
-            const_cast<uint16_t*>(M.gemv_x), 0, (int)((size_t)M.gemv_m * M.cols * (F8 ? 1 : 2)), 0x00020000);
+            const_cast<uint16_t*>(M.gemv_x), 0, (int)((size_t)M.gemv_m * M.cols * (CT == CT_BF16 ? 2 : 1)), 0x00020000);
         const uint32_t tiles_r = (M.rows + 15u) / 16u;          // column-major pair order, as above
         for (uint64_t p = p0 + (uint64_t)wave; p < p1; p += kWaves) {
             const uint32_t pc = (uint32_t)p / tiles_r, tr = (uint32_t)p % tiles_r;
-            rows_pair<N, MT, F8>(M, T, t, (uint64_t)tr * M.pairs_c + pc, rs, rx);
+            rows_pair<N, MT, CT>(M, T, t, (uint64_t)tr * M.pairs_c + pc, rs, rx);
         }
         if (t.err) atomicOr(M.err, t.err);
     }
 }
 
-template <int N, int MT, bool F8>
+template <int N, int MT, int CT>
 hipError_t launch_rows_n(const GroupArgs& g, uint64_t blocks, hipStream_t stream) {
     const MatDesc& m = g.m[0];
     const size_t lds = lds_table_bytes(m.n_tables, m.prob_bits, true) + (size_t)kWaves * 2 * kRingBytes;
-    const void* k = reinterpret_cast<const void*>(decode_mfma_rows<N, MT, F8>);
+    const void* k = reinterpret_cast<const void*>(decode_mfma_rows<N, MT, CT>);
     hipError_t e = allow_lds(k);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((decode_mfma_rows<N, MT, F8>), dim3((unsigned)blocks), dim3(64 * kWaves), lds, stream, g);
+    hipLaunchKernelGGL((decode_mfma_rows<N, MT, CT>), dim3((unsigned)blocks), dim3(64 * kWaves), lds, stream, g);
     return hipGetLastError();
 }
 
-template <int MT, bool F8>
+template <int MT, int CT>
 hipError_t launch_rows_mt(const GroupArgs& g, uint64_t blocks, hipStream_t stream) {
     switch (g.m[0].prob_bits) {
-        case 10: return launch_rows_n<10, MT, F8>(g, blocks, stream);
-        case 11: return launch_rows_n<11, MT, F8>(g, blocks, stream);
-        default: return launch_rows_n<12, MT, F8>(g, blocks, stream);
+        case 10: return launch_rows_n<10, MT, CT>(g, blocks, stream);
+        case 11: return launch_rows_n<11, MT, CT>(g, blocks, stream);
+        default: return launch_rows_n<12, MT, CT>(g, blocks, stream);
     }
 }
 
 // 16-row M tiles the kernel keeps per wave: 1 for the transposing kernel, up to 4 in the row layout.
 int fused_mt(const MatDesc& m, int64_t M) { return m.layout == 0 || M <= 16 ? 1 : M <= 32 ? 2 : 4; }
 
-template <bool F8>
+template <int CT>
 hipError_t launch_rows(const GroupArgs& g, int mt, uint64_t blocks, hipStream_t stream) {
     switch (mt) {
-        case 1: return launch_rows_mt<1, F8>(g, blocks, stream);
-        case 2: return launch_rows_mt<2, F8>(g, blocks, stream);
-        default: return launch_rows_mt<4, F8>(g, blocks, stream);
+        case 1: return launch_rows_mt<1, CT>(g, blocks, stream);
+        case 2: return launch_rows_mt<2, CT>(g, blocks, stream);
+        default: return launch_rows_mt<4, CT>(g, blocks, stream);
     }
 }
 
-template <int N, int MT, bool F8>
+template <int N, int MT, int CT>
 hipError_t launch_rows_many_n(const GroupArgs& g, uint64_t blocks, hipStream_t stream) {
     const MatDesc& m = g.m[0];
     const size_t lds = lds_table_bytes(m.n_tables, m.prob_bits, true) + (size_t)kWaves * 2 * kRingBytes;
-    const void* k = reinterpret_cast<const void*>(decode_mfma_rows_many<N, MT, F8>);
+    const void* k = reinterpret_cast<const void*>(decode_mfma_rows_many<N, MT, CT>);
     hipError_t e = allow_lds(k);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((decode_mfma_rows_many<N, MT, F8>), dim3((unsigned)blocks), dim3(64 * kWaves), lds, stream, g);
+    hipLaunchKernelGGL((decode_mfma_rows_many<N, MT, CT>), dim3((unsigned)blocks), dim3(64 * kWaves), lds, stream, g);
     return hipGetLastError();
 }
 
-template <int MT, bool F8>
+template <int MT, int CT>
 hipError_t launch_rows_many_mt(const GroupArgs& g, uint64_t blocks, hipStream_t stream) {
     switch (g.m[0].prob_bits) {
-        case 10: return launch_rows_many_n<10, MT, F8>(g, blocks, stream);
-        case 11: return launch_rows_many_n<11, MT, F8>(g, blocks, stream);
-        default: return launch_rows_many_n<12, MT, F8>(g, blocks, stream);
+        case 10: return launch_rows_many_n<10, MT, CT>(g, blocks, stream);
+        case 11: return launch_rows_many_n<11, MT, CT>(g, blocks, stream);
+        default: return launch_rows_many_n<12, MT, CT>(g, blocks, stream);
     }
 }
 
@@ -658,7 +727,7 @@ hipError_t launch_fused(const MatDesc& m, const uint16_t* x, int64_t M, float* p
     g.block_cost = (total + blocks - 1) / blocks;
     const uint64_t used = (total + g.block_cost - 1) / g.block_cost;
     const int mt = fused_mt(m, M);
-    hipError_t e = m.layout ? launch_rows<false>(g, mt, used, stream) : launch_mfma_mt<1>(g, used, stream);
+    hipError_t e = m.layout ? launch_rows<CT_BF16>(g, mt, used, stream) : launch_mfma_mt<1>(g, used, stream);
     if (e != hipSuccess) return e;
     return launch_finish(part, nullptr, nullptr, bias, y, (int)M, (int)m.rows, (int)m.pairs_c, mt, stream);
 }
@@ -682,7 +751,7 @@ hipError_t launch_fused_f8(const MatDesc& m, const uint8_t* xq, const float* xs,
     g.block_cost = (total + blocks - 1) / blocks;
     const uint64_t used = (total + g.block_cost - 1) / g.block_cost;
     const int mt = fused_mt(m, M);
-    hipError_t e = m.layout ? launch_rows<true>(g, mt, used, stream) : launch_mfma_f8_mt<1>(g, used, stream);
+    hipError_t e = m.layout ? launch_rows<CT_F8E4M3>(g, mt, used, stream) : launch_mfma_f8_mt<1>(g, used, stream);
     if (e != hipSuccess) return e;
     return launch_finish(part, xs, m.row_scale, bias, y, (int)M, (int)m.rows, (int)m.pairs_c, mt, stream);
 }
@@ -698,10 +767,11 @@ bool fused_many_fits(const MatDesc* ms, int count, int64_t M) {
 
 namespace {
 // launch_fused_many and launch_fused_many_f8: x the BF16 activations, or the E4M3 codes with their
-// row scales xs (F8)
-template <bool F8>
+// row scales xs
+template <int CT>
 hipError_t fused_many(const MatDesc* ms, int count, const void* x, const float* xs, int64_t M, float* const* parts,
                       const uint16_t* const* bias, uint16_t* const* y, hipStream_t stream) {
+    constexpr bool F8 = CT == CT_F8E4M3;
     if (!fused_many_fits(ms, count, M) || (F8 && (ms[0].cols & 15))) return hipErrorInvalidValue;
     GroupArgs g{};
     g.count = count;
@@ -722,9 +792,9 @@ hipError_t fused_many(const MatDesc* ms, int count, const void* x, const float* 
         const uint64_t used = (total + g.block_cost - 1) / g.block_cost;
         hipError_t e;
         switch (mt) {
-            case 1: e = launch_rows_many_mt<1, F8>(g, used, stream); break;
-            case 2: e = launch_rows_many_mt<2, F8>(g, used, stream); break;
-            default: e = launch_rows_many_mt<4, F8>(g, used, stream); break;
+            case 1: e = launch_rows_many_mt<1, CT>(g, used, stream); break;
+            case 2: e = launch_rows_many_mt<2, CT>(g, used, stream); break;
+            default: e = launch_rows_many_mt<4, CT>(g, used, stream); break;
         }
         if (e != hipSuccess) return e;
     }
@@ -740,12 +810,78 @@ hipError_t fused_many(const MatDesc* ms, int count, const void* x, const float* 
 
 hipError_t launch_fused_many(const MatDesc* ms, int count, const uint16_t* x, int64_t M, float* const* parts,
                              const uint16_t* const* bias, uint16_t* const* y, hipStream_t stream) {
-    return fused_many<false>(ms, count, x, nullptr, M, parts, bias, y, stream);
+    return fused_many<CT_BF16>(ms, count, x, nullptr, M, parts, bias, y, stream);
 }
 
 hipError_t launch_fused_many_f8(const MatDesc* ms, int count, const uint8_t* xq, const float* xs, int64_t M,
                                 float* const* parts, const uint16_t* const* bias, uint16_t* const* y,
                                 hipStream_t stream) {
-    return fused_many<true>(ms, count, xq, xs, M, parts, bias, y, stream);
+    return fused_many<CT_F8E4M3>(ms, count, xq, xs, M, parts, bias, y, stream);
 }
+
+namespace {
+template <int MT, int CT>
+hipError_t fused_rows_mt(const GroupArgs& g, const FinishMany& f, uint64_t blocks, int64_t most, hipStream_t stream) {
+    hipError_t e = blocks ? launch_rows_many_mt<MT, CT>(g, blocks, stream) : hipSuccess;
+    if (e != hipSuccess || most == 0) return e;
+    hipLaunchKernelGGL((fused_finish_many<MT, CT>), dim3((unsigned)((most + 255) / 256), (unsigned)g.count), dim3(256), 0, stream, f);
+    return hipGetLastError();
+}
+
+template <int CT>
+hipError_t fused_rows(const MatDesc* ms, int count, const void* const* x, const float* const* xs, const int* M, int mt,
+                      float* const* parts, const uint16_t* const* bias, uint16_t* const* y, hipStream_t stream) {
+    GroupArgs g{};
+    FinishMany f{};
+    g.count = count;
+    uint64_t total = 0;
+    int64_t most = 0;
+    for (int i = 0; i < count; ++i) {
+        g.m[i] = ms[i];
+        g.m[i].gemv_x = static_cast<const uint16_t*>(x[i]);
+        g.m[i].gemv_m = (uint8_t)M[i];
+        g.m[i].out = parts[i];
+        g.cost_start[i] = total;
+        total += (uint64_t)((ms[i].rows + ms[i].tile_rows - 1) / ms[i].tile_rows) * ms[i].pairs_c * ms[i].pair_cost;
+        f.m[i] = {parts[i], CT == CT_BF16 ? nullptr : xs[i], ms[i].row_scale, ms[i].row_qmax, bias[i], y[i], ms[i].step,
+                  M[i], (int)ms[i].rows, (int)ms[i].pairs_c};
+        most = std::max(most, (int64_t)M[i] * ms[i].rows);
+    }
+    g.cost_start[count] = total;
+    const uint64_t cus = (uint64_t)device_cus();
+    g.block_cost = total ? (total + cus - 1) / cus : 1;
+    const uint64_t used = (total + g.block_cost - 1) / g.block_cost;
+    switch (mt) {
+        case 1: return fused_rows_mt<1, CT>(g, f, used, most, stream);
+        case 2: return fused_rows_mt<2, CT>(g, f, used, most, stream);
+        default: return fused_rows_mt<4, CT>(g, f, used, most, stream);
+    }
+}
+}  // namespace
+
+int fused_rows_mt_of(const int* M, int count) {
+    int most = 1;
+    for (int i = 0; i < count; ++i) most = std::max(most, M[i]);
+    return most <= 16 ? 1 : most <= 32 ? 2 : 4;
+}
+
+size_t fused_rows_partial_bytes(const MatDesc& m, int mt) {
+    return (size_t)((m.rows + m.tile_rows - 1) / m.tile_rows) * m.pairs_c * (size_t)mt * 256 * sizeof(float);
+}
+
+hipError_t launch_fused_rows(const MatDesc* ms, int count, int ct, const void* const* x, const float* const* xs, const int* M,
+                             float* const* parts, const uint16_t* const* bias, uint16_t* const* y, hipStream_t stream) {
+    for (int i = 0; i < count; ++i)
+        if (!fused_many_fits(&ms[i], 1, M[i]) || ms[i].prob_bits != ms[0].prob_bits || (ct != CT_BF16 && (ms[i].cols & 15)))
+            return hipErrorInvalidValue;
+    if (count < 1 || count > kMaxGroup) return hipErrorInvalidValue;
+    const int mt = fused_rows_mt_of(M, count);
+    switch (ct) {
+        case CT_BF16: return fused_rows<CT_BF16>(ms, count, x, xs, M, mt, parts, bias, y, stream);
+        case CT_F8E4M3: return fused_rows<CT_F8E4M3>(ms, count, x, xs, M, mt, parts, bias, y, stream);
+        case CT_I8: return fused_rows<CT_I8>(ms, count, x, xs, M, mt, parts, bias, y, stream);
+        default: return hipErrorInvalidValue;
+    }
+}
+
 }  // namespace ep

@@ -382,9 +382,11 @@ ep_status ep_gemm_int8_experts(const int8_t* dev_xq, const float* dev_xs, const 
 ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_t* dev_dst, int64_t ld, void* hip_stream);
 
 /* INT8 variant of ep_linear_forward: Y = diag(xs) Xq Wq^T diag(ws) (+ bias), BF16 output. The weight is
- * decoded into the INT8 container with its per-row scales, slice by slice in the workspace as in
- * ep_linear_forward, the activations are quantized per row as ep_quantize_rows_int8 does, and both meet
- * in ep_gemm_int8's kernels.
+ * decoded into the INT8 container with its per-row scales, the activations are quantized per row as
+ * ep_quantize_rows_int8 does. For M <= 64 on row-layout streams the codes go straight into the INT8
+ * MFMA's B operand (fused, as in ep_linear_forward); otherwise the weight is decoded slice by slice into
+ * the workspace and multiplied by ep_gemm_int8's kernels. The sums are exact: both ways give the same
+ * bits.
  * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates",
  * Abstract (decoding fused into the computation that uses the weight, the INT8 container); "EntroPack
  * PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one linear layer
@@ -395,6 +397,22 @@ ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_
  * hip_stream. */
 ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t M, const void* dev_bias, void* dev_y,
                                  void* hip_stream);
+
+/* Compressed expert layers: expert e (handle w[e], all of one shape [N][K]) multiplies the rows offsets[e]
+ * ... offsets[e + 1] - 1 of X (ep_sort_tokens' order), each row of Y the same bits as the expert's own
+ * forward of those rows (ep_linear_forward, ep_linear_forward_fp8 or ep_linear_forward_int8 by compute:
+ * EP_BF16, EP_F8E4M3 or EP_I8; EP_EUNSUPPORTED otherwise). Experts with 1 to 64 rows whose streams are in the
+ * row layout share one fused decode + MFMA launch per 32 of them, cost-balanced, and one finishing
+ * launch; experts without rows are not decoded; the others run their own forward.
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
+ * linear layer before a whole model" (compressed layers inside a model's forward). Grouping the experts
+ * of a layer is this library's scheduling, not a step of the method.
+ *   w: count handles (1 ... 1024, EP_ERANGE otherwise); dev_x: [R][K] bf16, 16-byte aligned; host_offsets:
+ * count + 1 host integers, ascending from 0 (EP_EINVAL otherwise), R = the last; dev_bias: NULL or count
+ * pointers (each [N] bf16 or NULL); dev_y: [R][N] bf16. K % 8 == 0, K % 16 == 0 in FP8 and INT8 (EP_EINVAL).
+ * Workspace rules of ep_linear_forward. Asynchronous on hip_stream. */
+ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dtype compute, const void* dev_x,
+                                    const int64_t* host_offsets, const void* const* dev_bias, void* dev_y, void* hip_stream);
 
 /* Tokens sorted by the experts they chose (the input order of ep_gemm_int8_experts, and of compressed
  * layers run expert by expert).

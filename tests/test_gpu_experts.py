@@ -1,0 +1,146 @@
+"""Mixture-of-experts layers of compressed experts (linear_forward_experts, ep_linear_forward_experts): every
+row must have the bits of its expert's own forward, whether the expert shared a fused launch (up to 64
+rows in the row layout) or ran its own; the sums over a token's experts are checked in 64 bits, where fp32
+steps (k fused multiply-adds of 2^-24) and the BF16 rounding (half of finfo.eps) are allowed."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import decode_tile_interleaved_rans_amd as ep
+from decode_tile_interleaved_rans_amd import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+
+
+def gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def experts(E, N, K, compute, layout=lambda e: ep.ROW_LAYOUT, bits=lambda e: 11, target=4.5, bias=True):
+    out = []
+    for e in range(E):
+        s, _ = ep.compress(W.student_t(N, K, 100 + e), target, dtype=ep.BF16, layout=layout(e), prob_bits=bits(e))
+        b = torch.randn(N, generator=gen(e), device="cuda").to(torch.bfloat16) if bias and e % 3 else None
+        out.append(ep.CompressedLinear(s, b, compute))
+    return out
+
+
+def tokens(T, K, seed):
+    return torch.from_numpy(W.activations(T, K, seed).view(np.int16)).view(torch.bfloat16).cuda()
+
+
+def check(layers, x, ids, w):
+    y = ep.linear_forward_experts(layers, x, ids, w)
+    rows, off, pos = ep.sort_tokens(x, ids, len(layers))
+    off = off.tolist()
+    own = torch.zeros((rows.shape[0], layers[0].out_features), dtype=torch.bfloat16, device="cuda")
+    for e, l in enumerate(layers):
+        if off[e + 1] > off[e]:
+            own[off[e]:off[e + 1]] = l(rows[off[e]:off[e + 1]])
+    for l in layers:
+        l.handle.check()
+    assert torch.equal(y, ep.combine_tokens(own, pos, w))      # the same rows, bit for bit
+    p = pos.long()
+    w64 = torch.ones(p.shape, dtype=torch.float64, device="cuda") if w is None else w.double()
+    part = torch.where((p >= 0)[..., None], w64[..., None] * own.double()[p.clamp_min(0)], 0.0)
+    ref, mag = part.sum(1), part.abs().sum(1)
+    fp32 = p.shape[1] * U * mag
+    tol = fp32 + torch.finfo(torch.bfloat16).eps / 2 * (ref.abs() + fp32) + 2.0 ** -134
+    assert ((y.double() - ref).abs() <= tol).all()
+    return y
+
+
+@pytest.mark.parametrize("compute", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("T", [0, 1, 5, 40, 300])
+def test_experts_of_one_layer(T, compute):
+    E, k, N, K = 6, 2, 200, 1040
+    layers = experts(E, N, K, compute)
+    ids = torch.randint(0, E, (T, k), generator=gen(T), device="cuda")
+    if T > 4:
+        ids[3] = -1                                           # a token without experts
+        ids[:, 1] = torch.where(ids[:, 1] == 2, 7, ids[:, 1])  # an expert that the second choice drops
+    w = torch.rand((T, k), generator=gen(T + 1), device="cuda")
+    y = check(layers, tokens(T, K, T), ids, w)
+    if T > 4:
+        assert not y[3].any()
+    check(layers, tokens(T, K, T), ids.to(torch.int32), None)
+
+
+@pytest.mark.parametrize("compute", ["bf16", "fp8", "int8"])
+def test_mixed_layouts_precisions_and_group_sizes(compute):
+    # more experts than one launch takes, two probability precisions, some in layout 0, one with more
+    # than 64 rows, some without any
+    E, N, K, T = 70, 48, 528, 200
+    layers = experts(E, N, K, compute, layout=lambda e: 0 if e % 9 == 4 else ep.ROW_LAYOUT, bits=lambda e: 10 + e % 2)
+    ids = torch.randint(0, E, (T, 3), generator=gen(5), device="cuda")
+    ids[:90, 0] = 7
+    ids = torch.where(ids == 20, -1, ids)
+    check(layers, tokens(T, K, 3), ids, torch.rand((T, 3), generator=gen(6), device="cuda"))
+
+
+def test_wide_values_divide_in_int8():
+    # rows whose largest |q| passes 127 (large targets): the INT8 container divides them
+    E, N, K = 2, 64, 1024
+    layers = experts(E, N, K, "int8", target=9.0)
+    x = tokens(20, K, 9)
+    ids = torch.arange(20, device="cuda")[:, None] % E
+    check(layers, x, ids, None)
+    cq, cs = oracle.decompress(layers[0].stream, oracle.I8)
+    alone = layers[1]
+    dq, ds = alone.handle.decompress(torch.int8)
+    q, s = ep.quantize_rows_int8(x)
+    assert torch.equal(alone(x), ep.gemm_int8(q, s, dq, ds, alone.bias))
+    assert (cs > 0).all() and np.abs(cq.view(np.int8)).max() > 64
+
+
+def test_router_gradient():
+    E, k, N, K, T = 4, 2, 96, 512, 30
+    layers = experts(E, N, K, "int8")
+    x = tokens(T, K, 2)
+    ids = torch.randint(0, E, (T, k), generator=gen(1), device="cuda")
+    w = torch.rand((T, k), generator=gen(2), device="cuda").requires_grad_(True)
+    y = ep.linear_forward_experts(layers, x, ids, w)
+    dy = torch.randn((T, N), generator=gen(3), device="cuda").to(torch.bfloat16)
+    (dw,) = torch.autograd.grad(y, w, dy)
+    own = torch.stack([torch.stack([layers[int(e)](x[t:t + 1])[0] for e in ids[t]]) for t in range(T)]).double()
+    prod = own * dy.double()[:, None, :]
+    assert ((dw.double() - prod.sum(2)).abs() <= (N + 8) * U * prod.abs().sum(2)).all()
+    with pytest.raises(ValueError, match="detach"):
+        ep.linear_forward_experts(layers, x.clone().requires_grad_(True), ids, w)
+
+
+def test_other_stream():
+    layers = experts(3, 64, 512, "int8")
+    x, ids = tokens(50, 512, 4), torch.randint(0, 3, (50, 2), generator=gen(4), device="cuda")
+    want = ep.linear_forward_experts(layers, x, ids)
+    s = torch.cuda.Stream()
+    got = ep.linear_forward_experts(layers, x + 0, ids + 0, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+
+
+def test_refusals():
+    a, b = experts(1, 32, 512, "int8")[0], experts(1, 32, 256, "int8")[0]
+    x, ids = tokens(4, 512, 1), torch.zeros((4, 1), dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError, match="share"):
+        ep.linear_forward_experts([a, b], x, ids)
+    with pytest.raises(ValueError, match="share"):
+        ep.linear_forward_experts([a, ep.CompressedLinear(a.stream)], x, ids)
+    with pytest.raises(ValueError, match="bfloat16"):
+        ep.linear_forward_experts([a], x.float(), ids)
+    L, st = ep.lib(), C.c_void_p(torch.cuda.current_stream().cuda_stream)
+    hs = (C.c_void_p * 2)(a.handle.ptr.value, a.handle.ptr.value)
+    y = torch.zeros((4, 32), dtype=torch.bfloat16, device="cuda")
+    f = lambda offs, h=hs, px=x.data_ptr(): L.ep_linear_forward_experts(h, 2, ep.I8, px, (C.c_int64 * 3)(*offs), None,
+                                                                        y.data_ptr(), st)
+    assert f([0, 3, 2]) == -1 and f([1, 2, 3]) == -1 and f([0, 1, 2 ** 31]) == -4
+    assert f([0, 1, 2], px=x.data_ptr() + 2) == -1
+    assert f([0, 1, 2], h=(C.c_void_p * 2)(a.handle.ptr.value, b.handle.ptr.value)) == -1
+    assert f([0, 0, 0]) == 0 and f([0, 2, 4]) == 0

@@ -100,6 +100,19 @@ def test_combine():
     assert fw(T=0, R=0, ys=None, y=None, pos=None) == 0
 
 
+def test_compressed_experts():
+    f = ep.lib().ep_linear_forward_experts
+    hs, off = (C.c_void_p * 2)(), (C.c_int64 * 3)(0, 1, 2)
+    for n in (0, -1, 1025):
+        assert f(hs, n, ep.BF16, P, off, None, P, None) == ERANGE
+    assert f(hs, 2, ep.F16, P, off, None, P, None) == EUNSUPPORTED
+    assert f(hs, 2, ep.BF16, P, off, None, P, None) == EINVAL and b"null handle" in ep.lib().ep_last_error()
+    assert f(None, 2, ep.BF16, P, off, None, P, None) == EINVAL and f(hs, 2, ep.BF16, P, None, None, P, None) == EINVAL
+    assert ep.lib().ep_linear_forward_int8(None, P, 1, None, P, None) == EINVAL
+    with pytest.raises(ValueError, match="at least one"):
+        ep.linear_forward_experts([], torch.zeros(1), torch.zeros(1))
+
+
 def test_binding_refuses_tensors():
     i8 = lambda *s: torch.zeros(s, dtype=torch.int8)
     f32 = lambda *s: torch.zeros(s)

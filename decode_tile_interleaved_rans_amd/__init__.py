@@ -126,21 +126,29 @@ def _check(rc: int, call: str):
         raise EPError(rc, call, lib().ep_last_error().decode(errors="replace"))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 _DT_OF_TORCH = None
 
 
 def _dtype_code(t) -> int:
-    torch = _torch()
-    table = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: F8E4M3,
-             torch.int8: I8, torch.uint8: U8}
-    if t not in table:
+    global _DT_OF_TORCH
+    if _DT_OF_TORCH is None:
+        torch = _torch()
+        _DT_OF_TORCH = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: F8E4M3,
+                        torch.int8: I8, torch.uint8: U8}
+    if t not in _DT_OF_TORCH:
         raise ValueError(f"unsupported dtype {t}")
-    return table[t]
+    return _DT_OF_TORCH[t]
 
 
 def _torch_dtype(code: int):
@@ -461,6 +469,12 @@ def _need_rows(t, name: str, dtypes):
     return rows, cols, apart
 
 
+def _fits(t, dtype, shape, device: int) -> bool:
+    """Whether _need(t, ..., dtype, shape) passes, for `device` the current one: one quick test, so that a
+    small call does not spend its time on checks; where it fails, _need says why."""
+    return t.is_cuda and t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous()
+
+
 def _on_stream(stream, call, *tensors):
     """call() with `stream` current, ordered as _run_on and _used_on order it. The calls below run on
     the current stream without a stream object or context of their own, which would cost a small
@@ -481,9 +495,15 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_FLOAT_TYPES = None
+
+
 def _float_types():
-    torch = _torch()
-    return torch.bfloat16, torch.float16, torch.float32
+    global _FLOAT_TYPES
+    if _FLOAT_TYPES is None:
+        torch = _torch()
+        _FLOAT_TYPES = torch.bfloat16, torch.float16, torch.float32
+    return _FLOAT_TYPES
 
 
 def quantize_rows_int8(x, stream=None):
@@ -528,14 +548,16 @@ def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype):
         raise ValueError("xq must be [rows, K] and wq " + ("[N, K]" if offsets is None else "[experts, N, K]"))
     M, K = xq.shape
     lead = tuple(wq.shape[:-1])
-    _need(xq, "xq", torch.int8)
-    _need(wq, "wq", torch.int8, shape=(*lead, K))
-    _need(xs, "xs", torch.float32, shape=(M,))
-    _need(ws, "ws", torch.float32, shape=lead)
+    args = [("xq", xq, torch.int8, (M, K)), ("wq", wq, torch.int8, (*lead, K)), ("xs", xs, torch.float32, (M,)),
+            ("ws", ws, torch.float32, lead)]
     if bias is not None:
-        _need(bias, "bias", torch.bfloat16, shape=lead)
+        args.append(("bias", bias, torch.bfloat16, lead))
     if offsets is not None:
-        _need(offsets, "offsets", torch.int32, shape=(lead[0] + 1,))
+        args.append(("offsets", offsets, torch.int32, (lead[0] + 1,)))
+    dev = torch.cuda.current_device() if xq.is_cuda else -1
+    for name, t, dtype, shape in args:
+        if not _fits(t, dtype, shape, dev):
+            _need(t, name, dtype, shape=shape)
     if K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16:
         xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
         K = xq.shape[1]

@@ -540,8 +540,8 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
         read_frags<TI>(nxt, wm, 0, x0);
         read_frags<TJ>(nxt + BM * 128, wn, 0, w0);
         multiply<TI, TJ>(x1, w1, acc);
-        interleave<kLoads, TI * TJ / 2, 0x20>();
-        interleave<TI + TJ, TI * TJ / 2, 0x100>();
+        interleave<kLoads, TI * TJ * 3 / 4, 0x20>();         // spread widely: 1% over half and half, 4% over reads first
+        interleave<TI + TJ, TI * TJ / 4, 0x100>();
         cur = nxt;
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);                      // no load may still write LDS when the block ends

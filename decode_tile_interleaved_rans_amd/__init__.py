@@ -629,7 +629,11 @@ def _routing_functions():
     global _routing
     if _routing is None:
         torch = _torch()
-        once = torch.autograd.function.once_differentiable
+
+        def once(backward):
+            # refuses a second derivative; its wrapper (4 us) is left out where none can be asked for
+            guarded = torch.autograd.function.once_differentiable(backward)
+            return lambda ctx, *grads: (guarded if torch.is_grad_enabled() else backward)(ctx, *grads)
 
         class SortTokens(torch.autograd.Function):
             @staticmethod
@@ -685,8 +689,11 @@ def sort_tokens(x, expert_ids, n_experts: int, stream=None):
     _need(expert_ids, "expert_ids", expert_ids.dtype)
     if x.dim() != 2 or x.shape[0] != expert_ids.shape[0]:
         raise ValueError(f"x must have shape [{expert_ids.shape[0]}, H], got {tuple(x.shape)}")
+    grad = x.requires_grad and torch.is_grad_enabled()
+    if grad and x.dtype not in _float_types():
+        raise ValueError(f"rows of {x.dtype} have no gradient; detach x")
     rows, offsets, pos = _sort_raw(x, expert_ids, n_experts)
-    if x.requires_grad and torch.is_grad_enabled():
+    if grad:
         rows = _routing_functions()[0].apply(x, rows, pos)
     return rows, offsets, pos
 

@@ -287,6 +287,39 @@ def test_large_result_offsets():
     del y
 
 
+def test_experts_weights_past_32_bit_offsets():
+    # 4.8e9 codes of weights: the last experts lie past 2^31 and 2^32 bytes
+    E, N, K = 72, 8192, 8192
+    wq = torch.empty((E, N, K), dtype=torch.int8, device="cuda")
+    for e in range(E):
+        wq[e] = torch.randint(-127, 128, (N, K), generator=gen(e), device="cuda", dtype=torch.int8)
+    counts = [0] * E
+    counts[3], counts[35], counts[E - 1] = 5, 70, 9
+    off = torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+    R = sum(counts)
+    xq = torch.randint(-127, 128, (R, K), generator=gen(99), device="cuda", dtype=torch.int8)
+    xs, ws = torch.full((R,), 1e-3, device="cuda"), torch.full((E, N), 1e-3, device="cuda")
+    y = ep.gemm_int8_experts(xq, xs, wq, ws, off)
+    for e, a, b in ((3, 0, 5), (35, 5, 75), (E - 1, 75, 84)):
+        check_product(y[a:b], product64(xq[a:b], wq[e]), xs[a:b], ws[e], None)
+
+
+def test_layer_files_and_model_replacement_in_int8(tmp_path):
+    from decode_tile_interleaved_rans_amd import plan
+    torch.manual_seed(0)
+    model = torch.nn.Sequential(torch.nn.Linear(256, 192), torch.nn.GELU(), torch.nn.Linear(192, 64)).cuda()
+    a = ep.CompressedLinear.from_linear(model[0], 5.0, compute="int8")
+    a.save(tmp_path / "a.npz")
+    x = torch.randn((33, 256), generator=gen(2), device="cuda").to(torch.bfloat16)
+    y = a(x)
+    assert torch.equal(ep.CompressedLinear.load(tmp_path / "a.npz", compute="int8")(x), y)
+    assert torch.equal(a(x.view(3, 11, 256)), y.view(3, 11, 192))
+    streams = {n: ep.compress(model[int(n)].weight, 5.0, layout=ep.ROW_LAYOUT, prob_bits=11)[0] for n in ("0", "2")}
+    originals = plan.replace_linears(model, streams, compute="int8")
+    assert torch.equal(model[0](x), y) and model(x).shape == (33, 64)
+    plan.restore_linears(model, originals)
+
+
 def test_other_stream():
     xq, xs, wq, ws, b = operands(300, 400, 512, 31)
     x = torch.randn((300, 512), generator=gen(32), device="cuda").to(torch.bfloat16)

@@ -288,6 +288,79 @@ def test_same_bits_every_time():
         assert all(torch.equal(a, b) for a, b in zip(out, first))
 
 
+def test_rows_past_32_bit_offsets():
+    # 2.4e9 elements of sorted rows: 64-bit addresses in every kernel
+    T, k, E, H = 300000, 2, 16, 4000
+    ids = choices(T, k, E, 8, drop=0.0)
+    x = (torch.arange(T, device="cuda")[:, None] % 251).to(torch.bfloat16).expand(T, H).contiguous()
+    rows, off, pos = ep.sort_tokens(x, ids, E)
+    want = torch.empty(T * k, dtype=torch.bfloat16, device="cuda")
+    want[pos.long().reshape(-1)] = (torch.arange(T, device="cuda") % 251).to(torch.bfloat16).repeat_interleave(k)
+    for c in (0, 1777, H - 1):
+        assert torch.equal(rows[:, c], want)
+    w = torch.ones((T, k), device="cuda").requires_grad_(True)
+    rows.requires_grad_(True)
+    y = ep.combine_tokens(rows, pos, w)
+    assert torch.equal(y.detach()[:, H - 1], 2 * x[:, 0])      # at most 500: exact in BF16
+    d_rows, d_w = torch.autograd.grad(y, [rows, w], x)
+    assert torch.equal(d_rows[:, H - 1], want)
+    ref = H * x[:, :1].double() ** 2                           # every product exact, sums in fp32
+    assert ((d_w.double() - ref).abs() <= (H + 8) * U * ref).all()
+
+
+def test_second_derivative_is_refused():
+    x = torch.randn((6, 16), device="cuda").requires_grad_(True)
+    ids = choices(6, 2, 3, 1)
+    rows, _, pos = ep.sort_tokens(x, ids, 3)
+    y = ep.combine_tokens(rows * rows, pos)
+    (dx,) = torch.autograd.grad(y.sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        dx.sum().backward()
+
+
+def test_float8_rows_have_no_gradient():
+    x = torch.randn((4, 32), device="cuda").to(torch.float8_e4m3fn).requires_grad_(True)
+    with pytest.raises(ValueError, match="detach"):
+        ep.sort_tokens(x, torch.zeros((4, 1), dtype=torch.int64, device="cuda"), 2)
+
+
+def test_from_several_threads():
+    import threading
+    T, k, E, H = 1500, 2, 8, 256
+    ids = choices(T, k, E, 4)
+    x = torch.randn((T, H), generator=gen(1), device="cuda").to(torch.bfloat16)
+    w = torch.rand((T, k), generator=gen(2), device="cuda")
+    q, s = ep.quantize_rows_int8(x)
+
+    def work():
+        rows, off, pos = ep.sort_tokens(x, ids, E)
+        q2, s2 = ep.quantize_rows_int8(rows)
+        return rows, off, pos, ep.combine_tokens(rows, pos, w), q2, s2, ep.gemm_int8(q, s, q, s)
+
+    want = work()
+    torch.cuda.synchronize()
+    errors = []
+
+    def run():
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()) as _:
+                for _ in range(5):
+                    got = work()
+                    torch.cuda.current_stream().synchronize()
+                    for a, b in zip(got, want):
+                        assert torch.equal(a, b)
+        except BaseException as e:
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=run) for _ in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    assert not errors, errors
+
+
 # ------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 13, 600])
 def test_expert_layer_in_int8(T):

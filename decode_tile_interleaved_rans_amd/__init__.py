@@ -104,7 +104,7 @@ def lib() -> C.CDLL:
         L.ep_gemm_int8_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_pad_rows_int8.argtypes = [vp, i64, i64, vp, i64, vp]
         L.ep_linear_forward_int8.argtypes = [vp, vp, i64, vp, vp, vp]
-        L.ep_linear_forward_experts.argtypes = [vp, C.c_int, C.c_int, vp, vp, vp, vp, vp]
+        L.ep_linear_forward_experts.argtypes = [vp, C.c_int, C.c_int, vp, vp, vp, vp, vp, vp]
         L.ep_sort_tokens_scratch.argtypes = [i64, C.c_int, C.c_int, C.POINTER(sz)]
         L.ep_sort_tokens.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp]
         L.ep_combine_tokens.argtypes = [vp, C.c_int, vp, vp, i64, C.c_int, i64, i64, vp, vp]
@@ -889,6 +889,7 @@ def linear_forward_experts(layers, x, expert_ids, weights=None, stream=None):
     hs = (C.c_void_p * n)(*[l.handle.ptr.value for l in layers])
     bs = (C.c_void_p * n)(*[_ptr(b) for b in biases])
     code = {"bf16": BF16, "fp8": F8E4M3, "int8": I8}[layers[0].compute]
-    _check(lib().ep_linear_forward_experts(hs, n, code, _ptr(rows), offs, bs, _ptr(ys), _current_raw()),
+    _check(lib().ep_linear_forward_experts(hs, n, code, _ptr(rows), offs, _ptr(offsets), bs, _ptr(ys),
+                                           _current_raw()),
            "ep_linear_forward_experts")
     return combine_tokens(ys, pos, weights)

@@ -412,6 +412,54 @@ ep_status linear_forward(const ep_handle* w, const void* dev_x, int64_t M, const
     return he == hipSuccess ? EP_OK : hip_fail(he, "recording the workspace event");
 }
 
+// Compressed experts in INT8 with rows of any number (ep_linear_forward_experts has checked everything).
+ep_status int8_experts(const ep_handle* const* w, int count, const uint16_t* x, const int64_t* host_offsets,
+                       const int32_t* dev_offsets, const void* const* dev_bias, uint16_t* y, int64_t R, int64_t N, int64_t K,
+                       size_t codes, int dev, hipStream_t s) {
+    const size_t one = (size_t)N * (size_t)K;                // K % 16 == 0: every expert's codes are 16-byte aligned
+    const int each = (int)std::min<size_t>((size_t)count, std::max<size_t>(1, codes / one));
+    bool biased = false;
+    for (int i = 0; dev_bias && i < count; ++i) biased = biased || dev_bias[i];
+    // workspace: X codes [R][K] | X scales [R] | a chunk's weight codes [each][N][K], scales [each][N], biases
+    const size_t o_xs = up((size_t)R * (size_t)K, 256), o_wq = up(o_xs + 4 * (size_t)R, 256);
+    const size_t o_ws = up(o_wq + (size_t)each * one, 256), o_b = up(o_ws + 4 * (size_t)each * (size_t)N, 256);
+    const size_t need = o_b + (biased ? 2 * (size_t)each * (size_t)N : 0);
+    WsLease ws;
+    hipError_t e = ws_acquire(dev, s, need, &ws);
+    if (e != hipSuccess) return hip_fail(e, "hipMalloc for the linear forward workspace");
+    uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+    int8_t* xq = reinterpret_cast<int8_t*>(ws8);
+    float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+    int8_t* wq = reinterpret_cast<int8_t*>(ws8 + o_wq);
+    float* wsc = reinterpret_cast<float*>(ws8 + o_ws);
+    uint16_t* bias = reinterpret_cast<uint16_t*>(ws8 + o_b);
+    e = ep::launch_quantize_rows_i8(x, EP_BF16, (int)R, (int)K, K, xq, xs, s);
+    if (e != hipSuccess) return hip_fail(e, "quantize launch");
+    for (int e0 = 0; e0 < count; e0 += each) {
+        const int n = std::min(each, count - e0);
+        if (host_offsets[e0 + n] == host_offsets[e0]) continue;
+        std::vector<ep::MatDesc> ds;
+        for (int i = 0; i < n; ++i)
+            if (host_offsets[e0 + i + 1] > host_offsets[e0 + i])
+                ds.push_back(desc_for(w[e0 + i], ep::CT_I8, wq + (size_t)i * one, wsc + (size_t)i * (size_t)N));
+        e = launch_all(ds, s);
+        for (int i = 0; biased && e == hipSuccess && i < n; i += 32) {
+            const uint16_t* b[32];
+            const int m = std::min(32, n - i);
+            for (int j = 0; j < m; ++j) b[j] = static_cast<const uint16_t*>(dev_bias[e0 + i + j]);
+            e = ep::launch_gather_bias(b, m, (int)N, bias + (size_t)i * (size_t)N, s);
+        }
+        if (e != hipSuccess) return hip_fail(e, "grouped expert decode launch");
+        // rows up to the chunk's last expert's: none is left behind it for the product to clear
+        const ep::GemmI8Args g{xq, xs, wq, wsc, biased ? bias : nullptr, y, dev_offsets + e0, (int)host_offsets[e0 + n],
+                               (int)N, (int)K, (int)K, (int)K, (int)N, n, EP_BF16};
+        e = ep::launch_gemm_i8(g, s);
+        if (e != hipSuccess) return hip_fail(e, "expert int8 gemm launch");
+    }
+    e = ws.queued();
+    return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
+}
+
 // Checks and launch of the INT8 products (experts = 0: one weight for all rows).
 ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const int32_t* offsets,
                     int experts, int64_t M, int64_t N, int64_t K, const void* bias, ep_dtype out, void* y, hipStream_t s) {
@@ -1134,7 +1182,8 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
 }
 
 ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dtype compute, const void* dev_x,
-                                    const int64_t* host_offsets, const void* const* dev_bias, void* dev_y, void* hip_stream) {
+                                    const int64_t* host_offsets, const int32_t* dev_offsets, const void* const* dev_bias,
+                                    void* dev_y, void* hip_stream) {
     return guarded([&]() -> ep_status {
         if (count < 1 || count > ep::kRouteMaxExperts) return fail(EP_ERANGE, "the number of experts must be 1 ... 1024");
         if (compute != EP_BF16 && compute != EP_F8E4M3 && compute != EP_I8)
@@ -1152,7 +1201,7 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
         const int64_t N = w[0]->view.rows, K = w[0]->view.cols, R = host_offsets[count];
         if (host_offsets[0] != 0) return fail(EP_EINVAL, "the offsets must start at 0");
         if (R == 0 || N == 0) return EP_OK;
-        if (!dev_y || (K > 0 && !dev_x)) return fail(EP_EINVAL, "null pointer");
+        if (!dev_y || (K > 0 && !dev_x) || (compute == EP_I8 && !dev_offsets)) return fail(EP_EINVAL, "null pointer");
         if (R > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "the rows and out_features must be below 2^31");
         if (K % (compute == EP_BF16 ? 8 : 16)) return fail(EP_EINVAL, "in_features must be a multiple of 8 (16 in FP8 and INT8)");
         if (compute == EP_I8 && K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131071: the int32 sums could overflow");
@@ -1164,6 +1213,19 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
         const int ct = (int)compute;
         const uint16_t* x = static_cast<const uint16_t*>(dev_x);
         uint16_t* y = static_cast<uint16_t*>(dev_y);
+        // INT8 with an expert that the fused launches below do not take (more than 64 rows, layout 0): the
+        // experts with rows are decoded by grouped launches and multiplied by one product per expert, in
+        // chunks of at most kExpertCodes of codes. The sums are exact, so the bits are the same.
+        constexpr size_t kExpertCodes = 512u << 20;
+        if (compute == EP_I8 && K > 0 && (size_t)N * (size_t)K <= kExpertCodes) {
+            bool fits = true;
+            for (int i = 0; i < count && fits; ++i) {
+                const ep::MatDesc d = desc_for(w[i], ct, nullptr, nullptr);
+                const int64_t M = host_offsets[i + 1] - host_offsets[i];
+                fits = M == 0 || ep::fused_many_fits(&d, 1, M);
+            }
+            if (!fits) return int8_experts(w, count, x, host_offsets, dev_offsets, dev_bias, y, R, N, K, kExpertCodes, dev, s);
+        }
         // experts of 1 to 64 rows in the row layout share fused launches: groups of one probability
         // precision, at most kMaxGroup experts and kExpertPartials bytes of partial sums each
         constexpr size_t kExpertPartials = 256u << 20;

@@ -311,7 +311,11 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
     PairRows P;
     begin_pair<CT, true>(M, rs, pair, true, t, P);
     constexpr bool F8 = CT == CT_F8E4M3, I8 = CT == CT_I8;
-    const bool divide = I8 && __any(P.k_l != 1u);   // INT8 rows whose largest |q| is at most 127 store q itself
+    // INT8: round-half-away(q / k) = floor(|q| / k + 1/2), of |q| / k + 1/2 + 1/(4 k): the exact value is a
+    // multiple of 1/(2 k) below 128, so a quarter step more and an fp32 rounding (1.5e-5, k <= 258) never
+    // reach the next integer, and k = 1 gives q. One fused multiply-add and a truncation per value; by
+    // the decode kernel's multiply-high the forward took 88 us instead of 80 at 8192 x 8192 (16 rows).
+    const float inv_k = I8 ? 1.0f / (float)P.k_l : 0.0f, half_k = 0.5f + 0.25f * inv_k;
     const float alpha = h * P.sc_l;                 // the lane's row (scale 0 past the matrix)
     const int lane = threadIdx.x & 63, qg = lane >> 4, n = lane & 15;
     const uint32_t K = M.cols;
@@ -342,21 +346,19 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
         refill(t);
         const uint32_t base = (uint32_t)b << N;
         const uint2* ent_b = T.ent + b * 256;
-        float q[8];                                 // INT8: the coordinate's bit pattern (int32)
+        float q[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             uint2 e;
             const uint2* ent_j = ent_b + 2 * j * 256;
             rans_steps<N, 1>(&t, (2 * j) << N, &base, &ent_j, &e);
             refill_all<1>(&t);
-            if constexpr (I8) q[j] = __int_as_float((int32_t)e.y >> 16);
-            else q[j] = hi16_to_f32(e.y);
+            q[j] = hi16_to_f32(e.y);
             if ((M.esc_tables >> (2 * j)) & 3u) {
                 const bool esc = (int32_t)e.x < 0;
                 if (__ballot(esc)) {
                     const uint32_t w = take_words(t, esc);
-                    const int32_t v = (int32_t)(int16_t)(2 * (int32_t)(int16_t)w + b);
-                    if (esc) q[j] = I8 ? __int_as_float(v) : (float)v;
+                    if (esc) q[j] = (float)(int32_t)(int16_t)(2 * (int32_t)(int16_t)w + b);
                 }
             }
         }
@@ -377,18 +379,10 @@ __device__ __forceinline__ void rows_pair(const MatDesc& M, const Tables& T, Til
                 acc[mt] = __builtin_amdgcn_mfma_f32_16x16x32_fp8_fp8(
                     __builtin_bit_cast(i64_t, make_uint2(ax[mt].x, ax[mt].y)), bop, acc[mt], 0, 0, 0);
         } else if constexpr (I8) {
-            // the INT8 container's values (round-half-away(q / k), as the decode kernel stores them)
+            // the INT8 container's values, as the decode kernel stores them
             int32_t v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = __float_as_int(q[j]);
-            if (divide) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t m = (uint32_t)(v[j] < 0 ? -v[j] : v[j]);
-                    const int32_t d = (int32_t)__umulhi(2u * m + P.k_l, P.magic_l);
-                    v[j] = P.k_l == 1u ? v[j] : v[j] < 0 ? -d : d;
-                }
-            }
+            for (int j = 0; j < 8; ++j) v[j] = (int32_t)__builtin_fmaf(q[j], inv_k, __builtin_copysignf(half_k, q[j]));
             uint32_t bw[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i)             // the low bytes of four values, in order
@@ -453,13 +447,13 @@ __global__ __launch_bounds__(64 * kWaves) void decode_mfma_rows(GroupArgs g) {
 
 // 0 + p[0] + p[1] + ... + p[n - 1] (stride MT x 256) in that order, with eight loads in flight at
 // a time (a loop of dependent additions would wait for each load in turn).
-template <int MT>
-__device__ __forceinline__ float sum_partials(const float* p, int n) {
-    float v = 0.0f;
+template <int MT, typename T = float>
+__device__ __forceinline__ T sum_partials(const T* p, int n) {
+    T v = 0;
     for (int pc0 = 0; pc0 < n; pc0 += 8) {
-        float t[8];
+        T t[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) t[j] = pc0 + j < n ? p[(uint64_t)(pc0 + j) * (MT * 256)] : 0.0f;
+        for (int j = 0; j < 8; ++j) t[j] = pc0 + j < n ? p[(uint64_t)(pc0 + j) * (MT * 256)] : (T)0;
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if (pc0 + j < n) v += t[j];
@@ -527,8 +521,7 @@ __global__ __launch_bounds__(256) void fused_finish_many(FinishMany f) {
     const float* p = o.part + (uint64_t)tr * o.pairs_c * (MT * 256) + ((mt * 4 + qg) * 16 + n) * 4 + i;
     float v;
     if constexpr (CT == CT_I8) {
-        int32_t sum = 0;
-        for (int pc = 0; pc < o.pairs_c; ++pc) sum += __float_as_int(p[(uint64_t)pc * (MT * 256)]);
+        const int32_t sum = sum_partials<MT>(reinterpret_cast<const int32_t*>(p), o.pairs_c);
         const uint32_t qm = o.row_qmax[col], k = qm > 127u ? (qm + 126u) / 127u : 1u;
         const float alpha = (o.step * 0.5f) * o.row_scale[col];
         v = (float)sum * (alpha * (float)k) * o.sx[m];

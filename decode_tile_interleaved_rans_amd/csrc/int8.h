@@ -37,6 +37,9 @@ struct GemmI8Args {
 // e's weight and rows from offsets[experts] on are set to zero.
 hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream);
 
+// dst [count][N] = bias[i] [N] for i < count <= 32; a null bias gives -0, which added to a sum leaves its bits.
+hipError_t launch_gather_bias(const uint16_t* const* bias, int count, int N, uint16_t* dst, hipStream_t stream);
+
 // dst [rows][ld] = src [rows][K] with zeros in columns K .. ld - 1 (ld a multiple of 16, dst 16-byte
 // aligned, src of any alignment, rows contiguous).
 hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* dst, int ld, hipStream_t stream);

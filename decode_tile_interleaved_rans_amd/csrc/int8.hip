@@ -228,6 +228,15 @@ __global__ __launch_bounds__(256) void pad_rows_i8(const int8_t* src, int64_t ro
     *reinterpret_cast<uint4*>(dst + r * (int64_t)ld + k0) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+struct BiasList {
+    const uint16_t* p[32];
+};
+__global__ __launch_bounds__(256) void gather_bias(BiasList b, int N, uint16_t* dst) {
+    const uint16_t* src = b.p[blockIdx.y];
+    for (int64_t n = (int64_t)blockIdx.x * 256 + threadIdx.x; n < N; n += (int64_t)gridDim.x * 256)
+        dst[(int64_t)blockIdx.y * N + n] = src ? src[n] : 0x8000u;
+}
+
 // ------------------------------------------------------------------------------- tile of a block
 // The output tile of a block: rows [m0, m0 + BM) up to m_end, columns [n0, n0 + BN), of expert e
 // (0 without experts). e == experts stands for the rows behind the last expert's, which are zeroed;
@@ -600,6 +609,15 @@ hipError_t launch_quantize_rows_i8(const void* X, int src, int M, int K, int64_t
         case EP_F16: return quantize_src<EP_F16>(X, M, K, ldx, Q, S, stream);
         default: return hipErrorInvalidValue;
     }
+}
+
+hipError_t launch_gather_bias(const uint16_t* const* bias, int count, int N, uint16_t* dst, hipStream_t stream) {
+    if (count < 1 || count > 32) return hipErrorInvalidValue;
+    BiasList b{};
+    for (int i = 0; i < count; ++i) b.p[i] = bias[i];
+    const int64_t blocks = ((int64_t)N + 255) / 256;
+    hipLaunchKernelGGL(gather_bias, dim3((unsigned)(blocks < 1024 ? blocks : 1024), (unsigned)count), dim3(256), 0, stream, b, N, dst);
+    return hipGetLastError();
 }
 
 hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* dst, int ld, hipStream_t stream) {

@@ -403,16 +403,20 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
  * forward of those rows (ep_linear_forward, ep_linear_forward_fp8 or ep_linear_forward_int8 by compute:
  * EP_BF16, EP_F8E4M3 or EP_I8; EP_EUNSUPPORTED otherwise). Experts with 1 to 64 rows whose streams are in the
  * row layout share one fused decode + MFMA launch per 32 of them, cost-balanced, and one finishing
- * launch; experts without rows are not decoded; the others run their own forward.
+ * launch; experts without rows are not decoded. Where an expert has more rows, INT8 decodes the experts
+ * by grouped launches (up to 512 MiB of codes at a time) and multiplies them by ep_gemm_int8_experts'
+ * kernel; in BF16 and FP8 each such expert runs its own forward.
  * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
  * linear layer before a whole model" (compressed layers inside a model's forward). Grouping the experts
  * of a layer is this library's scheduling, not a step of the method.
  *   w: count handles (1 ... 1024, EP_ERANGE otherwise); dev_x: [R][K] bf16, 16-byte aligned; host_offsets:
- * count + 1 host integers, ascending from 0 (EP_EINVAL otherwise), R = the last; dev_bias: NULL or count
+ * count + 1 host integers, ascending from 0 (EP_EINVAL otherwise), R = the last; dev_offsets: the same
+ * values as int32 in device memory (required for EP_I8, else unused and may be NULL); dev_bias: NULL or count
  * pointers (each [N] bf16 or NULL); dev_y: [R][N] bf16. K % 8 == 0, K % 16 == 0 in FP8 and INT8 (EP_EINVAL).
  * Workspace rules of ep_linear_forward. Asynchronous on hip_stream. */
 ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dtype compute, const void* dev_x,
-                                    const int64_t* host_offsets, const void* const* dev_bias, void* dev_y, void* hip_stream);
+                                    const int64_t* host_offsets, const int32_t* dev_offsets, const void* const* dev_bias,
+                                    void* dev_y, void* hip_stream);
 
 /* Tokens sorted by the experts they chose (the input order of ep_gemm_int8_experts, and of compressed
  * layers run expert by expert).

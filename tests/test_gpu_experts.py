@@ -85,6 +85,17 @@ def test_mixed_layouts_precisions_and_group_sizes(compute):
     check(layers, tokens(T, K, 3), ids, torch.rand((T, 3), generator=gen(6), device="cuda"))
 
 
+def test_int8_experts_beyond_one_chunk():
+    # 256 MiB of codes per expert, 512 MiB at a time: three experts in two chunks, one without rows
+    N, K, T = 16384, 16384, 150
+    s, _ = ep.compress_device(W.gpu_student_t(N, K, 3), 3.0, layout=ep.ROW_LAYOUT, prob_bits=11)
+    layers = [ep.CompressedLinear(s, None, "int8") for _ in range(4)]
+    layers[3].bias = torch.randn(N, generator=gen(1), device="cuda").to(torch.bfloat16)
+    ids = torch.tensor([0, 1, 3], device="cuda")[torch.arange(T, device="cuda") % 3][:, None]
+    ids[:70] = 1
+    check(layers, tokens(T, K, 4), ids, None)
+
+
 def test_wide_values_divide_in_int8():
     # rows whose largest |q| passes 127 (large targets): the INT8 container divides them
     E, N, K = 2, 64, 1024
@@ -98,6 +109,19 @@ def test_wide_values_divide_in_int8():
     q, s = ep.quantize_rows_int8(x)
     assert torch.equal(alone(x), ep.gemm_int8(q, s, dq, ds, alone.bias))
     assert (cs > 0).all() and np.abs(cq.view(np.int8)).max() > 64
+    # many divisors: rows of growing outliers, against the decode kernel's integer rounding
+    w = W.student_t(400, 512, 77).astype(np.uint16)
+    f = W.bf16_bits_to_f32(w).copy()
+    f[:, 7] *= np.linspace(1.0, 400.0, 400)
+    st, _ = ep.compress(f.astype(np.float32), 9.0, layout=ep.ROW_LAYOUT, prob_bits=11)
+    lay = ep.CompressedLinear(st, compute="int8")
+    dq, ds = lay.handle.decompress(torch.int8)
+    eye = torch.eye(512, device="cuda").to(torch.bfloat16)     # unit rows: the products are the codes themselves
+    for r0 in range(0, 512, 64):
+        q, sc = ep.quantize_rows_int8(eye[r0:r0 + 64])
+        assert torch.equal(lay(eye[r0:r0 + 64]), ep.gemm_int8(q, sc, dq, ds))
+    qs = lay.handle.decode_symbols().abs().amax(1).int()
+    assert len(((qs + 126) // 127).unique()) > 30              # the case covers what it is for
 
 
 def test_router_gradient():
@@ -138,9 +162,11 @@ def test_refusals():
     L, st = ep.lib(), C.c_void_p(torch.cuda.current_stream().cuda_stream)
     hs = (C.c_void_p * 2)(a.handle.ptr.value, a.handle.ptr.value)
     y = torch.zeros((4, 32), dtype=torch.bfloat16, device="cuda")
-    f = lambda offs, h=hs, px=x.data_ptr(): L.ep_linear_forward_experts(h, 2, ep.I8, px, (C.c_int64 * 3)(*offs), None,
-                                                                        y.data_ptr(), st)
+    f = lambda offs, h=hs, px=x.data_ptr(), d=torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda"): \
+        L.ep_linear_forward_experts(h, 2, ep.I8, px, (C.c_int64 * 3)(*offs), None if d is None else d.data_ptr(), None,
+                                    y.data_ptr(), st)
     assert f([0, 3, 2]) == -1 and f([1, 2, 3]) == -1 and f([0, 1, 2 ** 31]) == -4
     assert f([0, 1, 2], px=x.data_ptr() + 2) == -1
     assert f([0, 1, 2], h=(C.c_void_p * 2)(a.handle.ptr.value, b.handle.ptr.value)) == -1
+    assert f([0, 2, 4], d=None) == -1
     assert f([0, 0, 0]) == 0 and f([0, 2, 4]) == 0

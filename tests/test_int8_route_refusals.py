@@ -1,7 +1,9 @@
 """Refusals of the INT8 products and the expert routing, on the CPU: arguments are checked before any
-device work, in the binding for tensors and in the C ABI for sizes, so no GPU is needed."""
+device work, in the binding for tensors and in the C ABI for sizes, so no GPU is needed. And the
+arithmetic of the fused INT8 forward's rounding, over every coordinate and divisor."""
 import ctypes as C
 
+import numpy as np
 import pytest
 import torch
 
@@ -104,10 +106,11 @@ def test_compressed_experts():
     f = ep.lib().ep_linear_forward_experts
     hs, off = (C.c_void_p * 2)(), (C.c_int64 * 3)(0, 1, 2)
     for n in (0, -1, 1025):
-        assert f(hs, n, ep.BF16, P, off, None, P, None) == ERANGE
-    assert f(hs, 2, ep.F16, P, off, None, P, None) == EUNSUPPORTED
-    assert f(hs, 2, ep.BF16, P, off, None, P, None) == EINVAL and b"null handle" in ep.lib().ep_last_error()
-    assert f(None, 2, ep.BF16, P, off, None, P, None) == EINVAL and f(hs, 2, ep.BF16, P, None, None, P, None) == EINVAL
+        assert f(hs, n, ep.BF16, P, off, P, None, P, None) == ERANGE
+    assert f(hs, 2, ep.F16, P, off, P, None, P, None) == EUNSUPPORTED
+    assert f(hs, 2, ep.BF16, P, off, P, None, P, None) == EINVAL and b"null handle" in ep.lib().ep_last_error()
+    assert f(None, 2, ep.BF16, P, off, P, None, P, None) == EINVAL
+    assert f(hs, 2, ep.BF16, P, None, P, None, P, None) == EINVAL
     assert ep.lib().ep_linear_forward_int8(None, P, 1, None, P, None) == EINVAL
     with pytest.raises(ValueError, match="at least one"):
         ep.linear_forward_experts([], torch.zeros(1), torch.zeros(1))
@@ -138,3 +141,15 @@ def test_binding_refuses_tensors():
         ep.combine_tokens(f32(2, 8), torch.zeros((2, 1), dtype=torch.int32))
     with pytest.raises(ValueError, match="int8"):
         ep.CompressedLinear(b"", compute="int4")
+
+
+def test_fused_int8_rounding_formula():
+    """round-half-away(q / k) as trunc(fma(q, fp32(1 / k), 1/2 + fp32(1 / k) / 4)), for every |q| <= 127 k and every
+    divisor up to the largest a coordinate needs. fp64 holds the product (39 bits) and the sum exactly, so
+    its rounding to fp32 is the fused multiply-add's."""
+    for k in range(1, 259):
+        q = np.arange(0, min(127 * k, 32767) + 1, dtype=np.int64)
+        inv = np.float32(1.0) / np.float32(k)
+        half = np.float32(np.float64(np.float32(0.25) * inv) + 0.5)
+        t = (q.astype(np.float64) * np.float64(inv) + np.float64(half)).astype(np.float32)
+        assert np.array_equal(np.trunc(t).astype(np.int64), (2 * q + k) // (2 * k)), k

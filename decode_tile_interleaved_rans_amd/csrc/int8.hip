@@ -255,34 +255,65 @@ __device__ __forceinline__ void expert_rows(const GemmI8Args& g, int e, int* a, 
     *b = hi < *a ? *a : hi < g.M ? hi : g.M;
 }
 
-// Every wave looks the tile up on its own: 64 experts at a time, one per lane, a running sum of
-// their tile counts over the lanes.
+// The row tiles of 64 experts from e0 on, one expert per lane: its rows [a, b), its tile count and the
+// sum of the counts of the lanes up to it. Returns the 64 experts' total.
 template <int BM>
-__device__ __forceinline__ TileAt expert_tile(const GemmI8Args& g, int tm) {
+__device__ __forceinline__ int expert_counts(const GemmI8Args& g, int e0, int* a, int* b, int* cnt, int* upto) {
     const int lane = threadIdx.x & 63;
-    int before = 0;
-    TileAt t{0, 0, 0, 0, false};
-    for (int e0 = 0; e0 <= g.experts; e0 += 64) {
-        int a = 0, b = 0;
-        if (e0 + lane <= g.experts) expert_rows(g, e0 + lane, &a, &b);
-        const int cnt = (b - a + BM - 1) / BM;
-        int sum = cnt;
+    *a = *b = 0;
+    if (e0 + lane <= g.experts) expert_rows(g, e0 + lane, a, b);
+    *cnt = (*b - *a + BM - 1) / BM;
+    int sum = *cnt;
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(sum, o);
-            if (lane >= o) sum += v;
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(sum, o);
+        if (lane >= o) sum += v;
+    }
+    *upto = sum;
+    return __builtin_amdgcn_readlane(sum, 63);
+}
+
+// Every wave looks its tile up on its own. Tiles are numbered expert by expert, within an expert in groups
+// of 8 row tiles that walk the column tiles together. Consecutive block ids land on different XCDs, so
+// each XCD takes a contiguous eighth of the numbers: the rows and the weight of a group then meet in
+// one L2. Against tiles dealt out round robin, column tiles innermost: 4096 tokens on 4 of 32 experts (2048 x
+// 4096) 171 us for 181, 8 of 128 (1408 x 2048) 184 for 204, 1024 tokens 72 for 80, 16 tokens 30.3 for 31.6;
+// 2 of 8 (8192 x 4096) 313 for 303, with groups of one row tile 391.
+template <int BM, int BN>
+__device__ __forceinline__ TileAt expert_tile(const GemmI8Args& g) {
+    constexpr int G = 8;
+    const int tiles_n = (g.N + BN - 1) / BN;
+    int a, b, cnt, upto;
+    int total = expert_counts<BM>(g, 0, &a, &b, &cnt, &upto);
+    for (int e0 = 64; e0 <= g.experts; e0 += 64) {
+        int a2, b2, c2, u2;
+        total += expert_counts<BM>(g, e0, &a2, &b2, &c2, &u2);
+    }
+    const int64_t all = (int64_t)total * tiles_n;
+    const int64_t each = (all + 7) / 8, at = (int64_t)blockIdx.x / 8;
+    const int64_t number = (int64_t)(blockIdx.x % 8) * each + at;
+    TileAt t{0, 0, 0, 0, false};
+    if (at >= each || number >= all) return t;
+    int before = 0;
+    for (int e0 = 0; e0 <= g.experts; e0 += 64) {
+        if (e0 > 0) {
+            before += __builtin_amdgcn_readlane(upto, 63);
+            expert_counts<BM>(g, e0, &a, &b, &cnt, &upto);
         }
-        const int mine = before + sum - cnt;                   // tiles before this lane's expert
-        const uint64_t hit = __ballot(tm >= mine && tm < mine + cnt);
+        const int64_t mine = (int64_t)(before + upto - cnt) * tiles_n;     // tiles before this lane's expert
+        const uint64_t hit = __ballot(number >= mine && number < mine + (int64_t)cnt * tiles_n);
         if (hit) {
             const int l = __builtin_ctzll(hit);
+            const int in = (int)(number - __shfl(mine, l)), tms = __shfl(cnt, l);
+            const int per = G * tiles_n, first = in / per * G, size = tms - first < G ? tms - first : G;
+            const int tm = first + (in % per) % size, tn = (in % per) / size;
             t.e = __builtin_amdgcn_readfirstlane(e0 + l);
-            t.m0 = __builtin_amdgcn_readfirstlane(__shfl(a, l) + BM * (tm - __shfl(mine, l)));
+            t.m0 = __builtin_amdgcn_readfirstlane(__shfl(a, l) + BM * tm);
+            t.n0 = __builtin_amdgcn_readfirstlane(BN * tn);
             t.m_end = __builtin_amdgcn_readfirstlane(__shfl(b, l));
             t.any = true;
             return t;
         }
-        before += __shfl(sum, 63);
     }
     return t;
 }
@@ -482,18 +513,16 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
     static_assert(kSums <= KS * kRing, "the sums of the other K groups reuse the rings");
     __shared__ __align__(1024) uint8_t smem[KS * kRing + (kSpare ? 1024 : 0)];
     uint8_t* spare = smem + KS * kRing;
-    const int tiles_n = (g.N + BN - 1) / BN;
     TileAt t;
     if constexpr (EXPERTS) {
-        t = expert_tile<BM>(g, (int)blockIdx.x / tiles_n);
+        t = expert_tile<BM, BN>(g);
         if (!t.any) return;
-        t.n0 = __builtin_amdgcn_readfirstlane(((int)blockIdx.x % tiles_n) * BN);
         if (t.e == g.experts) {
             zero_rows(g, t, BM, BN);
             return;
         }
     } else {
-        const int tiles_m = (g.M + BM - 1) / BM, nblk = tiles_m * tiles_n;
+        const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN, nblk = tiles_m * tiles_n;
         int b = blockIdx.x;
         if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
         constexpr int G = 4;
@@ -589,7 +618,8 @@ int64_t row_tiles(const GemmI8Args& g, int bm) {
 
 template <int BM, int BN, int WGM, int WGN, int S, int KS>
 hipError_t tiled_go(const GemmI8Args& g, hipStream_t stream) {
-    const int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
+    int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
+    if (g.experts) blocks = (blocks + 7) / 8 * 8;              // an eighth of the tiles for each XCD
     if (blocks * (64 * WGM * WGN * KS) > kMaxThreads) return hipErrorInvalidValue;
     if (g.experts)
         hipLaunchKernelGGL((gemm_i8<BM, BN, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
@@ -663,9 +693,10 @@ hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
     }
     // Experts: how many rows each has is known to the device only, so the tile goes by the average, several
     // small blocks share a CU where the weights' bytes bound the time, and a tile too large to give
-    // every CU one makes way for the next. Measured, 32 experts: 2 rows each on 16 x 64 tiles 31.5 us (4096 x
-    // 2048; 32 x 64: 31.9, 64 x 64: 33.3), 8 rows on 32 x 64 41.4 (16 x 64: 43.0), 32 rows (2048 x 4096) on
-    // 128 x 128 48.8 (64 x 64: 52.4), 512 rows on 128 x 256 186 (256 x 256: 195, 128 x 128: 198).
+    // every CU one makes way for the next. Measured: 2 rows each on 16 x 64 tiles 45 us (128 experts, 1408 x
+    // 2048; 32 x 64: 48, 64 x 64: 58), 8 rows on 32 x 64 39.6 (32 experts, 4096 x 2048; 16 x 64: 41.8), 32 rows
+    // on 128 x 128 46 (32 experts, 2048 x 4096; 64 x 64: 48), 512 rows on 128 x 256 182 (256 x 256: 191, 128 x
+    // 128: 195).
     const int64_t used = g.M < g.experts ? g.M : g.experts, rows = (g.M + used - 1) / used;
     auto fills = [&](int bm, int bn) { return used * ((rows + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn) >= device_cus(); };
     if (rows > 64 && fills(128, 256)) return tiled_go<128, 256, 2, 4, 3, 1>(g, stream);

@@ -429,8 +429,7 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 //
 // At 4096 x 8192 x 8192 (256 x 256 tiles) 202-215 us, 2.6-2.7 POP/s: the MFMAs are busy 73% of the cycles,
 // at the 1.7 GHz that the card holds under this load; no LDS bank conflicts. With the fragments read just
-// before their MFMAs and two barriers' worth of waits per step it took 260 us (2.1 POP/s). Smaller tiles are
-// bound by the loads: without the MFMAs 512 x 3840 x 10240 takes as long (28 us). Slower: a ring of 64-code
+// before their MFMAs, in the compiler's order, it took 260 us (2.1 POP/s). Smaller tiles are bound by the loads: without the MFMAs 512 x 3840 x 10240 takes as long (28 us). Slower: a ring of 64-code
 // stages with twice the bytes in flight (half lines: 252 for 226 us), 4 waves of 128 x 128 (237), raised wave
 // priority around the MFMAs (228 for 202). Walking the tiles in one persistent block per CU, the next tile's
 // loads ahead of the stores, gained 2-3% on several rounds of tiles and lost 1-3% on one.

@@ -249,6 +249,41 @@ def test_captured_and_replayed():
                 assert torch.equal(a, b), i
 
 
+def test_training_step_captured_and_replayed():
+    # forward and backward in one graph, on leaves of its own; every replay against eager leaves
+    T, k, E, H = 600, 2, 8, 128
+    ids = choices(T, k, E, 4)
+    x, w = torch.randn((T, H), generator=gen(1), device="cuda"), torch.rand((T, k), generator=gen(2), device="cuda")
+    dy = torch.randn((T, H), generator=gen(3), device="cuda")
+
+    def step(x, w):
+        rows, _, pos = ep.sort_tokens(x, ids, E)
+        y = ep.combine_tokens(rows * 2, pos, w)
+        return (y, *torch.autograd.grad(y, [x, w], dy))
+
+    gx, gw = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step(gx, gw)                                      # warm up; its graph is gone before the capture
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = [t.detach() for t in step(gx, gw)]
+    for i in range(4):
+        with torch.no_grad():
+            gx.copy_(torch.roll(x, i, 0))
+            gw.copy_(torch.roll(w, i, 0))
+        ids.copy_(choices(T, k, E, 20 + i))
+        graph.replay()
+        want = step(gx.detach().clone().requires_grad_(True), gw.detach().clone().requires_grad_(True))
+        torch.cuda.synchronize()
+        for a, b in zip(out, want):
+            assert torch.equal(a, b.detach()), i
+
+
 def test_other_stream_with_gradients():
     T, k, E, H = 600, 2, 8, 512
     ids = choices(T, k, E, 4)

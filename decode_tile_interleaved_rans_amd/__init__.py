@@ -41,8 +41,8 @@ EXPORTS = ["ep_compress", "ep_free", "ep_stream_info", "ep_upload", "ep_handle_i
            "ep_release", "ep_last_error", "ep_version", "ep_linear_forward_fp8", "ep_quantize_rows_fp8",
            "ep_gemm_fp8", "ep_compress_device", "ep_linear_forward_noalloc", "ep_linear_forward_many",
            "ep_linear_forward_fp8_many", "ep_quantize_rows_int8", "ep_gemm_int8", "ep_gemm_int8_experts",
-           "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_linear_forward_experts",
-           "ep_sort_tokens_scratch", "ep_sort_tokens",
+           "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_linear_forward_int8_many",
+           "ep_linear_forward_experts", "ep_sort_tokens_scratch", "ep_sort_tokens",
            "ep_combine_tokens", "ep_combine_tokens_grad"]
 
 
@@ -104,6 +104,7 @@ def lib() -> C.CDLL:
         L.ep_gemm_int8_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_pad_rows_int8.argtypes = [vp, i64, i64, vp, i64, vp]
         L.ep_linear_forward_int8.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.ep_linear_forward_int8_many.argtypes = [vp, C.c_int, vp, i64, vp, vp, vp]
         L.ep_linear_forward_experts.argtypes = [vp, C.c_int, C.c_int, vp, vp, vp, vp, vp, vp]
         L.ep_sort_tokens_scratch.argtypes = [i64, C.c_int, C.c_int, C.POINTER(sz)]
         L.ep_sort_tokens.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp]
@@ -816,15 +817,15 @@ def linear_forward_many(layers, x, stream=None):
     """[layer(x) for layer in layers] for CompressedLinear layers of one compute mode that take the
     same input x (BF16, [..., in_features] on the GPU), each output the same bits as the layer's own
     forward. Up to 64 activation rows of row-layout layers with one prob_bits decode in one fused
-    launch (ep_linear_forward_many, ep_linear_forward_fp8_many), so that small layers share the
-    GPU's rounds of tile pairs; above 64 rows BF16 layers can share one slice decode; other cases
-    run the layers one by one."""
+    launch (ep_linear_forward_many, ep_linear_forward_fp8_many, ep_linear_forward_int8_many), so that
+    small layers share the GPU's rounds of tile pairs; above 64 rows BF16 layers can share one slice
+    decode; other cases run the layers one by one."""
     torch = _torch()
     layers = list(layers)
     if not layers:
         return []
-    fp8 = layers[0].compute == "fp8"
-    if len(layers) > 32 or any(l.compute != layers[0].compute or l.compute == "int8" for l in layers):
+    name = "ep_linear_forward" + ("" if layers[0].compute == "bf16" else "_" + layers[0].compute) + "_many"
+    if len(layers) > 32 or any(l.compute != layers[0].compute for l in layers):
         return [l(x, stream=stream) for l in layers]
     K = layers[0].in_features
     shp = x.shape
@@ -846,9 +847,7 @@ def linear_forward_many(layers, x, stream=None):
         hs = (C.c_void_p * n)(*[l.handle.ptr.value for l in layers])
         bs = (C.c_void_p * n)(*[(l.bias.data_ptr() if l.bias is not None else None) for l in layers])
         os_ = (C.c_void_p * n)(*[y.data_ptr() for y in ys])
-        fn = lib().ep_linear_forward_fp8_many if fp8 else lib().ep_linear_forward_many
-        _check(fn(hs, n, C.c_void_p(x2.data_ptr()), rows, bs, os_, C.c_void_p(s.cuda_stream)),
-               "ep_linear_forward_fp8_many" if fp8 else "ep_linear_forward_many")
+        _check(getattr(lib(), name)(hs, n, C.c_void_p(x2.data_ptr()), rows, bs, os_, C.c_void_p(s.cuda_stream)), name)
     _used_on(s, other, x2, *[l.bias for l in layers])
     return [y.reshape(*shp[:-1], l.out_features) for y, l in zip(ys, layers)]
 

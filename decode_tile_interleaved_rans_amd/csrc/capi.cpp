@@ -460,6 +460,69 @@ ep_status int8_experts(const ep_handle* const* w, int count, const uint16_t* x, 
     return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
 }
 
+// Compressed experts in BF16 or FP8 that are not `done` and whose own forward takes one slice and hipBLASLt
+// (the linear forwards' rule): decoded in groups, multiplied one by one, marked done. A group's slices stay
+// within 64 MiB, near the caches when the products read them, and still fill the CUs with decode blocks: 1024
+// tokens over 4 of 32 experts of 4096 x 2048, 615 us (BF16) and 595 (FP8) against 717 and 646 with 512 MiB and
+// 1120 and 1207 with each expert's own forward; 4 of 128 experts of 2048 x 2048, 4096 tokens, 1589 and 1490
+// against 1629 and 1561.
+ep_status sliced_experts(const ep_handle* const* w, int count, ep_dtype compute, const uint16_t* x, const int64_t* host_offsets,
+                         const void* const* dev_bias, uint16_t* y, int64_t R, int64_t N, int64_t K, std::vector<char>* done,
+                         int dev, hipStream_t s) {
+    constexpr size_t kExpertSlices = 64u << 20;
+    const bool f8 = compute == EP_F8E4M3;
+    const size_t one = (size_t)N * (size_t)K * (f8 ? 1 : 2), each = up(one, 256);
+    std::vector<int> todo;
+    for (int i = 0; i < count; ++i) {
+        const int64_t M = host_offsets[i + 1] - host_offsets[i];
+        // one slice: whole tile rows within kSliceBytes
+        if (M > 64 && !(*done)[i] && use_gemm_library(M, N, K) &&
+            up((size_t)N, (size_t)w[i]->view.tile_rows) * (one / (size_t)N) <= kSliceBytes)
+            todo.push_back(i);
+    }
+    if (todo.size() < 2) return EP_OK;                       // a single one: its own forward
+    const int group = (int)std::min<size_t>({todo.size(), (size_t)ep::kMaxGroup, std::max<size_t>(1, kExpertSlices / each)});
+    // workspace: X codes [R][K] | X scales [R] | a group's weight scales (FP8) | its slices | hipBLASLt workspace
+    const size_t o_xs = f8 ? up((size_t)R * (size_t)K, 256) : 0, o_sc = f8 ? up(o_xs + 4 * (size_t)R, 256) : 0;
+    const size_t o_sl = f8 ? up(o_sc + 4 * (size_t)group * (size_t)N, 256) : 0, o_lt = o_sl + (size_t)group * each;
+    WsLease ws;
+    hipError_t e = ws_acquire(dev, s, o_lt + kLtWorkspace, &ws);
+    if (e != hipSuccess) return hip_fail(e, "hipMalloc for the linear forward workspace");
+    uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+    float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+    if (f8) e = ep::launch_quantize_rows_f8(x, (int)R, (int)K, (int)K, ws8, (int)K, xs, s);
+    if (e != hipSuccess) return hip_fail(e, "quantize launch");
+    for (size_t g0 = 0; g0 < todo.size(); g0 += (size_t)group) {
+        const size_t n = std::min(todo.size() - g0, (size_t)group);
+        std::vector<ep::MatDesc> ds;
+        for (size_t j = 0; j < n; ++j)
+            ds.push_back(desc_for(w[todo[g0 + j]], (int)compute, ws8 + o_sl + j * each,
+                                  f8 ? reinterpret_cast<float*>(ws8 + o_sc) + j * (size_t)N : nullptr));
+        e = launch_all(ds, s);
+        for (size_t j = 0; j < n && e == hipSuccess; ++j) {
+            const int i = todo[g0 + j];
+            const int64_t r0 = host_offsets[i], M = host_offsets[i + 1] - r0;
+            const uint16_t* b = dev_bias ? static_cast<const uint16_t*>(dev_bias[i]) : nullptr;
+            uint8_t* sl = ws8 + o_sl + j * each;
+            if (f8) {
+                const ep::GemmF8Args g{ws8 + (size_t)r0 * (size_t)K, xs + r0, sl, reinterpret_cast<float*>(ws8 + o_sc) + j * (size_t)N,
+                                       b, y + r0 * N, (int)M, (int)N, (int)K, (int)K, (int)K, (int)N};
+                e = ep::lt_gemm_f8(g, ws8 + o_lt, kLtWorkspace, s);
+                if (e == hipErrorNotSupported) e = ep::launch_gemm_f8(g, s);
+            } else {
+                ep::GemmArgs g{x + r0 * K, reinterpret_cast<uint16_t*>(sl), b, y + r0 * N, (int)M, (int)N, (int)K, (int)K, (int)K,
+                               (int)N};
+                e = ep::lt_gemm(g, ws8 + o_lt, kLtWorkspace, s);
+                if (e == hipErrorNotSupported) e = ep::launch_gemm(g, s);
+            }
+            (*done)[i] = 1;
+        }
+        if (e != hipSuccess) return hip_fail(e, "grouped expert slice decode + GEMM launch");
+    }
+    e = ws.queued();
+    return e == hipSuccess ? EP_OK : hip_fail(e, "recording the workspace event");
+}
+
 // Checks and launch of the INT8 products (experts = 0: one weight for all rows).
 ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const int32_t* offsets,
                     int experts, int64_t M, int64_t N, int64_t K, const void* bias, ep_dtype out, void* y, hipStream_t s) {
@@ -1181,6 +1244,71 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
     });
 }
 
+ep_status ep_linear_forward_int8_many(const ep_handle* const* w, int count, const void* dev_x, int64_t M,
+                                      const void* const* dev_bias, void* const* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (count < 0 || count > ep::kMaxGroup) return fail(EP_ERANGE, "count must be 0 ... 32");
+        if (count == 0) return EP_OK;
+        if (!w || !dev_y) return fail(EP_EINVAL, "null pointer");
+        hipStream_t s = static_cast<hipStream_t>(hip_stream);
+        for (int i = 0; i < count; ++i) {
+            if (!w[i] || !dev_y[i]) return fail(EP_EINVAL, "null handle or output at layer " + std::to_string(i));
+            if (ep_status st = on_its_device(w[i]); st != EP_OK) return st;
+            if (w[i]->view.mode != EP_MODE_LOSSY_E8) return fail(EP_EUNSUPPORTED, "the linear forward takes a lossy stream");
+            if (w[i]->view.cols != w[0]->view.cols) return fail(EP_EINVAL, "the layers take inputs of different widths");
+        }
+        const int64_t K = w[0]->view.cols;
+        if (M < 0) return fail(EP_EINVAL, "negative M");
+        if (M == 0) return EP_OK;
+        if (K > 0 && !dev_x) return fail(EP_EINVAL, "null pointer");
+        std::vector<ep::MatDesc> ds;
+        bool nonempty = true;
+        for (int i = 0; i < count; ++i) {
+            ds.push_back(desc_for(w[i], ep::CT_I8, nullptr, nullptr));
+            nonempty = nonempty && w[i]->view.rows > 0;
+        }
+        if (K == 0 || K % 16 || K > ep::kI8MaxK || !nonempty || !ep::fused_many_fits(ds.data(), count, M)) {
+            // each layer's own INT8 forward, in order
+            for (int i = 0; i < count; ++i)
+                if (ep_status st = ep_linear_forward_int8(w[i], dev_x, M, dev_bias ? dev_bias[i] : nullptr, dev_y[i], hip_stream);
+                    st != EP_OK)
+                    return st;
+            return EP_OK;
+        }
+        if (reinterpret_cast<uintptr_t>(dev_x) & 15) return fail(EP_EINVAL, "X must be 16-byte aligned");
+        int dev = 0;
+        hipError_t he = hipGetDevice(&dev);
+        if (he != hipSuccess) return hip_fail(he, "hipGetDevice");
+        // workspace: X codes [M][K] | X scales [M] | each layer's int32 partial sums
+        const std::vector<int> rows(count, (int)M);
+        const int mt = ep::fused_rows_mt_of(rows.data(), count);
+        const size_t o_xs = up((size_t)M * (size_t)K, 256);
+        std::vector<size_t> off(count + 1, up(o_xs + 4 * (size_t)M, 256));
+        for (int i = 0; i < count; ++i) off[i + 1] = off[i] + up(ep::fused_rows_partial_bytes(ds[i], mt), 256);
+        WsLease ws;
+        if ((he = ws_acquire(dev, s, off[count], &ws)) != hipSuccess)
+            return hip_fail(he, "hipMalloc for the linear forward workspace");
+        uint8_t* ws8 = static_cast<uint8_t*>(ws.ptr);
+        float* xs = reinterpret_cast<float*>(ws8 + o_xs);
+        const std::vector<const void*> x(count, ws8);
+        const std::vector<const float*> xss(count, xs);
+        std::vector<float*> parts(count);
+        std::vector<const uint16_t*> bias(count);
+        std::vector<uint16_t*> ys(count);
+        for (int i = 0; i < count; ++i) {
+            parts[i] = reinterpret_cast<float*>(ws8 + off[i]);
+            bias[i] = dev_bias ? static_cast<const uint16_t*>(dev_bias[i]) : nullptr;
+            ys[i] = static_cast<uint16_t*>(dev_y[i]);
+        }
+        hipError_t e = ep::launch_quantize_rows_i8(dev_x, EP_BF16, (int)M, (int)K, K, reinterpret_cast<int8_t*>(ws8), xs, s);
+        if (e == hipSuccess)
+            e = ep::launch_fused_rows(ds.data(), count, ep::CT_I8, x.data(), xss.data(), rows.data(), parts.data(), bias.data(),
+                                      ys.data(), s);
+        if (e == hipSuccess) e = ws.queued();
+        return e == hipSuccess ? EP_OK : hip_fail(e, "grouped fused INT8 decode + MFMA launch");
+    });
+}
+
 ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dtype compute, const void* dev_x,
                                     const int64_t* host_offsets, const int32_t* dev_offsets, const void* const* dev_bias,
                                     void* dev_y, void* hip_stream) {
@@ -1215,8 +1343,10 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
         uint16_t* y = static_cast<uint16_t*>(dev_y);
         // INT8 with an expert that the fused launches below do not take (more than 64 rows, layout 0): the
         // experts with rows are decoded by grouped launches and multiplied by one product per expert, in
-        // chunks of at most kExpertCodes of codes. The sums are exact, so the bits are the same.
-        constexpr size_t kExpertCodes = 512u << 20;
+        // chunks of at most kExpertCodes of codes. The sums are exact, so the bits are the same. One product per
+        // chunk: 4096 tokens over 4 of 32 experts of 4096 x 2048 take 599 us in one chunk of 256 MiB, 642 in two
+        // and 686 in four; 512 MiB bring nothing more (4 of 128 of 2048 x 2048: 881 against 868).
+        constexpr size_t kExpertCodes = 256u << 20;
         if (compute == EP_I8 && K > 0 && (size_t)N * (size_t)K <= kExpertCodes) {
             bool fits = true;
             for (int i = 0; i < count && fits; ++i) {
@@ -1291,6 +1421,12 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
                 if (e != hipSuccess) return hip_fail(e, "grouped expert decode + MFMA launch");
             }
             if ((e = ws.queued()) != hipSuccess) return hip_fail(e, "recording the workspace event");
+        }
+        // BF16 and FP8 experts whose own forward would decode them as one slice and multiply it by hipBLASLt:
+        // several slices decoded by one grouped launch, then the same products
+        if (compute != EP_I8 && K > 0) {
+            if (ep_status st = sliced_experts(w, count, compute, x, host_offsets, dev_bias, y, R, N, K, &done, dev, s); st != EP_OK)
+                return st;
         }
         // the others: each its own forward
         for (int i = 0; i < count; ++i) {

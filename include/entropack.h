@@ -398,14 +398,28 @@ ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_
 ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t M, const void* dev_bias, void* dev_y,
                                  void* hip_stream);
 
+/* ep_linear_forward_many in INT8: Y_i the same bits as ep_linear_forward_int8(w[i], dev_x, M, dev_bias[i],
+ * dev_y[i]) for every layer. When the layers are row-layout streams with one prob_bits, 1 <= M <= 64 and
+ * K % 16 == 0, the activations are quantized once for the group, one kernel decodes every layer's tile
+ * pairs into INT8 codes for the INT8 MFMA and one finishes all outputs; otherwise one
+ * ep_linear_forward_int8 per layer, in order.
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
+ * linear layer before a whole model"; "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at
+ * Arbitrary Bitrates", Abstract (INT8 among the containers the decode fills). Grouping layers that share an
+ * input is this library's scheduling, not a step of the method.
+ * Arguments, checks and errors as ep_linear_forward_many, plus those of ep_linear_forward_int8. */
+ep_status ep_linear_forward_int8_many(const ep_handle* const* w, int count, const void* dev_x, int64_t M,
+                                      const void* const* dev_bias, void* const* dev_y, void* hip_stream);
+
 /* Compressed expert layers: expert e (handle w[e], all of one shape [N][K]) multiplies the rows offsets[e]
  * ... offsets[e + 1] - 1 of X (ep_sort_tokens' order), each row of Y the same bits as the expert's own
  * forward of those rows (ep_linear_forward, ep_linear_forward_fp8 or ep_linear_forward_int8 by compute:
  * EP_BF16, EP_F8E4M3 or EP_I8; EP_EUNSUPPORTED otherwise). Experts with 1 to 64 rows whose streams are in the
  * row layout share one fused decode + MFMA launch per 32 of them, cost-balanced, and one finishing
  * launch; experts without rows are not decoded. Where an expert has more rows, INT8 decodes the experts
- * by grouped launches (up to 512 MiB of codes at a time) and multiplies them by ep_gemm_int8_experts'
- * kernel; in BF16 and FP8 each such expert runs its own forward.
+ * by grouped launches (up to 256 MiB of codes at a time) and multiplies them by ep_gemm_int8_experts'
+ * kernel; in BF16 and FP8 such experts are decoded by grouped launches and multiplied one by one where
+ * their own forward would take one slice and hipBLASLt, and run their own forward elsewhere.
  * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one
  * linear layer before a whole model" (compressed layers inside a model's forward). Grouping the experts
  * of a layer is this library's scheduling, not a step of the method.

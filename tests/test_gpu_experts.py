@@ -85,8 +85,19 @@ def test_mixed_layouts_precisions_and_group_sizes(compute):
     check(layers, tokens(T, K, 3), ids, torch.rand((T, 3), generator=gen(6), device="cuda"))
 
 
+@pytest.mark.parametrize("compute", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("N,K", [(200, 1040), (512, 8192)])    # hipBLASLt, and (the larger, up to 255 rows) the own kernel
+def test_experts_of_many_rows(N, K, compute):
+    E, T = 40, 3000
+    layers = experts(E, N, K, compute, layout=lambda e: e % 2)
+    ids = torch.randint(0, E, (T, 2), generator=gen(5), device="cuda")
+    ids[:400, 0] = 11
+    ids = torch.where((ids == 20) | (ids == 3), -1, ids)
+    check(layers, tokens(T, K, 3), ids, torch.rand((T, 2), generator=gen(6), device="cuda"))
+
+
 def test_int8_experts_beyond_one_chunk():
-    # 256 MiB of codes per expert, 512 MiB at a time: three experts in two chunks, one without rows
+    # 256 MiB of codes per expert, 256 MiB at a time: three experts in a chunk each, one without rows
     N, K, T = 16384, 16384, 150
     s, _ = ep.compress_device(W.gpu_student_t(N, K, 3), 3.0, layout=ep.ROW_LAYOUT, prob_bits=11)
     layers = [ep.CompressedLinear(s, None, "int8") for _ in range(4)]

@@ -359,6 +359,22 @@ def test_compressed_forward(M, layout):
     assert torch.equal(ep.linear_forward_many([layer, layer], x)[1], y)
 
 
+@pytest.mark.parametrize("M", [1, 16, 40, 64, 65])
+def test_layers_that_share_an_input(M):
+    K = 784
+    layers = []
+    for i, N in enumerate((300, 16, 1000)):
+        s, _ = ep.compress(W.student_t(N, K, 40 + i), 4.5, dtype=ep.BF16, layout=ep.ROW_LAYOUT, prob_bits=11)
+        b = torch.randn(N, generator=gen(i), device="cuda").to(torch.bfloat16) if i != 1 else None
+        layers.append(ep.CompressedLinear(s, b, compute="int8"))
+    s0, _ = ep.compress(W.student_t(64, K, 50), 4.5, dtype=ep.BF16, layout=0, prob_bits=11)
+    x = torch.randn((M, K), generator=gen(M), device="cuda").to(torch.bfloat16)
+    for group in (layers, layers[:1], layers + [ep.CompressedLinear(s0, compute="int8")]):   # the last not fused
+        for y, l in zip(ep.linear_forward_many(group, x), group):
+            assert torch.equal(y, l(x))
+            l.handle.check()
+
+
 def test_compressed_forward_on_two_slices():
     # a weight of more than one 128 MiB slice, 128 MiB / K rows each
     N, K, M = 9000, 16384, 70

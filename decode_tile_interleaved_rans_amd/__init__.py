@@ -524,9 +524,10 @@ def quantize_rows_int8(x, stream=None):
 
 
 def pad_rows_int8(codes, stream=None):
-    """INT8 codes [..., K] in new memory with K rounded up to a multiple of 16, zeros behind: the layout
-    the INT8 products read. They call this for codes that lack it; a program with such a weight lays
-    it out once and keeps it (and pads the activations' codes to the same width)."""
+    """INT8 codes [..., K] in new memory with K rounded up to a multiple of 16 (of 128 from 1024 to
+    130944: whole cache lines), zeros behind: the layout the INT8 products read. They call this for
+    codes that lack it; a program with such a weight lays it out once and keeps it (and pads the
+    activations' codes to the same width)."""
     if stream is not None:
         return _on_stream(stream, lambda: pad_rows_int8(codes), codes)
     torch = _torch()
@@ -534,7 +535,10 @@ def pad_rows_int8(codes, stream=None):
     if codes.dim() < 1:
         raise ValueError("codes must have rows")
     K = codes.shape[-1]
-    rows, ld = codes.numel() // K if K else 0, (K + 15) // 16 * 16
+    # rows that begin inside a 128-byte line cost the product's loads two lines a piece: 333 x 5003 from
+    # rows of 3856 codes 23.0 us, of 3968 18.8
+    step = 128 if 1024 <= K <= 130944 else 16
+    rows, ld = codes.numel() // K if K else 0, (K + step - 1) // step * step
     out = torch.empty((*codes.shape[:-1], ld), dtype=torch.int8, device=codes.device)
     _check(lib().ep_pad_rows_int8(_ptr(codes), rows, K, _ptr(out), ld, _current_raw()), "ep_pad_rows_int8")
     return out

@@ -209,7 +209,9 @@ hipError_t quantize_src(const void* X, int M, int K, int64_t ldx, int8_t* Q, flo
 
 // ------------------------------------------------------------------------------- rows to 16 bytes
 // Codes whose rows are not 16-byte aligned (K % 16, or a base address inside a row) are copied once
-// to rows of K rounded up to 16 with zeros behind; the zeros add nothing to the sums.
+// to rows of ld >= K codes with zeros behind; the zeros add nothing to the sums. The piece that a row ends
+// in is read like the others where the next row's codes lie behind it, and masked; only the last row's is
+// read byte by byte.
 __global__ __launch_bounds__(256) void pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* dst, int ld) {
     const int cpr = ld / 16;
     const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
@@ -218,12 +220,18 @@ __global__ __launch_bounds__(256) void pad_rows_i8(const int8_t* src, int64_t ro
     const int k0 = 16 * (int)(c % cpr);
     const uint8_t* s = reinterpret_cast<const uint8_t*>(src) + r * (int64_t)K + k0;
     uint32_t w[4] = {0, 0, 0, 0};
-    if (k0 + 16 <= K) {
+    const int left = K - k0;                                   // codes of the row from here on
+    if (left > 0 && r * (int64_t)K + k0 + 16 <= rows * (int64_t)K) {
         __builtin_memcpy(w, s, 16);                            // one load of any alignment
-    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = left - 4 * i;                        // valid bytes of this word
+            w[i] = n >= 4 ? w[i] : n > 0 ? w[i] & ((1u << (8 * n)) - 1) : 0;
+        }
+    } else if (left > 0) {
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            if (k0 + i < K) w[i / 4] |= (uint32_t)s[i] << (8 * (i % 4));
+            if (i < left) w[i / 4] |= (uint32_t)s[i] << (8 * (i % 4));
     }
     *reinterpret_cast<uint4*>(dst + r * (int64_t)ld + k0) = make_uint4(w[0], w[1], w[2], w[3]);
 }

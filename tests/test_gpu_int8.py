@@ -148,7 +148,8 @@ def test_product(M, N, K, out):
     check_product(ep.gemm_int8(xq, xs, wq, ws, b, out_dtype=out), acc, xs, ws, b)
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 5, 1), (3, 70, 15), (40, 33, 17), (90, 65, 127), (300, 401, 1001)])
+@pytest.mark.parametrize("M,N,K", [(1, 5, 1), (3, 70, 15), (40, 33, 17), (90, 65, 127), (300, 401, 1001),
+                                   (200, 130, 1500), (20, 50, 4097), (3, 4, 130945), (2, 5, 131041)])
 def test_product_of_any_width(M, N, K):
     xq, xs, wq, ws, b = operands(M, N, K, K)
     check_product(ep.gemm_int8(xq, xs, wq, ws, b), product64(xq, wq), xs, ws, b)

@@ -482,9 +482,10 @@ ep_status sliced_experts(const ep_handle* const* w, int count, ep_dtype compute,
     }
     if (todo.size() < 2) return EP_OK;                       // a single one: its own forward
     const int group = (int)std::min<size_t>({todo.size(), (size_t)ep::kMaxGroup, std::max<size_t>(1, kExpertSlices / each)});
+    const size_t sn = up((size_t)N, 64);                     // a weight's scales
     // workspace: X codes [R][K] | X scales [R] | a group's weight scales (FP8) | its slices | hipBLASLt workspace
     const size_t o_xs = f8 ? up((size_t)R * (size_t)K, 256) : 0, o_sc = f8 ? up(o_xs + 4 * (size_t)R, 256) : 0;
-    const size_t o_sl = f8 ? up(o_sc + 4 * (size_t)group * (size_t)N, 256) : 0, o_lt = o_sl + (size_t)group * each;
+    const size_t o_sl = f8 ? up(o_sc + 4 * (size_t)group * sn, 256) : 0, o_lt = o_sl + (size_t)group * each;
     WsLease ws;
     hipError_t e = ws_acquire(dev, s, o_lt + kLtWorkspace, &ws);
     if (e != hipSuccess) return hip_fail(e, "hipMalloc for the linear forward workspace");
@@ -497,7 +498,7 @@ ep_status sliced_experts(const ep_handle* const* w, int count, ep_dtype compute,
         std::vector<ep::MatDesc> ds;
         for (size_t j = 0; j < n; ++j)
             ds.push_back(desc_for(w[todo[g0 + j]], (int)compute, ws8 + o_sl + j * each,
-                                  f8 ? reinterpret_cast<float*>(ws8 + o_sc) + j * (size_t)N : nullptr));
+                                  f8 ? reinterpret_cast<float*>(ws8 + o_sc) + j * sn : nullptr));
         e = launch_all(ds, s);
         for (size_t j = 0; j < n && e == hipSuccess; ++j) {
             const int i = todo[g0 + j];
@@ -505,7 +506,7 @@ ep_status sliced_experts(const ep_handle* const* w, int count, ep_dtype compute,
             const uint16_t* b = dev_bias ? static_cast<const uint16_t*>(dev_bias[i]) : nullptr;
             uint8_t* sl = ws8 + o_sl + j * each;
             if (f8) {
-                const ep::GemmF8Args g{ws8 + (size_t)r0 * (size_t)K, xs + r0, sl, reinterpret_cast<float*>(ws8 + o_sc) + j * (size_t)N,
+                const ep::GemmF8Args g{ws8 + (size_t)r0 * (size_t)K, xs + r0, sl, reinterpret_cast<float*>(ws8 + o_sc) + j * sn,
                                        b, y + r0 * N, (int)M, (int)N, (int)K, (int)K, (int)K, (int)N};
                 e = ep::lt_gemm_f8(g, ws8 + o_lt, kLtWorkspace, s);
                 if (e == hipErrorNotSupported) e = ep::launch_gemm_f8(g, s);

@@ -32,8 +32,11 @@ struct LtPlan {
 };
 
 // Plans kept at most: a caller whose row count varies from call to call (serving with variable
-// token counts) would otherwise add a plan, and a heuristic query, per distinct M for ever.
-constexpr size_t kMaxPlans = 128;
+// token counts) would otherwise add a plan, and a heuristic query, per distinct M for ever. A layer of
+// experts asks for one plan per row count (45 us each): 1024 tokens on 4 of 32 experts, with new choices every
+// call, took 1.9 ms at first and 0.65 once the counts were known; 128 plans would be gone in four calls,
+// the other layers' among them.
+constexpr size_t kMaxPlans = 1024;
 
 void destroy(LtPlan& p) {
     if (p.a) hipblasLtMatrixLayoutDestroy(p.a);

@@ -86,7 +86,7 @@ def test_mixed_layouts_precisions_and_group_sizes(compute):
 
 
 @pytest.mark.parametrize("compute", ["bf16", "fp8", "int8"])
-@pytest.mark.parametrize("N,K", [(200, 1040), (512, 8192)])    # hipBLASLt, and (the larger, up to 255 rows) the own kernel
+@pytest.mark.parametrize("N,K", [(200, 1040), (201, 528), (512, 8192)])    # the last: up to 255 rows the own kernel
 def test_experts_of_many_rows(N, K, compute):
     E, T = 40, 3000
     layers = experts(E, N, K, compute, layout=lambda e: e % 2)
@@ -94,6 +94,22 @@ def test_experts_of_many_rows(N, K, compute):
     ids[:400, 0] = 11
     ids = torch.where((ids == 20) | (ids == 3), -1, ids)
     check(layers, tokens(T, K, 3), ids, torch.rand((T, 2), generator=gen(6), device="cuda"))
+
+
+def test_row_counts_beyond_the_plan_cache():
+    # more distinct row counts than hipBLASLt plans are kept: the first one again gives the same bits
+    N, K = 128, 128
+    wq, ws = ep.quantize_rows_fp8(torch.randn((N, K), generator=gen(1), device="cuda").to(torch.bfloat16))
+    xq, xs = ep.quantize_rows_fp8(torch.randn((1650, K), generator=gen(2), device="cuda").to(torch.bfloat16))
+    x64, w64 = (q.view(torch.float8_e4m3fn).float().double() * s[:, None].double() for q, s in ((xq, xs), (wq, ws)))
+    first = ep.gemm_fp8(xq[:600], xs[:600], wq, ws)
+    for M in range(600, 1650):
+        y = ep.gemm_fp8(xq[:M], xs[:M], wq, ws)
+        if M % 150 == 0:
+            want, room = x64[:M] @ w64.T, x64[:M].abs() @ w64.T.abs()
+            # bf16 output: 2^-8 of the value; fp32 sums of 128 products: 2^-16 of the sum of magnitudes
+            assert ((y.double() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -16 * room).all()
+    assert torch.equal(ep.gemm_fp8(xq[:600], xs[:600], wq, ws), first)
 
 
 def test_int8_experts_beyond_one_chunk():

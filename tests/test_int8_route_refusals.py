@@ -112,6 +112,12 @@ def test_compressed_experts():
     assert f(None, 2, ep.BF16, P, off, P, None, P, None) == EINVAL
     assert f(hs, 2, ep.BF16, P, None, P, None, P, None) == EINVAL
     assert ep.lib().ep_linear_forward_int8(None, P, 1, None, P, None) == EINVAL
+    many = ep.lib().ep_linear_forward_int8_many
+    for n in (-1, 33):
+        assert many(hs, n, P, 4, None, hs, None) == ERANGE
+    assert many(None, 2, P, 4, None, hs, None) == EINVAL and many(hs, 2, P, 4, None, None, None) == EINVAL
+    assert many(hs, 2, P, 4, None, hs, None) == EINVAL and b"null handle" in ep.lib().ep_last_error()
+    assert many(None, 0, None, 4, None, None, None) == 0
     with pytest.raises(ValueError, match="at least one"):
         ep.linear_forward_experts([], torch.zeros(1), torch.zeros(1))
 

@@ -437,7 +437,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 //
 // At 4096 x 8192 x 8192 (256 x 256 tiles) 202-215 us, 2.6-2.7 POP/s: the MFMAs are busy 73% of the cycles,
 // at the 1.7 GHz that the card holds under this load; no LDS bank conflicts. With the fragments read just
-// before their MFMAs, in the compiler's order, it took 260 us (2.1 POP/s). Smaller tiles are bound by the loads: without the MFMAs 512 x 3840 x 10240 takes as long (28 us). Slower: a ring of 64-code
+// before their MFMAs, in the compiler's order, it took 260 us (2.1 POP/s). Smaller tiles are bound by the
+// loads: without the MFMAs 512 x 3840 x 10240 takes as long (28 us). Slower: a ring of 64-code
 // stages with twice the bytes in flight (half lines: 252 for 226 us), 4 waves of 128 x 128 (237), raised wave
 // priority around the MFMAs (228 for 202). Walking the tiles in one persistent block per CU, the next tile's
 // loads ahead of the stores, gained 2-3% on several rounds of tiles and lost 1-3% on one.
@@ -538,8 +539,10 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
         }
     } else {
         const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN, nblk = tiles_m * tiles_n;
-        int b = blockIdx.x;
-        if (nblk % 8 == 0) b = (b % 8) * (nblk / 8) + b / 8;
+        // each XCD a contiguous range of the tiles, so that a column's row tiles meet in one L2 (333 x 5003 x 3968,
+        // 237 tiles: 17.6 us, dealt out round robin 18.3; 200 x 4100 x 8192: 23.2 and 25.2)
+        const int xcd = blockIdx.x % 8, rest = nblk % 8;
+        const int b = xcd * (nblk / 8) + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
         constexpr int G = 4;
         const int per_group = G * tiles_n, first_m = (b / per_group) * G;
         const int gsize = tiles_m - first_m < G ? tiles_m - first_m : G;
@@ -674,23 +677,27 @@ hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* ds
 }
 
 // Tile of a product with one weight. A step of 128 K columns takes a block about the time below, whatever
-// M, N and K (measured with one block per CU; small tiles are bound by the latency and the rate of the
-// loads from L2, the largest by the MFMAs), so the estimate is rounds of tiles over the CUs times steps
-// times that. It picks, e.g., 256 x 256 for 4096 x 8192 x 8192 (211 us; 128 x 128: 266), 128 x 128 for
-// 512 x 8192 x 8192 (42; 64 x 64: 59), 128 x 64 for 333 x 5003 x 3856 (22; 128 x 128: 24, 64 x 64: 26),
-// 32 x 64 for 64 x 8192 x 8192 (20; 64 x 64: 24), 16 x 64 for 1 x 11520 x 3840 (11) and 16 x 32 with two
-// K groups for 1 x 8192 x 8192 (15; 16 x 64: 16) and 1 x 4096 x 16384 (16; 16 x 64: 25).
+// M, N and K (measured with one block per CU and weights that come from HBM; small tiles are bound by the
+// latency and the rate of the loads, the largest by the MFMAs), so the estimate is rounds of tiles over the
+// CUs times steps times that. It picks, e.g., 256 x 256 for 4096 x 8192 x 8192 (211 us; 128 x 128: 322), 256 x 192
+// for 1024 x 11520 x 3840 (51; 256 x 256: 55, 256 x 128: 66), 128 x 128 for 512 x 8192 x 8192 (44; 128 x 64: 60, 64 x
+// 64: 69), 128 x 64 for 333 x 5003 x 3968 (17.6; 64 x 64: 20.4, 128 x 128: 24.3), 64 x 64 for 256 x 4096 x 4096 (12.8;
+// 32 x 64: 15.9, 128 x 64: 17.1), 32 x 64 for 64 x 8192 x 8192 (19.5; 64 x 64: 23.9), 16 x 64 for 1 x 11520 x 3840
+// (10.9) and 16 x 32 with two K groups for 1 x 8192 x 8192 (15.1; 16 x 64: 16.5) and 1 x 4096 x 16384 (16.2; 16 x
+// 64: 24.7). Waves per block where one tile fills a CU: 128 x 128 in 16 (1024 x 4096 x 4096 24.5; in 8 29.7), 128 x 64
+// in 8 (333 x 5003 x 3968 17.6; in 4 18.4), 64 x 64 in 8 (256 x 4096 x 4096 12.8; in 4 13.4): more of them hide the
+// barrier and the LDS reads of a step.
 struct TileCost {
     int bm, bn;
     float step_us;
     hipError_t (*go)(const GemmI8Args&, hipStream_t);
 };
 const TileCost kTiles[] = {
-    {256, 256, 1.65f, tiled_go<256, 256, 2, 4, 2, 1>}, {256, 128, 0.97f, tiled_go<256, 128, 4, 2, 3, 1>},
-    {128, 128, 0.65f, tiled_go<128, 128, 2, 4, 4, 1>}, {128, 64, 0.50f, tiled_go<128, 64, 2, 2, 6, 1>},
-    {64, 64, 0.375f, tiled_go<64, 64, 2, 2, 4, 1>},    {32, 64, 0.305f, tiled_go<32, 64, 1, 4, 5, 1>},
-    {32, 32, 0.245f, tiled_go<32, 32, 1, 2, 4, 2>},    {16, 64, 0.28f, tiled_go<16, 64, 1, 4, 6, 1>},
-    {16, 32, 0.235f, tiled_go<16, 32, 1, 2, 6, 2>},
+    {256, 256, 1.65f, tiled_go<256, 256, 2, 4, 2, 1>}, {256, 192, 1.33f, tiled_go<256, 192, 2, 4, 2, 1>},
+    {256, 128, 0.97f, tiled_go<256, 128, 4, 2, 3, 1>}, {128, 128, 0.65f, tiled_go<128, 128, 4, 4, 3, 1>},
+    {128, 64, 0.47f, tiled_go<128, 64, 4, 2, 4, 1>},   {64, 64, 0.365f, tiled_go<64, 64, 2, 4, 4, 1>},
+    {32, 64, 0.305f, tiled_go<32, 64, 1, 4, 5, 1>},    {32, 32, 0.245f, tiled_go<32, 32, 1, 2, 4, 2>},
+    {16, 64, 0.28f, tiled_go<16, 64, 1, 4, 6, 1>},     {16, 32, 0.235f, tiled_go<16, 32, 1, 2, 6, 2>},
 };
 constexpr float kTileUs = 1.5f;             // start and epilogue of a tile
 
@@ -710,13 +717,16 @@ hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
     // small blocks share a CU where the weights' bytes bound the time, and a tile too large to give
     // every CU one makes way for the next. Measured: 2 rows each on 16 x 64 tiles 45 us (128 experts, 1408 x
     // 2048; 32 x 64: 48, 64 x 64: 58), 8 rows on 32 x 64 39.6 (32 experts, 4096 x 2048; 16 x 64: 41.8), 32 rows
-    // on 128 x 128 46 (32 experts, 2048 x 4096; 64 x 64: 48), 512 rows on 128 x 256 182 (256 x 256: 191, 128 x
-    // 128: 195).
+    // on 128 x 128 43.3 (32 experts, 2048 x 4096; in 4 waves instead of 16 46.3; 64 x 64: 48), 128 rows on
+    // 128 x 256 75 (128 x 192: 87), and from 192 rows on 128 x 192, two blocks to a CU, so that one's start and end run
+    // behind the other's MFMAs: 512 rows of 2048 x 4096 181 (128 x 256: 184, 256 x 256: 191, 128 x 128: 195), 375 rows of
+    // 16 experts of 4096 x 2048 70 (128 x 256: 83), 2048 rows of 4 of 2048 x 2048 46 (61).
     const int64_t used = g.M < g.experts ? g.M : g.experts, rows = (g.M + used - 1) / used;
     auto fills = [&](int bm, int bn) { return used * ((rows + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn) >= device_cus(); };
+    if (rows >= 192 && fills(128, 192)) return tiled_go<128, 192, 2, 4, 2, 1>(g, stream);
     if (rows > 64 && fills(128, 256)) return tiled_go<128, 256, 2, 4, 3, 1>(g, stream);
-    if (rows > 16 && fills(128, 128)) return tiled_go<128, 128, 2, 2, 2, 1>(g, stream);
-    if (rows > 16 && fills(128, 64)) return tiled_go<128, 64, 2, 2, 3, 1>(g, stream);
+    if (rows > 16 && fills(128, 128)) return tiled_go<128, 128, 4, 4, 2, 1>(g, stream);
+    if (rows > 16 && fills(128, 64)) return tiled_go<128, 64, 4, 2, 3, 1>(g, stream);
     if (rows > 4) return tiled_go<32, 64, 1, 4, 3, 1>(g, stream);
     return tiled_go<16, 64, 1, 4, 3, 1>(g, stream);
 }

@@ -136,7 +136,8 @@ def check_product(y, acc, xs, ws, b):
 
 SHAPES = [(1, 1, 16), (1, 17, 32), (2, 64, 128), (5, 100, 144), (16, 48, 1024), (17, 33, 4112), (31, 130, 256), (33, 20, 512),
           (64, 257, 2048), (65, 63, 640), (100, 500, 96), (128, 128, 128), (200, 1000, 1040), (257, 300, 16), (130, 4100, 272),
-          (700, 1300, 400), (1030, 2050, 256), (4100, 4099, 144)]
+          (700, 1300, 400), (1030, 2050, 256), (4100, 4099, 144), (1000, 11500, 272), (1000, 7001, 144), (333, 5003, 272),
+          (2048, 8190, 144), (64, 8190, 144), (16, 11520, 144)]
 
 
 @pytest.mark.parametrize("out", TYPES)
@@ -242,6 +243,21 @@ def test_experts(counts, N, K, out):
                 assert torch.equal(y[a:a + c], ep.gemm_int8(xq[a:a + c], xs[a:a + c], wq[e], ws[e],
                                                             None if bias is None else b[e], out_dtype=out))
             a += c
+
+
+# tiles of 128 x 192, 128 x 256, 128 x 128 and 128 x 64
+@pytest.mark.parametrize("counts,N", [([700, 0, 129, 1, 900], 4001), ([100] * 19 + [191], 4000), ([33, 64, 40, 1, 60], 7000),
+                                      ([30] * 20, 1000)], ids=["192", "256", "128", "64"])
+def test_experts_that_fill_the_chip(counts, N):
+    K, R = 272, sum(counts) + 150
+    off, xq, xs, wq, ws, b = expert_case(counts, N, K, R, N)
+    y = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)
+    assert not y[sum(counts):].any()
+    a = 0
+    for e, c in enumerate(counts):
+        if c:
+            check_product(y[a:a + c], product64(xq[a:a + c], wq[e]), xs[a:a + c], ws[e], b[e])
+        a += c
 
 
 def test_experts_any_width_and_no_rows():

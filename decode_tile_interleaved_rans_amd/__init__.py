@@ -599,6 +599,15 @@ def gemm_int8_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream
 
 
 # ------------------------------------------------------------------------------------ expert routing
+def _no_tangents(*tensors):
+    """Refuses the dual tensors of forward-mode differentiation: they do not require a gradient, so the
+    kernels would drop their tangents without a word."""
+    unpack = _torch().autograd.forward_ad.unpack_dual
+    for t in tensors:
+        if t is not None and unpack(t).tangent is not None:
+            raise ValueError("the expert routing has no forward-mode derivative; use reverse mode")
+
+
 def _sort_raw(x, ids, n_experts):
     torch = _torch()
     T, k = ids.shape
@@ -650,6 +659,7 @@ def _routing_functions():
             @once
             def backward(ctx, d_rows):
                 # a token's gradient is the sum of its rows'; dropped choices have no part in it
+                _no_tangents(d_rows)
                 (pos,) = ctx.saved_tensors
                 return _combine_raw(d_rows.contiguous(), pos, None), None, None
 
@@ -665,6 +675,7 @@ def _routing_functions():
             @once
             def backward(ctx, dy):
                 ys, pos, weights = ctx.saved_tensors
+                _no_tangents(dy)
                 dy = dy.contiguous()
                 T, k = pos.shape
                 H = dy.shape[1]
@@ -684,11 +695,13 @@ def sort_tokens(x, expert_ids, n_experts: int, stream=None):
     than H), expert_ids: [T, k] int32 or int64; a number outside 0 ... n_experts - 1 drops the choice.
     Returns (rows [T k, H], offsets [n_experts + 1] int32, pos [T, k] int32): expert e has rows offsets[e]
     ... offsets[e + 1] - 1, in the order of the choices; choice (t, j) is row pos[t, j], or dropped, with
-    pos[t, j] = -1 - row of a zero row behind the last expert's. Differentiable in x; the host waits for
-    nothing. On `stream` (default: the current stream; another stream first waits for the current one)."""
+    pos[t, j] = -1 - row of a zero row behind the last expert's. Differentiable in x (reverse mode; dual
+    tensors are refused); the host waits for nothing. On `stream` (default: the current stream; another
+    stream first waits for the current one)."""
     torch = _torch()
     if stream is not None:
         return _on_stream(stream, lambda: sort_tokens(x, expert_ids, n_experts), x, expert_ids)
+    _no_tangents(x)
     if expert_ids.dim() != 2 or expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError("expert_ids must be an int32 or int64 tensor of shape [tokens, choices]")
     _need(expert_ids, "expert_ids", expert_ids.dtype)
@@ -707,11 +720,13 @@ def combine_tokens(ys, pos, weights=None, stream=None):
     """The experts' rows summed back per token: y[t] = sum over j of weights[t, j] ys[pos[t, j]] in fp32,
     rounded once to the rows' type; dropped choices are left out, and without weights they are 1. ys:
     [T k, H] BF16, FP16 or FP32 (more rows are allowed where no gradient is wanted), pos: sort_tokens'
-    positions [T, k], weights: fp32 [T, k]. Differentiable in ys and weights. On `stream` (default: the
-    current stream; another stream first waits for the current one)."""
+    positions [T, k], weights: fp32 [T, k]. Differentiable in ys and weights (reverse mode; dual tensors
+    are refused). On `stream` (default: the current stream; another stream first waits for the current
+    one)."""
     torch = _torch()
     if stream is not None:
         return _on_stream(stream, lambda: combine_tokens(ys, pos, weights), ys, pos, weights)
+    _no_tangents(ys, weights)
     if ys.dim() != 2 or ys.dtype not in _float_types():
         raise ValueError(f"ys must be a bfloat16, float16 or float32 matrix, got {ys.dtype} of shape {tuple(ys.shape)}")
     _need(ys, "ys", ys.dtype)

@@ -159,3 +159,30 @@ def test_fused_int8_rounding_formula():
         half = np.float32(np.float64(np.float32(0.25) * inv) + 0.5)
         t = (q.astype(np.float64) * np.float64(inv) + np.float64(half)).astype(np.float32)
         assert np.array_equal(np.trunc(t).astype(np.int64), (2 * q + k) // (2 * k)), k
+
+
+def test_routing_refuses_forward_mode():
+    """A dual tensor does not require a gradient, so nothing else would tell that its tangent is lost."""
+    fw = torch.autograd.forward_ad
+    x, ids, pos = torch.randn(4, 8), torch.zeros((4, 1), dtype=torch.int64), torch.zeros((4, 1), dtype=torch.int32)
+    with fw.dual_level():
+        dual = fw.make_dual(x, torch.ones_like(x))
+        weights = fw.make_dual(torch.ones(4, 1), torch.ones(4, 1))
+        assert not dual.requires_grad
+        for call in (lambda: ep.sort_tokens(dual, ids, 4), lambda: ep.combine_tokens(dual, pos),
+                     lambda: ep.combine_tokens(x, pos, weights)):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()
+    with pytest.raises(ValueError, match="forward-mode"):
+        torch.func.jvp(lambda v: ep.sort_tokens(v, ids, 4)[0], (x,), (x,))
+    # the gradients of the rows and of the sums, which may be dual where their inputs were not
+    sort, combine = ep._routing_functions()
+
+    class Saved:
+        saved_tensors = (None, pos, None)
+
+    with fw.dual_level():
+        for f in (sort, combine):
+            with pytest.raises(ValueError, match="forward-mode"):
+                Saved.saved_tensors = (pos,) if f is sort else (None, pos, None)
+                f.backward(Saved, fw.make_dual(x, x))

@@ -164,7 +164,17 @@ __global__ __launch_bounds__(256) void quantize_rows_i8(const void* Xv, int M, i
         const bool bad = a >= inf_bits<SRC>();
         if (a == 0 || bad) {
             if (t == 0) S[m] = bad ? __builtin_nanf("") : 0.0f;
-            for (int k = t; k < K; k += TPR) q[k] = 0;
+            // in the codes' own pieces: a row may have 2^31 - 1 codes, and padding tokens are rows of zeros
+            auto clear = [&](auto k) { __builtin_memset(q + start(k), 0, V); };
+            if constexpr (CH > 0) {
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    const int k = V * (t + TPR * c);
+                    if (k < K) clear(k);
+                }
+            } else {
+                for (int64_t k = V * t; k < K; k += V * TPR) clear(k);
+            }
             continue;
         }
         amax = fmaxf(amax, 0x1p-100f);

@@ -99,6 +99,41 @@ def test_quantizer_special_rows(K, dtype):
     assert s[1] == 0 and s[6] == 0
 
 
+@pytest.mark.parametrize("K", [1, 7, 8, 9, 511, 1025, 2049, 8193, 16385, 40003])
+def test_quantizer_clears_its_own_rows(K):
+    # zero rows and rows without a scale between ordinary ones, in memory that held something else
+    M = 9
+    x = torch.randn((M, K), generator=gen(K), device="cuda").to(torch.bfloat16)
+    x[1:3] = 0
+    x[5, K - 1], x[7, 0] = float("nan"), float("inf")
+    held = torch.full((M * K + 64,), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M,), 5.0, device="cuda")
+    q = held[32:32 + M * K].view(M, K)
+    ep._check(ep.lib().ep_quantize_rows_int8(x.data_ptr(), ep.BF16, M, K, K, q.data_ptr(), s.data_ptr(),
+                                             torch.cuda.current_stream().cuda_stream), "ep_quantize_rows_int8")
+    good = [0, 3, 4, 6, 8]
+    wq, ws = reference_codes(x[good])
+    assert torch.equal(q[good], wq) and torch.equal(s[good], ws)
+    assert not q[[1, 2, 5, 7]].any() and not s[1:3].any() and s[[5, 7]].isnan().all()
+    assert (held[:32] == 77).all() and (held[32 + M * K:] == 77).all()
+
+
+def test_quantizer_longest_row():
+    # 2^31 - 1 elements: a step behind the last of them leaves 32 bits
+    K = 2 ** 31 - 1
+    x = torch.zeros((1, K), dtype=torch.bfloat16, device="cuda")
+    held = torch.full((K + 1 + 64,), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((1,), 5.0, device="cuda")
+    for last in (0.0, float("inf"), -3.0):
+        held.fill_(77)
+        x[0, K - 1] = last
+        ep._check(ep.lib().ep_quantize_rows_int8(x.data_ptr(), ep.BF16, 1, K, K, held.data_ptr() + 32, s.data_ptr(),
+                                                 torch.cuda.current_stream().cuda_stream), "ep_quantize_rows_int8")
+        assert int(held[32 + K - 1]) == (-127 if last == -3.0 else 0) and not held[32:32 + K - 1].any()
+        assert (held[:32] == 77).all() and (held[32 + K:] == 77).all()
+        assert s.isnan().all() if last == float("inf") else float(s) == float(np.float32(abs(last)) / np.float32(127))
+
+
 def test_quantizer_row_strides_and_offsets():
     base = torch.randn((20, 3000), generator=gen(4), device="cuda").to(torch.bfloat16)
     for x in (base[:, 8:1032], base[:, 3:1000], base[::2, :512], base[4:5, 1:9], base[:, :1]):

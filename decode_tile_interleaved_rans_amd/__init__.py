@@ -651,13 +651,18 @@ def _routing_functions():
 
         class SortTokens(torch.autograd.Function):
             @staticmethod
-            def forward(ctx, x, rows, pos):
+            def forward(ctx, x, ids, n_experts):
+                rows, offsets, pos = _sort_raw(x, ids, n_experts)
+                ctx.mark_non_differentiable(offsets, pos)
+                ctx.set_materialize_grads(False)             # no zeros are made for offsets and pos
                 ctx.save_for_backward(pos)
-                return rows.view_as(rows)
+                return rows, offsets, pos
 
             @staticmethod
             @once
-            def backward(ctx, d_rows):
+            def backward(ctx, d_rows, *_):
+                if d_rows is None:
+                    return None, None, None
                 # a token's gradient is the sum of its rows'; dropped choices have no part in it
                 _no_tangents(d_rows)
                 (pos,) = ctx.saved_tensors
@@ -710,10 +715,9 @@ def sort_tokens(x, expert_ids, n_experts: int, stream=None):
     grad = x.requires_grad and torch.is_grad_enabled()
     if grad and x.dtype not in _float_types():
         raise ValueError(f"rows of {x.dtype} have no gradient; detach x")
-    rows, offsets, pos = _sort_raw(x, expert_ids, n_experts)
     if grad:
-        rows = _routing_functions()[0].apply(x, rows, pos)
-    return rows, offsets, pos
+        return _routing_functions()[0].apply(x, expert_ids, n_experts)
+    return _sort_raw(x, expert_ids, n_experts)
 
 
 def combine_tokens(ys, pos, weights=None, stream=None):

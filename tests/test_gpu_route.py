@@ -343,6 +343,31 @@ def test_rows_past_32_bit_offsets():
     assert ((d_w.double() - ref).abs() <= (H + 8) * U * ref).all()
 
 
+def test_rows_can_be_changed_in_place():
+    # the sorted rows are the caller's own, with and without a gradient: an in-place step on them is a step of
+    # the graph, as on rows taken by an index
+    T, k, E, H = 37, 3, 5, 72
+    ids, w = choices(T, k, E, 2), torch.rand((T, k), generator=gen(3), device="cuda")
+    x = torch.randn((T, H), generator=gen(1), device="cuda")
+    dy = torch.randn((T, H), generator=gen(4), device="cuda")
+    outs, grads = [], []
+    for grad in (False, True):
+        leaf = x.clone().requires_grad_(grad)
+        rows, off, pos = ep.sort_tokens(leaf, ids, E)
+        assert rows.requires_grad == grad and not off.requires_grad and not pos.requires_grad
+        rows.mul_(3.0)
+        rows += 1.0
+        torch.nn.functional.dropout(rows, 0.0, inplace=True)
+        outs.append(ep.combine_tokens(rows, pos, w))
+        if grad:
+            (dx,) = torch.autograd.grad(outs[1], leaf, dy)
+    assert torch.equal(outs[0], outs[1].detach())
+    taken = ((ids >= 0) & (ids < E)).double() * w.double()
+    ref = 3.0 * dy.double() * taken.sum(1, keepdim=True)
+    # a row's gradient w dy and its triple, each one rounding, then k sums
+    assert ((dx.double() - ref).abs() <= (k + 2) * U * 3.0 * dy.double().abs() * taken.sum(1, keepdim=True)).all()
+
+
 def test_second_derivative_is_refused():
     x = torch.randn((6, 16), device="cuda").requires_grad_(True)
     ids = choices(6, 2, 3, 1)

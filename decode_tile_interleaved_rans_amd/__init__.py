@@ -544,6 +544,9 @@ def pad_rows_int8(codes, stream=None):
     return out
 
 
+_I8_MAX_K = 131056                   # the widest codes whose sums stay within int32 however they are laid out
+
+
 def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype):
     torch = _torch()
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
@@ -563,7 +566,8 @@ def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype):
     for name, t, dtype, shape in args:
         if not _fits(t, dtype, shape, dev):
             _need(t, name, dtype, shape=shape)
-    if K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16:
+    # wider codes than the products take are refused below, not copied first
+    if K <= _I8_MAX_K and (K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16):
         xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
         K = xq.shape[1]
     y = torch.empty((M, lead[-1]), dtype=out_dtype, device=xq.device)
@@ -580,8 +584,8 @@ def gemm_int8(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
     """Y = diag(xs) Xq Wq^T diag(ws) (+ bias) from INT8 codes xq [M, K] and wq [N, K] with a scale per
     token xs [M] and per channel ws [N] (quantize_rows_int8; a weight's codes and scales come from
     Handle.decompress(torch.int8)); exact int32 sums, output BF16 (default), FP16 or FP32. K a multiple
-    of 16 and 16-byte aligned codes are read in place, others are laid out first (pad_rows_int8). On
-    `stream` (default: the current stream; another stream first waits for the current one)."""
+    of 16 and 16-byte aligned codes are read in place, others are laid out first (pad_rows_int8). K is at
+    most 131056. On `stream` (default: the current stream; another stream first waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype), xq, xs, wq, ws, bias)
     return _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype)

@@ -530,8 +530,8 @@ ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const f
     if (M < 0 || N < 0 || K < 0) return fail(EP_EINVAL, "negative size");
     if (out != EP_BF16 && out != EP_F16 && out != EP_F32)
         return fail(EP_EUNSUPPORTED, "the INT8 product writes BF16, F16 or F32");
+    if (K > ep::kI8MaxK) return fail(EP_ERANGE, "K above 131056: the int32 sums could overflow");
     if (K % 16) return fail(EP_EINVAL, "K must be a multiple of 16 (ep_pad_rows_int8 lays other rows out)");
-    if (K > ep::kI8MaxK) return fail(EP_ERANGE, "K above 131071: the int32 sums could overflow");
     if (M == 0 || N == 0) return EP_OK;
     if ((K > 0 && (!xq || !wq)) || !xs || !ws || !y) return fail(EP_EINVAL, "null pointer");
     if (M > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "M and N must be below 2^31");
@@ -1174,7 +1174,7 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
         if (!dev_y || (K > 0 && !dev_x)) return fail(EP_EINVAL, "null pointer");
         if (M > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "M and out_features must be below 2^31");
         if (K % 16) return fail(EP_EINVAL, "in_features must be a multiple of 16 for the INT8 forward");
-        if (K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131071: the int32 sums could overflow");
+        if (K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131056: the int32 sums could overflow");
         if (reinterpret_cast<uintptr_t>(dev_x) & 15) return fail(EP_EINVAL, "X must be 16-byte aligned");
         hipStream_t s = static_cast<hipStream_t>(hip_stream);
         int dev = 0;
@@ -1333,7 +1333,7 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
         if (!dev_y || (K > 0 && !dev_x) || (compute == EP_I8 && !dev_offsets)) return fail(EP_EINVAL, "null pointer");
         if (R > INT32_MAX || N > INT32_MAX) return fail(EP_ERANGE, "the rows and out_features must be below 2^31");
         if (K % (compute == EP_BF16 ? 8 : 16)) return fail(EP_EINVAL, "in_features must be a multiple of 8 (16 in FP8 and INT8)");
-        if (compute == EP_I8 && K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131071: the int32 sums could overflow");
+        if (compute == EP_I8 && K > ep::kI8MaxK) return fail(EP_ERANGE, "in_features above 131056: the int32 sums could overflow");
         if (reinterpret_cast<uintptr_t>(dev_x) & 15) return fail(EP_EINVAL, "X must be 16-byte aligned");
         hipStream_t s = static_cast<hipStream_t>(hip_stream);
         int dev = 0;

@@ -8,9 +8,10 @@
 
 namespace ep {
 
-// Largest K of an INT8 product: 131071 products of two codes, each at most 2^14 in magnitude (-128
-// squared), stay below 2^31, so the int32 sums are exact.
-constexpr int64_t kI8MaxK = 131071;
+// Largest K of an INT8 product, the largest multiple of 16 below 2^17: that many products of two codes, each at
+// most 2^14 in magnitude (-128 squared), stay below 2^31, so the int32 sums are exact. A longer row would be
+// laid out to 2^17 codes, which nothing tells from a row whose sum leaves int32.
+constexpr int64_t kI8MaxK = 131056;
 
 // Per-row INT8 quantization of rows of `src` elements (ep_dtype EP_F32, EP_BF16 or EP_F16):
 // Q [M][K], S [M]; see quantize_rows_i8 in int8.hip for the rule. Rows of X are ldx elements apart;

@@ -354,7 +354,7 @@ ep_status ep_quantize_rows_int8(const void* dev_x, ep_dtype src, int64_t M, int6
  * Checks", section "Replace one linear layer before a whole model".
  * xq [M][K] and wq [N][K] int8 codes (16-byte aligned), xs [M] and ws [N] fp32, bias [N] bf16 or NULL, Y
  * [M][N] elements of out (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise). Requires K % 16 == 0
- * (EP_EINVAL; ep_pad_rows_int8 lays other rows out) and K <= 131071 (EP_ERANGE: longer sums could leave
+ * (EP_EINVAL; ep_pad_rows_int8 lays other rows out) and K <= 131056 (EP_ERANGE: longer sums could leave
  * int32); M and N below 2^31 (EP_ERANGE). The library's own kernels; asynchronous on hip_stream;
  * allocates nothing. */
 ep_status ep_gemm_int8(const int8_t* dev_xq, const float* dev_xs, const int8_t* dev_wq, const float* dev_ws, int64_t M,
@@ -393,7 +393,7 @@ ep_status ep_pad_rows_int8(const int8_t* dev_src, int64_t rows, int64_t K, int8_
  * before a whole model".
  * dev_x: [M][K] bf16, 16-byte aligned (may be NULL when K == 0); dev_bias: [N] bf16 or NULL; dev_y: [M][N]
  * bf16. K == 0 gives Y = bias (or zeros). Requires a lossy stream and K % 16 == 0 (EP_EINVAL), K <=
- * 131071, M and N below 2^31 (EP_ERANGE). Workspace rules of ep_linear_forward. Asynchronous on
+ * 131056, M and N below 2^31 (EP_ERANGE). Workspace rules of ep_linear_forward. Asynchronous on
  * hip_stream. */
 ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t M, const void* dev_bias, void* dev_y,
                                  void* hip_stream);

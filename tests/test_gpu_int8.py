@@ -225,6 +225,23 @@ def test_empty_sum_and_empty_sides(M):
     assert ep.gemm_int8(xq, xs, wq[:0], ws[:0]).shape == (M, 0)
 
 
+def test_widest_product_and_the_first_refused():
+    # 131056 codes are the longest row whose laid-out width keeps the sums within int32; the next are refused
+    # before anything is copied
+    for K in (131055, 131056):
+        xq, xs, wq, ws, b = operands(3, 5, K, 1, full=True)
+        check_product(ep.gemm_int8(xq, xs, wq, ws, b), product64(xq, wq), xs, ws, b)
+    off = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    for K in (131057, 131071, 131072):
+        xq, xs, wq, ws, b = operands(3, 5, K, 1)
+        for call in (lambda: ep.gemm_int8(xq, xs, wq, ws), lambda: ep.gemm_int8_experts(xq, xs, wq[None], ws[None], off)):
+            torch.cuda.reset_peak_memory_stats()
+            before = torch.cuda.memory_allocated()
+            with pytest.raises(ep.EPError, match="131056"):
+                call()
+            assert torch.cuda.max_memory_allocated() - before < K
+
+
 def test_bad_rows_stay_bad():
     # a row with a NaN has scale NaN: its outputs are NaN and no other row's are
     x = torch.randn((70, 128), generator=gen(6), device="cuda").to(torch.bfloat16)

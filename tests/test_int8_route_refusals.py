@@ -186,3 +186,10 @@ def test_routing_refuses_forward_mode():
             with pytest.raises(ValueError, match="forward-mode"):
                 Saved.saved_tensors = (pos,) if f is sort else (None, pos, None)
                 f.backward(Saved, fw.make_dual(x, x))
+
+
+@pytest.mark.parametrize("K", [131057, 131071, 131072, I31])
+def test_widths_past_the_exact_sums(K):
+    L = ep.lib()
+    assert L.ep_gemm_int8(P, P, P, P, 4, 4, K, None, ep.BF16, P, None) == ERANGE and b"131056" in L.ep_last_error()
+    assert L.ep_gemm_int8_experts(P, P, P, P, P, 2, 4, 4, K, None, ep.BF16, P, None) == ERANGE

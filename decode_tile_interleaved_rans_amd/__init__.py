@@ -538,9 +538,15 @@ def pad_rows_int8(codes, stream=None):
     # rows that begin inside a 128-byte line cost the product's loads two lines a piece: 333 x 5003 from
     # rows of 3856 codes 17.9 us, of 3968 16.2
     step = 128 if 1024 <= K <= 130944 else 16
-    rows, ld = codes.numel() // K if K else 0, (K + step - 1) // step * step
-    out = torch.empty((*codes.shape[:-1], ld), dtype=torch.int8, device=codes.device)
-    _check(lib().ep_pad_rows_int8(_ptr(codes), rows, K, _ptr(out), ld, _current_raw()), "ep_pad_rows_int8")
+    return _lay_out(codes, (K + step - 1) // step * step)
+
+
+def _lay_out(codes, ld: int):
+    """Contiguous codes [..., K] in new memory, 16-byte aligned, in rows of ld >= K codes."""
+    K = codes.shape[-1]
+    out = _torch().empty((*codes.shape[:-1], ld), dtype=codes.dtype, device=codes.device)
+    _check(lib().ep_pad_rows_int8(_ptr(codes), codes.numel() // K if K else 0, K, _ptr(out), ld, _current_raw()),
+           "ep_pad_rows_int8")
     return out
 
 
@@ -567,9 +573,13 @@ def _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype):
         if not _fits(t, dtype, shape, dev):
             _need(t, name, dtype, shape=shape)
     # wider codes than the products take are refused below, not copied first
-    if K <= _I8_MAX_K and (K % 16 or (xq.data_ptr() | wq.data_ptr()) % 16):
+    if K % 16 and K <= _I8_MAX_K:
         xq, wq = pad_rows_int8(xq), pad_rows_int8(wq)
         K = xq.shape[1]
+    elif K <= _I8_MAX_K:
+        # a weight is read in place whatever the activations' address, and the other way round
+        xq = _lay_out(xq, K) if xq.data_ptr() % 16 else xq
+        wq = _lay_out(wq, K) if wq.data_ptr() % 16 else wq
     y = torch.empty((M, lead[-1]), dtype=out_dtype, device=xq.device)
     tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), _current_raw())
     if offsets is None:
@@ -584,8 +594,8 @@ def gemm_int8(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
     """Y = diag(xs) Xq Wq^T diag(ws) (+ bias) from INT8 codes xq [M, K] and wq [N, K] with a scale per
     token xs [M] and per channel ws [N] (quantize_rows_int8; a weight's codes and scales come from
     Handle.decompress(torch.int8)); exact int32 sums, output BF16 (default), FP16 or FP32. K a multiple
-    of 16 and 16-byte aligned codes are read in place, others are laid out first (pad_rows_int8). K is at
-    most 131056. On `stream` (default: the current stream; another stream first waits for the current one)."""
+    of 16 and 16-byte aligned codes are read in place; other widths of both operands, and an operand at
+    another address, are laid out first (pad_rows_int8). K is at most 131056. On `stream` (default: the current stream; another stream first waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype), xq, xs, wq, ws, bias)
     return _gemm_int8(xq, xs, wq, ws, None, bias, out_dtype)

@@ -254,6 +254,35 @@ def test_bad_rows_stay_bad():
     assert nan[13].all() and nan[44].all() and int(nan.sum()) == 180
 
 
+@pytest.mark.parametrize("K", [1024, 1040, 272])
+@pytest.mark.parametrize("which", ["x", "w", "both"])
+def test_only_misaligned_codes_are_copied(which, K):
+    E, R, N = 4, 20, 512
+    xq, xs, _, _, _ = operands(R, 1, K, 5)
+    wq, ws, b = zip(*(operands(1, N, K, 6 + e)[2:] for e in range(E)))
+    wq, ws, b = torch.stack(wq), torch.stack(ws), torch.stack(b)
+    off = torch.tensor([0, 3, 3, 11, 20], dtype=torch.int32, device="cuda")
+
+    def moved(t):
+        flat = torch.empty(t.numel() + 3, dtype=t.dtype, device="cuda")
+        flat[3:] = t.reshape(-1)
+        return flat[3:].view(t.shape)
+
+    x2, w2 = moved(xq) if which != "w" else xq, moved(wq) if which != "x" else wq
+    want, one = ep.gemm_int8_experts(xq, xs, wq, ws, off, b), ep.gemm_int8(xq, xs, wq[1], ws[1], b[1])
+    small, large = xq.numel(), wq.numel()
+    for call, ref, weight in ((lambda: ep.gemm_int8_experts(x2, xs, w2, ws, off, b), want, large),
+                              (lambda: ep.gemm_int8(x2, xs, w2[1], ws[1], b[1]), one, large // E)):
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        assert torch.equal(call(), ref)
+        used = torch.cuda.max_memory_allocated() - before
+        room = 2 * ref.numel() + ref.numel() + 8192            # the output, its comparison, the allocator's units
+        assert used <= room + (small if which != "w" else 0) + (weight if which != "x" else 0)
+        assert used >= (weight if which != "x" else 0)
+
+
 def test_rows_do_not_depend_on_their_batch():
     # exact sums: a row's outputs are the same bits whatever the other rows and the kernel chosen
     xq, xs, wq, ws, b = operands(4200, 1100, 528, 12)

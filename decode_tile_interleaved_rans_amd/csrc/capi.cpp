@@ -450,9 +450,11 @@ ep_status int8_experts(const ep_handle* const* w, int count, const uint16_t* x, 
             e = ep::launch_gather_bias(b, m, (int)N, bias + (size_t)i * (size_t)N, s);
         }
         if (e != hipSuccess) return hip_fail(e, "grouped expert decode launch");
-        // rows up to the chunk's last expert's: none is left behind it for the product to clear
+        // rows up to the chunk's last expert's: none is left behind it for the product to clear; the tile goes by
+        // the chunk's own
         const ep::GemmI8Args g{xq, xs, wq, wsc, biased ? bias : nullptr, y, dev_offsets + e0, (int)host_offsets[e0 + n],
-                               (int)N, (int)K, (int)K, (int)K, (int)N, n, EP_BF16};
+                               (int)N, (int)K, (int)K, (int)K, (int)N, n, EP_BF16,
+                               (int)(host_offsets[e0 + n] - host_offsets[e0])};
         e = ep::launch_gemm_i8(g, s);
         if (e != hipSuccess) return hip_fail(e, "expert int8 gemm launch");
     }
@@ -539,7 +541,7 @@ ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const f
         return fail(EP_EINVAL, "X and W codes must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(y) & (out == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "Y is not aligned to its elements");
     const ep::GemmI8Args g{xq, xs, wq, ws, static_cast<const uint16_t*>(bias), y, offsets, (int)M, (int)N, (int)K,
-                           (int)K, (int)K, (int)N, experts, out};
+                           (int)K, (int)K, (int)N, experts, out, (int)M};
     const hipError_t e = ep::launch_gemm_i8(g, s);
     if (e == hipErrorInvalidValue) return fail(EP_ERANGE, "M x N is too large for one launch");
     return e == hipSuccess ? EP_OK : hip_fail(e, "int8 gemm launch");
@@ -1236,7 +1238,7 @@ ep_status ep_linear_forward_int8(const ep_handle* w, const void* dev_x, int64_t 
             if (e != hipSuccess) return hip_fail(e, "slice decode launch");
             ep::GemmI8Args g{xq, xs, wq, wsc, dev_bias ? static_cast<const uint16_t*>(dev_bias) + r0 : nullptr,
                              static_cast<uint16_t*>(dev_y) + r0, nullptr, (int)M, (int)rows, (int)K, (int)K, (int)K, (int)N,
-                             0, EP_BF16};
+                             0, EP_BF16, (int)M};
             e = ep::launch_gemm_i8(g, s);
             if (e != hipSuccess) return hip_fail(e, "slice int8 gemm launch");
         }

@@ -31,6 +31,8 @@ struct GemmI8Args {
     int M, N, K, ldx, ldw, ldy;
     int experts;            // 0: one weight for all rows
     int out;                // ep_dtype EP_BF16, EP_F16 or EP_F32
+    int rows;               // rows that the tile and the grid are made for: M, or, with offsets that begin past 0, no
+                            // less than the rows from offsets[0] on
 };
 
 // Requires K % 16 == 0 and 16-byte aligned rows (ldx, ldw multiples of 16, aligned bases) and K at most

@@ -636,12 +636,12 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
     else store_tile<EP_F32, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
 }
 
-// Tiles of BM rows that M rows split over the experts can need: every range adds at most one partly
+// Tiles of BM rows that the rows split over the experts can need: every range adds at most one partly
 // filled tile (the rows behind the last expert's are a range of their own).
 int64_t row_tiles(const GemmI8Args& g, int bm) {
     if (!g.experts) return ((int64_t)g.M + bm - 1) / bm;
-    const int64_t most = (int64_t)g.M / bm + g.experts + 1;
-    return most < g.M ? most : g.M;
+    const int64_t most = (int64_t)g.rows / bm + g.experts + 1;
+    return most < g.rows ? most : g.rows;
 }
 
 template <int BM, int BN, int WGM, int WGN, int S, int KS>
@@ -712,7 +712,7 @@ const TileCost kTiles[] = {
 constexpr float kTileUs = 1.5f;             // start and epilogue of a tile
 
 hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
-    if (g.M <= 0 || g.N <= 0) return hipSuccess;
+    if (g.M <= 0 || g.N <= 0 || g.rows <= 0) return hipSuccess;
     if (!g.experts) {
         const TileCost* best = nullptr;
         float least = 0.0f;
@@ -731,7 +731,7 @@ hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
     // 128 x 256 75 (128 x 192: 87), and from 192 rows on 128 x 192, two blocks to a CU, so that one's start and end run
     // behind the other's MFMAs: 512 rows of 2048 x 4096 181 (128 x 256: 184, 256 x 256: 191, 128 x 128: 195), 375 rows of
     // 16 experts of 4096 x 2048 70 (128 x 256: 83), 2048 rows of 4 of 2048 x 2048 46 (61).
-    const int64_t used = g.M < g.experts ? g.M : g.experts, rows = (g.M + used - 1) / used;
+    const int64_t used = g.rows < g.experts ? g.rows : g.experts, rows = (g.rows + used - 1) / used;
     auto fills = [&](int bm, int bn) { return used * ((rows + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn) >= device_cus(); };
     if (rows >= 192 && fills(128, 192)) return tiled_go<128, 192, 2, 4, 2, 1>(g, stream);
     if (rows > 64 && fills(128, 256)) return tiled_go<128, 256, 2, 4, 3, 1>(g, stream);

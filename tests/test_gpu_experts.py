@@ -123,6 +123,39 @@ def test_int8_experts_beyond_one_chunk():
     check(layers, tokens(T, K, 4), ids, None)
 
 
+def test_int8_chunks_of_several_experts():
+    # 4 MiB of codes per expert, 64 experts to a chunk: three chunks, in each some experts without rows, some with
+    # a bias, one of many rows in the last
+    E, N, K, T = 150, 2048, 2048, 600
+    streams = [ep.compress_device(W.gpu_student_t(N, K, 3 + i), 3.0, layout=i % 2, prob_bits=11)[0] for i in range(3)]
+    layers = [ep.CompressedLinear(streams[e % 3], None, "int8") for e in range(E)]
+    for e in range(0, E, 7):
+        layers[e].bias = torch.randn(N, generator=gen(e), device="cuda").to(torch.bfloat16)
+    ids = torch.randint(0, E, (T, 2), generator=gen(5), device="cuda")
+    ids = torch.where((ids % 11 == 3) | ((ids >= 60) & (ids < 70)), -1, ids)
+    ids[:90, 0] = 140
+    check(layers, tokens(T, K, 3), ids, torch.rand((T, 2), generator=gen(6), device="cuda"))
+
+
+def test_int8_chunks_take_the_tile_of_their_own_rows():
+    # three chunks of 64 experts with 8 rows each: the same product of every chunk, so the same kernel on the same
+    # grid, whatever the chunks before it held
+    E, N, K = 192, 2048, 2048
+    s, _ = ep.compress_device(W.gpu_student_t(N, K, 3), 3.0, layout=0, prob_bits=11)
+    layers = [ep.CompressedLinear(s, None, "int8")] * E
+    x = tokens(8 * E, K, 4)
+    ids = torch.arange(8 * E, device="cuda")[:, None] % E
+    want = layers[0](x)
+    ep.linear_forward_experts(layers, x, ids)                  # the workspace
+    torch.cuda.synchronize()
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as prof:
+        y = ep.linear_forward_experts(layers, x, ids)
+        torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    products = [e.name for e in prof.events() if "gemm_i8" in e.name]
+    assert len(products) == 3 and len(set(products)) == 1, products
+
+
 def test_wide_values_divide_in_int8():
     # rows whose largest |q| passes 127 (large targets): the INT8 container divides them
     E, N, K = 2, 64, 1024

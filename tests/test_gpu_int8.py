@@ -359,6 +359,35 @@ def test_experts_wrong_offsets_stay_inside():
     torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("R", [40, 300])
+@pytest.mark.parametrize("out", TYPES)
+def test_experts_wrong_offsets_write_nothing_outside(R, out):
+    # Y in the middle of a larger buffer: whatever the offsets say, no row before or behind it changes, and the
+    # calls after them are right again
+    E, N, K, guard = 3, 100, 64, 96
+    xq, xs, wq, ws, b = operands(R, E * N, K, 8)
+    held = torch.full((guard + R + guard, N), 7.0, dtype=out, device="cuda")
+    y, code = held[guard:guard + R], {torch.bfloat16: ep.BF16, torch.float16: ep.F16, torch.float32: ep.F32}[out]
+
+    def call(offs):
+        off = torch.tensor(offs, dtype=torch.int32, device="cuda")
+        ep._check(ep.lib().ep_gemm_int8_experts(xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(), off.data_ptr(), E, R,
+                                                N, K, b.data_ptr(), code, y.data_ptr(), torch.cuda.current_stream().cuda_stream),
+                  "ep_gemm_int8_experts")
+        assert (held[:guard] == 7).all() and (held[guard + R:] == 7).all()
+
+    top = 2 ** 31 - 1
+    for offs in ([0, 5, 3, R], [0, R + 50, 7, 20], [-5, 1, 2, 3], [0, 0, 0, top], [R - 1, R + 1, R + 60, R + 95], [top] * 4,
+                 [-top - 1, -1, top, -top], [R, R, R, R], [20, 10, 5, 0]):
+        call(offs)
+    call([0, 11, 11, R - 4])
+    for e, (a, z) in enumerate(((0, 11), (11, 11), (11, R - 4))):
+        if z > a:
+            part = slice(e * N, (e + 1) * N)
+            check_product(y[a:z], product64(xq[a:z], wq[part]), xs[a:z], ws[part], b[part])
+    assert not y[R - 4:].any()
+
+
 def test_experts_take_new_offsets_in_a_captured_graph():
     off, xq, xs, wq, ws, b = expert_case([10, 0, 30, 8], 200, 256, 64, 15)
     y = ep.gemm_int8_experts(xq, xs, wq, ws, off, b)           # warm up

@@ -421,6 +421,47 @@ def test_from_several_threads():
     assert not errors, errors
 
 
+def test_threads_end_and_agree():
+    # as above, and every worker has to come to its end: one that hangs is a failure, not a silence
+    import threading
+    T, k, E, H = 900, 3, 16, 136
+    ids = choices(T, k, E, 9)
+    x = torch.randn((T, H), generator=gen(1), device="cuda")
+    w = torch.rand((T, k), generator=gen(2), device="cuda")
+    dy = torch.randn((T, H), generator=gen(3), device="cuda")
+
+    def work():
+        leaf, wl = x.clone().requires_grad_(True), w.clone().requires_grad_(True)
+        rows, off, pos = ep.sort_tokens(leaf, ids, E)
+        y = ep.combine_tokens(rows, pos, wl)
+        return rows.detach(), off, pos, y.detach(), *torch.autograd.grad(y, [leaf, wl], dy)
+
+    want = work()
+    torch.cuda.synchronize()
+    errors, ended = [], []
+
+    def run(i):
+        try:
+            torch.cuda.set_device(0)
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(5):
+                    got = work()
+                    torch.cuda.current_stream().synchronize()
+                    for a, b in zip(got, want):
+                        assert torch.equal(a, b)
+            ended.append(i)
+        except BaseException as e:
+            errors.append(repr(e))
+
+    threads = [threading.Thread(target=run, args=(i,), daemon=True) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=60)
+    assert not errors, errors
+    assert not any(t.is_alive() for t in threads) and sorted(ended) == [0, 1, 2, 3]
+
+
 # ------------------------------------------------------------------------------------ together
 @pytest.mark.parametrize("T", [1, 13, 600])
 def test_expert_layer_in_int8(T):

@@ -142,6 +142,9 @@ hipError_t launch_all(const std::vector<ep::MatDesc>& ds, hipStream_t stream) {
 // completed: when it must grow, or when its device has more than kMaxWsPerDevice entries and it
 // is the least recently used one (the stream it served may be gone; its event is still valid).
 // So no queued launch reads freed memory, and no caller holds a pointer that another frees.
+// A forward captured into a graph leaves the buffer's address in the graph, whose replays nothing here
+// sees: such a buffer is never freed (its entry moves on to a new one when it must grow) and no event is
+// recorded into the graph.
 struct WsEntry {
     int device;
     hipStream_t stream;
@@ -149,10 +152,13 @@ struct WsEntry {
     size_t bytes;
     hipEvent_t done;            // recorded behind the last forward that used the buffer
     uint64_t tick;              // last use, for eviction
+    bool in_graph;              // a captured forward holds ptr
 };
 constexpr int kMaxWsPerDevice = 4;
 std::mutex g_ws_mu;
 std::vector<WsEntry> g_ws;
+char g_no_stream;
+const hipStream_t kNoStream = reinterpret_cast<hipStream_t>(&g_no_stream);   // of a buffer that waits to be freed
 uint64_t g_ws_tick = 0;
 
 hipError_t ws_retire(WsEntry& e) {
@@ -164,11 +170,12 @@ hipError_t ws_retire(WsEntry& e) {
         e.done = nullptr;
     }
     if (e.ptr) {
-        const hipError_t r2 = hipFree(e.ptr);
+        const hipError_t r2 = e.in_graph ? hipSuccess : hipFree(e.ptr);
         if (r == hipSuccess) r = r2;
         e.ptr = nullptr;
     }
     e.bytes = 0;
+    e.in_graph = false;
     return r;
 }
 
@@ -180,9 +187,10 @@ struct WsLease {
     hipStream_t stream = nullptr;
     void* ptr = nullptr;
     size_t bytes = 0;
-    bool recorded = false;
+    bool recorded = false;      // (true from the start under stream capture)
     // After the forward's launches are queued: mark the buffer as in use by them.
     hipError_t queued() {
+        if (recorded) return hipSuccess;
         recorded = true;
         return entry ? hipEventRecord(entry->done, stream) : hipSuccess;
     }
@@ -196,10 +204,18 @@ struct WsLease {
 hipError_t ws_acquire(int device, hipStream_t stream, size_t need, WsLease* L) {
     L->lock = std::unique_lock<std::mutex>(g_ws_mu);
     L->stream = stream;
+    hipStreamCaptureStatus status = hipStreamCaptureStatusNone;        // (the null stream is never captured)
+    if (stream)
+        if (hipError_t r = hipStreamIsCapturing(stream, &status); r != hipSuccess) return r;
+    const bool capturing = status != hipStreamCaptureStatusNone;
     WsEntry* e = nullptr;
     for (WsEntry& x : g_ws)
         if (x.device == device && x.stream == stream) e = &x;
-    if (!e) {
+    if (e && capturing && e->bytes < need) {
+        e->stream = kNoStream;                           // a later eager call waits for it and frees it
+        e = nullptr;
+    }
+    while (!e && !capturing) {
         int count = 0;
         size_t lru = g_ws.size();
         for (size_t i = 0; i < g_ws.size(); ++i) {
@@ -207,12 +223,13 @@ hipError_t ws_acquire(int device, hipStream_t stream, size_t need, WsLease* L) {
             ++count;
             if (lru == g_ws.size() || g_ws[i].tick < g_ws[lru].tick) lru = i;
         }
-        if (count >= kMaxWsPerDevice) {
-            hipError_t r = ws_retire(g_ws[lru]);
-            g_ws.erase(g_ws.begin() + (std::ptrdiff_t)lru);
-            if (r != hipSuccess) return r;
-        }
-        WsEntry n{device, stream, nullptr, 0, nullptr, 0};
+        if (count < kMaxWsPerDevice) break;
+        hipError_t r = ws_retire(g_ws[lru]);
+        g_ws.erase(g_ws.begin() + (std::ptrdiff_t)lru);
+        if (r != hipSuccess) return r;
+    }
+    if (!e) {
+        WsEntry n{device, stream, nullptr, 0, nullptr, 0, false};
         hipError_t r = hipEventCreateWithFlags(&n.done, hipEventDisableTiming);
         if (r != hipSuccess) return r;
         g_ws.push_back(n);
@@ -220,12 +237,17 @@ hipError_t ws_acquire(int device, hipStream_t stream, size_t need, WsLease* L) {
     }
     if (e->bytes < need) {
         // earlier forwards on this stream may still read the old buffer: wait for them
-        hipError_t r = hipEventSynchronize(e->done);
-        if (r == hipSuccess && e->ptr) r = hipFree(e->ptr);
+        hipError_t r = capturing ? hipSuccess : hipEventSynchronize(e->done);
+        if (r == hipSuccess && e->ptr && !e->in_graph) r = hipFree(e->ptr);
         e->ptr = nullptr;
         e->bytes = 0;
+        e->in_graph = false;
         if (r != hipSuccess) return r;
+        // an allocation is no work of the captured graph
+        hipStreamCaptureMode mode = hipStreamCaptureModeRelaxed;
+        if (capturing && (r = hipThreadExchangeStreamCaptureMode(&mode)) != hipSuccess) return r;
         r = hipMalloc(&e->ptr, need);
+        if (capturing) (void)hipThreadExchangeStreamCaptureMode(&mode);
         if (r != hipSuccess) {
             e->ptr = nullptr;
             return r;
@@ -233,6 +255,8 @@ hipError_t ws_acquire(int device, hipStream_t stream, size_t need, WsLease* L) {
         e->bytes = need;
     }
     e->tick = ++g_ws_tick;
+    e->in_graph = e->in_graph || capturing;
+    L->recorded = capturing;
     L->entry = e;
     L->ptr = e->ptr;
     L->bytes = e->bytes;

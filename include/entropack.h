@@ -216,7 +216,9 @@ ep_status ep_decode_symbols(const ep_handle* h, int16_t* dev_q, void* hip_stream
  * The fused and slice paths multiply the same BF16-rounded weights. The workspace belongs
  * to the (device, hip_stream) pair: calls on one stream reuse it in order, calls on different
  * streams get different workspaces; it is allocated on first use
- * (hipMalloc, which may synchronize the device) and kept until the process ends.
+ * (hipMalloc, which may synchronize the device) and kept until the process ends. A captured
+ * call leaves its workspace to the graph, and it is not freed: replays, other graphs captured on
+ * that stream and eager calls on it have to be ordered by the caller.
  *   dev_x: [M][K] bf16, 16-byte aligned (may be NULL when K == 0); dev_bias: [N] bf16 or NULL;
  * dev_y: [M][N] bf16. K == 0 gives Y = bias (or zeros). Requires a lossy stream and K % 8 == 0
  * (EP_EINVAL); M and N below 2^31 (EP_ERANGE). Asynchronous on hip_stream. */

@@ -513,6 +513,83 @@ def test_compressed_forward_on_two_slices():
     assert torch.equal(layer(x), ep.gemm_int8(*ep.quantize_rows_int8(x), dq, ds))
 
 
+def layer_of(N, K, seed, compute):
+    s, _ = ep.compress_device(W.gpu_student_t(N, K, seed), 4.0, layout=ep.ROW_LAYOUT, prob_bits=11)
+    return ep.CompressedLinear(s, None, compute)
+
+
+@pytest.mark.parametrize("compute", ["bf16", "fp8", "int8"])
+@pytest.mark.parametrize("M", [20, 100])                       # fused, and slices with a product
+def test_captured_forwards_keep_their_workspace(M, compute):
+    """A graph holds the address of its stream's workspace. Later forwards that need a larger one, or evict the
+    stream's from the pool, must not hand that memory to others."""
+    layer, large = layer_of(200, 1040, M, compute), layer_of(512, 2048, M, compute)
+    x, xl = torch.empty((M, 1040), dtype=torch.bfloat16, device="cuda"), torch.zeros((9000, 2048), dtype=torch.bfloat16, device="cuda")
+    st = torch.cuda.Stream()
+    x.normal_(generator=gen(M))
+    torch.cuda.synchronize()
+    with torch.cuda.stream(st):
+        layer(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=st):
+        y = layer(x)
+    if M == 100:
+        with torch.cuda.stream(st):
+            large(xl)                                          # grows the stream's workspace
+        torch.cuda.synchronize()
+    held = []
+    for i in range(6):                                         # more streams than the pool keeps entries
+        with torch.cuda.stream(torch.cuda.Stream()):
+            large(xl)
+        torch.cuda.synchronize()
+        held.append(torch.full((1 << 24,), i, dtype=torch.uint8, device="cuda"))
+        x.normal_(generator=gen(10 + i))
+        y.fill_(float("nan"))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, layer(x)), i
+    for i, t in enumerate(held):
+        assert (t == i).all()
+    layer.handle.check()
+
+
+@pytest.mark.parametrize("compute", ["fp8", "int8"])
+def test_capture_that_has_to_allocate(compute):
+    # a workspace that is too small, then none, for the stream: the capture takes a new one, and the one that it
+    # replaces is freed by later eager calls
+    layer = layer_of(64, 4096, 1, compute)
+    x = torch.empty((30000, 4096), dtype=torch.bfloat16, device="cuda")          # 117 MiB of codes
+    st, graphs = torch.cuda.Stream(), []
+    for warm in (True, False):
+        if warm:
+            layer(x.normal_(generator=gen(1)))                 # the library's handles and plans
+            torch.cuda.synchronize()
+            with torch.cuda.stream(st):
+                layer(x[:100])
+            torch.cuda.synchronize()
+        else:
+            st = torch.cuda.Stream()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            y = layer(x)
+        graphs.append((graph, y))
+    for i in range(3):
+        x.normal_(generator=gen(5 + i))
+        for s in [st] + [torch.cuda.Stream() for _ in range(5)]:
+            torch.cuda.synchronize()
+            with torch.cuda.stream(s):
+                layer(x[:2000 + i])
+        want = layer(x)
+        torch.cuda.synchronize()
+        for graph, y in graphs:
+            y.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want), i
+
+
 def test_c_abi_refusals_reach_python():
     L = ep.lib()
     x = torch.zeros((4, 32), dtype=torch.int8, device="cuda")

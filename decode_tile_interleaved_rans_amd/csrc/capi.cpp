@@ -1371,8 +1371,8 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
         // INT8 with an expert that the fused launches below do not take (more than 64 rows, layout 0): the
         // experts with rows are decoded by grouped launches and multiplied by one product per expert, in
         // chunks of at most kExpertCodes of codes. The sums are exact, so the bits are the same. One product per
-        // chunk: 4096 tokens over 4 of 32 experts of 4096 x 2048 take 599 us in one chunk of 256 MiB, 642 in two
-        // and 686 in four; 512 MiB bring nothing more (4 of 128 of 2048 x 2048: 881 against 868).
+        // chunk: 4096 tokens over 4 of 32 experts of 4096 x 2048 take 598 us in one chunk of 256 MiB, 606 in two
+        // and 654 in four; 512 MiB bring nothing more (4 of 128 of 2048 x 2048: 877 against 866).
         constexpr size_t kExpertCodes = 256u << 20;
         if (compute == EP_I8 && K > 0 && (size_t)N * (size_t)K <= kExpertCodes) {
             bool fits = true;

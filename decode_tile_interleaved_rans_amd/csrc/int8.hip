@@ -294,9 +294,9 @@ __device__ __forceinline__ int expert_counts(const GemmI8Args& g, int e0, int* a
 // Every wave looks its tile up on its own. Tiles are numbered expert by expert, within an expert in groups
 // of 8 row tiles that walk the column tiles together. Consecutive block ids land on different XCDs, so
 // each XCD takes a contiguous eighth of the numbers: the rows and the weight of a group then meet in
-// one L2. Against tiles dealt out round robin, column tiles innermost: 4096 tokens on 4 of 32 experts (2048 x
-// 4096) 171 us for 181, 8 of 128 (1408 x 2048) 184 for 204, 1024 tokens 72 for 80, 16 tokens 30.3 for 31.6;
-// 2 of 8 (8192 x 4096) 313 for 303, with groups of one row tile 391.
+// one L2. Against tiles dealt out round robin, column tiles innermost (same weights every call): 4096 tokens
+// on 4 of 32 experts (2048 x 4096) 183 us for 261, 1024 tokens 73 for 80, 8 of 128 (1408 x 2048) 175 for 178, 2 of
+// 8 (8192 x 4096) 307 for 373, with groups of one row tile 355; 16 tokens (4096 x 2048) 30.7 for 31.4.
 template <int BM, int BN>
 __device__ __forceinline__ TileAt expert_tile(const GemmI8Args& g) {
     constexpr int G = 8;
@@ -445,10 +445,12 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_rsrc(const int8_t* src, i
 // the halves: by then every wave has read all of this stage (it may be overwritten: the loads of step
 // k + S start there) and the loads of step k + 1, in flight for S - 1 steps, have landed.
 //
-// At 4096 x 8192 x 8192 (256 x 256 tiles) 202-215 us, 2.6-2.7 POP/s: the MFMAs are busy 73% of the cycles,
+// At 4096 x 8192 x 8192 (256 x 256 tiles) 204-218 us, 2.5-2.7 POP/s: the MFMAs are busy 73% of the cycles,
 // at the 1.7 GHz that the card holds under this load; no LDS bank conflicts. With the fragments read just
-// before their MFMAs, in the compiler's order, it took 260 us (2.1 POP/s). Smaller tiles are bound by the
-// loads: without the MFMAs 512 x 3840 x 10240 takes as long (28 us). Slower: a ring of 64-code
+// before their MFMAs, in the compiler's order, it took 260 us (2.1 POP/s). Smaller tiles wait for the loads:
+// without the MFMAs 512 x 3840 x 10240 takes as long (28 us), though at well under half of what a CU's cache can
+// deliver: 128 x 64 tiles load 24 KiB per step of 0.47 us, 85% of it from L2. What counts is the loads' latency,
+// with S - 1 steps in flight. Slower: a ring of 64-code
 // stages with twice the bytes in flight (half lines: 252 for 226 us), 4 waves of 128 x 128 (237), raised wave
 // priority around the MFMAs (228 for 202). Walking the tiles in one persistent block per CU, the next tile's
 // loads ahead of the stores, gained 2-3% on several rounds of tiles and lost 1-3% on one.
@@ -550,7 +552,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_i8(GemmI8Args g) {
     } else {
         const int tiles_m = (g.M + BM - 1) / BM, tiles_n = (g.N + BN - 1) / BN, nblk = tiles_m * tiles_n;
         // each XCD a contiguous range of the tiles, so that a column's row tiles meet in one L2 (333 x 5003 x 3968,
-        // 237 tiles: 17.6 us, dealt out round robin 18.3; 200 x 4100 x 8192: 23.2 and 25.2)
+        // 237 tiles, same weights every call: 16.1 us, dealt out round robin 16.9; 200 x 4100 x 8192: 20.0 and 22.4)
         const int xcd = blockIdx.x % 8, rest = nblk % 8;
         const int b = xcd * (nblk / 8) + (xcd < rest ? xcd : rest) + blockIdx.x / 8;
         constexpr int G = 4;
@@ -689,14 +691,14 @@ hipError_t launch_pad_rows_i8(const int8_t* src, int64_t rows, int K, int8_t* ds
 // Tile of a product with one weight. A step of 128 K columns takes a block about the time below, whatever
 // M, N and K (measured with one block per CU and weights that come from HBM; small tiles are bound by the
 // latency and the rate of the loads, the largest by the MFMAs), so the estimate is rounds of tiles over the
-// CUs times steps times that. It picks, e.g., 256 x 256 for 4096 x 8192 x 8192 (211 us; 128 x 128: 322), 256 x 192
-// for 1024 x 11520 x 3840 (51; 256 x 256: 55, 256 x 128: 66), 128 x 128 for 512 x 8192 x 8192 (44; 128 x 64: 60, 64 x
-// 64: 69), 128 x 64 for 333 x 5003 x 3968 (17.6; 64 x 64: 20.4, 128 x 128: 24.3), 64 x 64 for 256 x 4096 x 4096 (12.8;
-// 32 x 64: 15.9, 128 x 64: 17.1), 32 x 64 for 64 x 8192 x 8192 (19.5; 64 x 64: 23.9), 16 x 64 for 1 x 11520 x 3840
-// (10.9) and 16 x 32 with two K groups for 1 x 8192 x 8192 (15.1; 16 x 64: 16.5) and 1 x 4096 x 16384 (16.2; 16 x
-// 64: 24.7). Waves per block where one tile fills a CU: 128 x 128 in 16 (1024 x 4096 x 4096 24.5; in 8 29.7), 128 x 64
-// in 8 (333 x 5003 x 3968 17.6; in 4 18.4), 64 x 64 in 8 (256 x 4096 x 4096 12.8; in 4 13.4): more of them hide the
-// barrier and the LDS reads of a step.
+// CUs times steps times that. It picks, e.g., 256 x 256 for 4096 x 8192 x 8192 (215 us; 256 x 128: 245, 128 x 128:
+// 321), 256 x 192 for 1024 x 11520 x 3840 (50; 256 x 256: 55, 256 x 128: 67), 128 x 128 for 512 x 8192 x 8192 (44; 256 x
+// 128: 55, 128 x 64: 59), 128 x 64 for 333 x 5003 x 3968 (17.6; 64 x 64: 20.8, 128 x 128: 23.7), 64 x 64 for 256 x 4096 x
+// 4096 (12.8; 32 x 64: 15.9, 128 x 64: 17.2), 32 x 64 for 64 x 8192 x 8192 (19.6; 64 x 64: 24.0), 16 x 64 for 1 x 11520 x
+// 3840 (10.9; 32 x 64: 10.8) and 16 x 32 with two K groups for 1 x 8192 x 8192 (15.2; 16 x 64: 16.4) and 1 x 4096 x
+// 16384 (16.4; 16 x 64: 24.7). Waves per block: 128 x 128 in 16 or 8 within 4% of each other either way (1024 x 4096 x
+// 4096 25.0 and 24.5, 1024 x 11520 x 3840 68.5 and 69.3), 128 x 64 in 8 (333 x 5003 x 3968 17.6; in 4 17.8) and 64 x 64
+// in 8 (256 x 4096 x 4096 12.8; in 4 13.4): more of them hide the barrier and the LDS reads of a step. All of one run.
 struct TileCost {
     int bm, bn;
     float step_us;
@@ -725,12 +727,16 @@ hipError_t launch_gemm_i8(const GemmI8Args& g, hipStream_t stream) {
     }
     // Experts: how many rows each has is known to the device only, so the tile goes by the average, several
     // small blocks share a CU where the weights' bytes bound the time, and a tile too large to give
-    // every CU one makes way for the next. Measured: 2 rows each on 16 x 64 tiles 45 us (128 experts, 1408 x
-    // 2048; 32 x 64: 48, 64 x 64: 58), 8 rows on 32 x 64 39.6 (32 experts, 4096 x 2048; 16 x 64: 41.8), 32 rows
-    // on 128 x 128 43.3 (32 experts, 2048 x 4096; in 4 waves instead of 16 46.3; 64 x 64: 48), 128 rows on
-    // 128 x 256 75 (128 x 192: 87), and from 192 rows on 128 x 192, two blocks to a CU, so that one's start and end run
-    // behind the other's MFMAs: 512 rows of 2048 x 4096 181 (128 x 256: 184, 256 x 256: 191, 128 x 128: 195), 375 rows of
-    // 16 experts of 4096 x 2048 70 (128 x 256: 83), 2048 rows of 4 of 2048 x 2048 46 (61).
+    // every CU one makes way for the next. Measured with the same weights every call, in us, and, behind the
+    // slash, with weights that come from HBM: 2 rows each on 16 x 64 tiles 34 / 41 (128 experts, 1408 x 2048; 32 x 64:
+    // 35 / 43, 64 x 64: 39 / 48), 8 rows on 32 x 64 40 / 51 (32 experts, 4096 x 2048; 16 x 64: 41 / 49), 32 rows on 128 x
+    // 128 44 / 67 (32 experts, 2048 x 4096; in 4 waves instead of 16 46 / 69; 64 x 64: 46 / 62), 128 rows on 128 x 256
+    // 75 / 85 (128 x 128: 83 / 90, 128 x 192: 93 / 101), and from 192 rows on 128 x 192, two blocks to a CU, so that one's
+    // start and end run behind the other's MFMAs: 375 rows of 16 experts of 4096 x 2048 71 / 87 (128 x 256: 84 / 93,
+    // 128 x 128: 81 / 94), 2048 rows of 4 of 2048 x 2048 44 / 45 (128 x 256: 47), 256 rows of 128 of 1408 x 2048 175
+    // (128 x 256: 192). 512 rows of 32 of 2048 x 4096: 181 / 185, as 128 x 256 (180 / 185); in the profile of six passes
+    // 196, in the one before with 128 x 256 185. 256 x 256 tiles, which no call takes here, took 179 /
+    // 181 there, 293 for 306 at 1024 rows of 8 of 8192 x 4096 and 70 / 78 at the 375 rows, but 189 for 175 at the 256.
     const int64_t used = g.rows < g.experts ? g.rows : g.experts, rows = (g.rows + used - 1) / used;
     auto fills = [&](int bm, int bn) { return used * ((rows + bm - 1) / bm) * (((int64_t)g.N + bn - 1) / bn) >= device_cus(); };
     if (rows >= 192 && fills(128, 192)) return tiled_go<128, 192, 2, 4, 2, 1>(g, stream);

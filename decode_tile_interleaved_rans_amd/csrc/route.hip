@@ -8,9 +8,11 @@
 // token's hidden vector is read once however many experts chose it. Nothing is summed by atomics on
 // floating values: results do not depend on scheduling.
 //
-// All of it is memory bound but the order itself: 16384 tokens of 4096 BF16 columns, 4 of 64 experts, 2% dropped:
-// order 9 us, rows 130 us (671 MB, 5.2 TB/s), sum 135 us (660 MB, 4.9 TB/s), the gradient of the sum 238 us
-// (1.2 GB, 5.0 TB/s); a copy reaches 5.2. A few tokens: one launch of 4.6 us for order and rows.
+// All of it is memory bound but the order itself: 16384 tokens of 4096 BF16 columns, 4 of 64 experts, 2% dropped,
+// each call repeated by itself: order 9 us, rows 130 us (671 MB, 5.1 TB/s), sum 135 us (660 MB, 4.9 TB/s), the
+// gradient of the sum 239 us (1.2 GB, 5.0 TB/s); a copy reaches 5.2. In passes of sort and sum the order takes
+// 11.5, the rows 107 and the sum, while the rows' last lines still leave the caches, 167. A few tokens: one
+// launch of 4.7 us for order and rows.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

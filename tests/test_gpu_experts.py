@@ -152,7 +152,10 @@ def test_int8_chunks_take_the_tile_of_their_own_rows():
         y = ep.linear_forward_experts(layers, x, ids)
         torch.cuda.synchronize()
     assert torch.equal(y, want)
-    products = [e.name for e in prof.events() if "gemm_i8" in e.name]
+    kernels = [e.name for e in prof.events()]
+    if not any("quantize_rows_i8" in n for n in kernels):
+        pytest.skip("the profiler records no kernels here")
+    products = [n for n in kernels if "gemm_i8" in n]
     assert len(products) == 3 and len(set(products)) == 1, products
 
 

@@ -43,7 +43,8 @@ EXPORTS = ["ep_compress", "ep_free", "ep_stream_info", "ep_upload", "ep_handle_i
            "ep_linear_forward_fp8_many", "ep_quantize_rows_int8", "ep_gemm_int8", "ep_gemm_int8_experts",
            "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_linear_forward_int8_many",
            "ep_linear_forward_experts", "ep_sort_tokens_scratch", "ep_sort_tokens",
-           "ep_combine_tokens", "ep_combine_tokens_grad"]
+           "ep_combine_tokens", "ep_combine_tokens_grad", "ep_quantize_rows_mxfp4", "ep_dequantize_rows_mxfp4",
+           "ep_gemm_mxfp4", "ep_gemm_mxfp4_experts"]
 
 
 class EPError(RuntimeError):
@@ -110,6 +111,10 @@ def lib() -> C.CDLL:
         L.ep_sort_tokens.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp]
         L.ep_combine_tokens.argtypes = [vp, C.c_int, vp, vp, i64, C.c_int, i64, i64, vp, vp]
         L.ep_combine_tokens_grad.argtypes = [vp, C.c_int, vp, vp, vp, i64, C.c_int, i64, i64, vp, vp, vp]
+        L.ep_quantize_rows_mxfp4.argtypes = [vp, C.c_int, i64, i64, i64, i64, vp, vp, vp]
+        L.ep_dequantize_rows_mxfp4.argtypes = [vp, vp, i64, i64, i64, i64, C.c_int, vp, vp]
+        L.ep_gemm_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, C.c_int, vp, vp]
+        L.ep_gemm_mxfp4_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_handle_check.argtypes = [vp, vp]
         L.ep_release.argtypes = [vp]
         L.ep_release.restype = None
@@ -610,6 +615,133 @@ def gemm_int8_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream
         return _on_stream(stream, lambda: _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype),
                           xq, xs, wq, ws, offsets, bias)
     return _gemm_int8(xq, xs, wq, ws, offsets, bias, out_dtype)
+
+
+# ------------------------------------------------------------------------------------ MXFP4
+def quantize_rows_mxfp4(x, stream=None):
+    """MXFP4 codes and scales of BF16, FP16 or FP32 rows: x [M, K] (rows may be further apart than K) or, for
+    the experts' weights, contiguous [E, M, K]. Blocks of 32 elements of a row share a scale 2^(b - 127), b = max(0,
+    floor(log2 max |x|) + 125); codes are x / scale rounded to nearest, ties to even, to 0, 0.5, 1, 1.5, 2, 3, 4
+    or 6 with a sign (a block whose largest magnitude is above 6 scale units saturates there). A block with an
+    infinity or a NaN gets b = 255 and codes 0, and products with it are NaN.
+
+    Returns (codes, scales), uint8, with Kp the width rounded up to whole 128 elements, zeros behind: codes [..., M,
+    Kp / 2], two to a byte, the even element in the low half; scales [..., Kp / 128, M, 4], the bytes b of a row's 128
+    elements side by side. Row-major scales s [M, Kp / 32] from elsewhere are
+    s.view(M, -1, 4).transpose(0, 1).contiguous(). On `stream` (default: the current stream; another stream first
+    waits for the current one)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: quantize_rows_mxfp4(x), x)
+    torch = _torch()
+    lead = ()
+    if x.dim() == 3:
+        _need(x, "x", x.dtype)
+        lead = x.shape[:1]
+        M, K = x.shape[1:]
+        x = x.reshape(lead[0] * M, K)
+    elif x.dim() == 2:
+        M, K = x.shape
+    else:
+        raise ValueError(f"x must be [M, K] or [E, M, K], got shape {tuple(x.shape)}")
+    rows, _, ldx = _need_rows(x, "x", _float_types())
+    chunks = (K + 127) // 128
+    q = torch.empty((*lead, M, 64 * chunks), dtype=torch.uint8, device=x.device)
+    s = torch.empty((*lead, chunks, M, 4), dtype=torch.uint8, device=x.device)
+    _check(lib().ep_quantize_rows_mxfp4(_ptr(x), _dtype_code(x.dtype), rows, M, K, ldx, _ptr(q), _ptr(s), _current_raw()),
+           "ep_quantize_rows_mxfp4")
+    return q, s
+
+
+def _mx_shapes(q, s, qname: str, sname: str, dims):
+    """Shape checks of MXFP4 codes and scales; their padded width."""
+    if q.dim() not in dims or q.shape[-1] % 64:
+        raise ValueError(f"{qname} must be codes {' or '.join('[rows, Kp / 2]' if d == 2 else '[experts, rows, Kp / 2]' for d in dims)}"
+                         f", Kp a multiple of 128, got shape {tuple(q.shape)}")
+    torch = _torch()
+    chunks = q.shape[-1] // 64
+    shape = (*q.shape[:-2], chunks, q.shape[-2], 4)
+    dev = torch.cuda.current_device() if q.is_cuda else -1
+    if not _fits(q, torch.uint8, q.shape, dev):
+        _need(q, qname, torch.uint8)
+    if not _fits(s, torch.uint8, shape, dev):
+        _need(s, sname, torch.uint8, shape=shape)
+    return 128 * chunks
+
+
+def dequantize_rows_mxfp4(codes, scales, out_dtype=None, columns=None, stream=None):
+    """The values of MXFP4 codes and scales (quantize_rows_mxfp4's, of a matrix or of the experts' matrices) as
+    [..., M, columns] in BF16 (default), FP16 or FP32; columns: how many of the Kp padded columns (default: all).
+    Exact in BF16 and FP32 for scale bytes up to 251, rounded to nearest even in FP16. On `stream` (default: the
+    current stream; another stream first waits for the current one)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: dequantize_rows_mxfp4(codes, scales, out_dtype, columns), codes, scales)
+    torch = _torch()
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in _float_types():
+        raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+    Kp = _mx_shapes(codes, scales, "codes", "scales", (2, 3))
+    K = Kp if columns is None else columns
+    if not 0 <= K <= Kp:
+        raise ValueError(f"columns must be 0 ... {Kp}, got {columns}")
+    M = codes.shape[-2]
+    y = torch.empty((*codes.shape[:-1], K), dtype=out_dtype, device=codes.device)
+    codes, scales = _mx_aligned(codes, 4), _mx_aligned(scales, 4)
+    _check(lib().ep_dequantize_rows_mxfp4(_ptr(codes), _ptr(scales), M * (codes.shape[0] if codes.dim() == 3 else 1), M, Kp, K,
+                                          _dtype_code(out_dtype), _ptr(y), _current_raw()), "ep_dequantize_rows_mxfp4")
+    return y
+
+
+def _mx_aligned(t, to: int):
+    """t, or where its address is no multiple of `to` a copy."""
+    return t.clone() if t.data_ptr() % to else t
+
+
+def _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype):
+    torch = _torch()
+    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
+    if out_dtype not in _float_types():
+        raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
+    K = _mx_shapes(xq, xs, "xq", "xs", (2,))
+    if _mx_shapes(wq, ws, "wq", "ws", (2 if offsets is None else 3,)) != K:
+        raise ValueError(f"xq and wq must have the same width, got {K} and {2 * wq.shape[-1]}")
+    M, N = xq.shape[0], wq.shape[-2]
+    lead = tuple(wq.shape[:-1])
+    dev = torch.cuda.current_device()
+    if bias is not None and not _fits(bias, torch.bfloat16, lead, dev):
+        _need(bias, "bias", torch.bfloat16, shape=lead)
+    if offsets is not None and not _fits(offsets, torch.int32, (lead[0] + 1,), dev):
+        _need(offsets, "offsets", torch.int32, shape=(lead[0] + 1,))
+    # codes are read in pieces of 16 bytes, scales in pieces of 4
+    xq, wq, xs, ws = _mx_aligned(xq, 16), _mx_aligned(wq, 16), _mx_aligned(xs, 4), _mx_aligned(ws, 4)
+    y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), _current_raw())
+    if offsets is None:
+        _check(lib().ep_gemm_mxfp4(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, N, K, *tail), "ep_gemm_mxfp4")
+    else:
+        _check(lib().ep_gemm_mxfp4_experts(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), lead[0], M, N, K, *tail),
+               "ep_gemm_mxfp4_experts")
+    return y
+
+
+def gemm_mxfp4(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
+    """Y = X W^T (+ bias) of two MXFP4 matrices: codes xq [M, Kp / 2] and wq [N, Kp / 2] with scales xs [Kp / 128, M, 4]
+    and ws [Kp / 128, N, 4], as quantize_rows_mxfp4 gives them; fp32 sums, bias BF16 [N], output BF16 (default), FP16
+    or FP32, rounded once. Codes at an address that is no multiple of 16 are copied first. On `stream` (default: the
+    current stream; another stream first waits for the current one)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: _gemm_mxfp4(xq, xs, wq, ws, None, bias, out_dtype), xq, xs, wq, ws, bias)
+    return _gemm_mxfp4(xq, xs, wq, ws, None, bias, out_dtype)
+
+
+def gemm_mxfp4_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, stream=None):
+    """gemm_mxfp4 with a weight per expert, in one launch: rows offsets[e] ... offsets[e + 1] - 1 of xq [R, Kp / 2]
+    (scales xs [Kp / 128, R, 4]) meet wq[e] ([experts, N, Kp / 2], scales ws [experts, Kp / 128, N, 4], bias [experts,
+    N]); rows behind the last expert's come out zero. offsets: int32 on the GPU, as sort_tokens gives them
+    (ascending from 0, at most R; they are not read on the host)."""
+    if stream is not None:
+        return _on_stream(stream, lambda: _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype),
+                          xq, xs, wq, ws, offsets, bias)
+    return _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype)
 
 
 # ------------------------------------------------------------------------------------ expert routing

@@ -19,6 +19,7 @@
 #include "gemm.h"
 #include "int8.h"
 #include "kernels.h"
+#include "mxfp4.h"
 #include "route.h"
 #include "static_scratch.h"
 
@@ -569,6 +570,39 @@ ep_status gemm_int8(const int8_t* xq, const float* xs, const int8_t* wq, const f
     const hipError_t e = ep::launch_gemm_i8(g, s);
     if (e == hipErrorInvalidValue) return fail(EP_ERANGE, "M x N is too large for one launch");
     return e == hipSuccess ? EP_OK : hip_fail(e, "int8 gemm launch");
+}
+
+// Checks that the MXFP4 quantizer and its inverse share; *empty: nothing to do.
+ep_status check_mx_rows(int64_t rows, int64_t M, int64_t K, bool* empty) {
+    if (rows < 0 || M < 0 || K < 0) return fail(EP_EINVAL, "negative size");
+    if (K > ep::kMxMaxK) return fail(EP_ERANGE, "K above 4194304");
+    if (M > ep::kMxMaxRows || rows >= (int64_t)1 << 40) return fail(EP_ERANGE, "too many rows");
+    *empty = rows == 0 || K == 0;
+    if (rows > 0 && (M == 0 || rows % M)) return fail(EP_EINVAL, "the rows must be whole matrices of rows_per_matrix rows");
+    return EP_OK;
+}
+
+// Checks and launch of the MXFP4 products (experts = 0: one weight for all rows).
+ep_status gemm_mx(const uint8_t* xq, const uint8_t* xs, const uint8_t* wq, const uint8_t* ws, const int32_t* offsets,
+                  int experts, int64_t M, int64_t N, int64_t K, const void* bias, ep_dtype out, void* y, hipStream_t s) {
+    if (M < 0 || N < 0 || K < 0) return fail(EP_EINVAL, "negative size");
+    if (out != EP_BF16 && out != EP_F16 && out != EP_F32)
+        return fail(EP_EUNSUPPORTED, "the MXFP4 product writes BF16, F16 or F32");
+    if (K > ep::kMxMaxK) return fail(EP_ERANGE, "K above 4194304");
+    if (K % 128) return fail(EP_EINVAL, "K must be a multiple of 128 (ep_quantize_rows_mxfp4 pads rows to that)");
+    if (M == 0 || N == 0) return EP_OK;
+    if ((K > 0 && (!xq || !wq || !xs || !ws)) || !y) return fail(EP_EINVAL, "null pointer");
+    if (M > ep::kMxMaxRows || N > ep::kMxMaxRows) return fail(EP_ERANGE, "M and N must be at most 2^27");
+    if ((reinterpret_cast<uintptr_t>(xq) | reinterpret_cast<uintptr_t>(wq)) & 15)
+        return fail(EP_EINVAL, "X and W codes must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(xs) | reinterpret_cast<uintptr_t>(ws)) & 3)
+        return fail(EP_EINVAL, "the scales must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(y) & (out == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "Y is not aligned to its elements");
+    const ep::GemmMxArgs g{xq, xs, wq, ws, static_cast<const uint16_t*>(bias), y, offsets, (int)M, (int)N, (int)K, (int)N,
+                           experts, out, (int)M};
+    const hipError_t e = ep::launch_gemm_mx(g, s);
+    if (e == hipErrorInvalidValue) return fail(EP_ERANGE, "M x N is too large for one launch");
+    return e == hipSuccess ? EP_OK : hip_fail(e, "mxfp4 gemm launch");
 }
 
 ep_status check_choices(int64_t T, int k, int E) {
@@ -1466,6 +1500,64 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
             if (st != EP_OK) return st;
         }
         return EP_OK;
+    });
+}
+
+ep_status ep_quantize_rows_mxfp4(const void* dev_x, ep_dtype src, int64_t rows, int64_t rows_per_matrix, int64_t K, int64_t ldx,
+                                 uint8_t* dev_q, uint8_t* dev_scale, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        bool empty = false;
+        if (src != EP_BF16 && src != EP_F16 && src != EP_F32)
+            return fail(EP_EUNSUPPORTED, "the MXFP4 quantizer takes BF16, F16 or F32 rows");
+        if (ep_status st = check_mx_rows(rows, rows_per_matrix, K, &empty); st != EP_OK) return st;
+        if (ldx < K) return fail(EP_EINVAL, "rows of X overlap (ldx < K)");
+        if (empty) return EP_OK;
+        if (ldx > (INT64_MAX / 8) / rows) return fail(EP_ERANGE, "X is too large");
+        if (!dev_x || !dev_q || !dev_scale) return fail(EP_EINVAL, "null pointer");
+        if (reinterpret_cast<uintptr_t>(dev_x) & (src == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "X is not aligned to its elements");
+        if ((reinterpret_cast<uintptr_t>(dev_q) | reinterpret_cast<uintptr_t>(dev_scale)) & 3)
+            return fail(EP_EINVAL, "the codes and scales must be 4-byte aligned");
+        const hipError_t e = ep::launch_quantize_rows_mx(dev_x, src, rows, rows_per_matrix, K, ldx, dev_q, dev_scale,
+                                                         static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "mxfp4 quantize launch");
+    });
+}
+
+ep_status ep_dequantize_rows_mxfp4(const uint8_t* dev_q, const uint8_t* dev_scale, int64_t rows, int64_t rows_per_matrix,
+                                   int64_t Kp, int64_t K, ep_dtype dst, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        bool empty = false;
+        if (dst != EP_BF16 && dst != EP_F16 && dst != EP_F32)
+            return fail(EP_EUNSUPPORTED, "MXFP4 values are written as BF16, F16 or F32");
+        if (ep_status st = check_mx_rows(rows, rows_per_matrix, Kp, &empty); st != EP_OK) return st;
+        if (K < 0 || K > Kp || Kp % 128) return fail(EP_EINVAL, "the codes must have a multiple of 128 columns, at least K");
+        if (empty || K == 0) return EP_OK;
+        if (!dev_q || !dev_scale || !dev_y) return fail(EP_EINVAL, "null pointer");
+        if (reinterpret_cast<uintptr_t>(dev_y) & (dst == EP_F32 ? 3 : 1)) return fail(EP_EINVAL, "Y is not aligned to its elements");
+        if ((reinterpret_cast<uintptr_t>(dev_q) | reinterpret_cast<uintptr_t>(dev_scale)) & 3)
+            return fail(EP_EINVAL, "the codes and scales must be 4-byte aligned");
+        const hipError_t e = ep::launch_dequantize_rows_mx(dev_q, dev_scale, rows, rows_per_matrix, Kp, K, dst, dev_y,
+                                                           static_cast<hipStream_t>(hip_stream));
+        return e == hipSuccess ? EP_OK : hip_fail(e, "mxfp4 dequantize launch");
+    });
+}
+
+ep_status ep_gemm_mxfp4(const uint8_t* dev_xq, const uint8_t* dev_xs, const uint8_t* dev_wq, const uint8_t* dev_ws, int64_t M,
+                        int64_t N, int64_t K, const void* dev_bias, ep_dtype out, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        return gemm_mx(dev_xq, dev_xs, dev_wq, dev_ws, nullptr, 0, M, N, K, dev_bias, out, dev_y,
+                       static_cast<hipStream_t>(hip_stream));
+    });
+}
+
+ep_status ep_gemm_mxfp4_experts(const uint8_t* dev_xq, const uint8_t* dev_xs, const uint8_t* dev_wq, const uint8_t* dev_ws,
+                                const int32_t* dev_offsets, int E, int64_t R, int64_t N, int64_t K, const void* dev_bias,
+                                ep_dtype out, void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (E < 1 || E > ep::kRouteMaxExperts) return fail(EP_ERANGE, "the number of experts must be 1 ... 1024");
+        if (R > 0 && N > 0 && !dev_offsets) return fail(EP_EINVAL, "null offsets");
+        return gemm_mx(dev_xq, dev_xs, dev_wq, dev_ws, dev_offsets, E, R, N, K, dev_bias, out, dev_y,
+                       static_cast<hipStream_t>(hip_stream));
     });
 }
 

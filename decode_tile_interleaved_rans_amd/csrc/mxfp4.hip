@@ -1,0 +1,456 @@
+// gfx950 MXFP4 row quantizer, its inverse, and MXFP4 matrix products: Y[m][n] = sum over blocks b of 32 of
+// 2^(sx[m][b] + sw[n][b] - 254) sum_{k in b} X[m][k] W[n][k] (+ bias[n]) on the matrix cores, which take the codes
+// and the scale bytes as they are (v_mfma_scale_f32_16x16x128_f8f6f4), fp32 sums. The format and its layout stand in
+// mxfp4.h.
+//
+// Operand lane layout (checked on the device): lane l supplies 32 codes (16 bytes) of A row l % 16 and of B column
+// l % 16, K group l / 16, and a scale byte for each, and receives C[4 (l / 16) + i][l % 16], i < 4. A and B take the
+// same K positions per lane, so equal k meet whatever the order. W is the A operand and X the B operand: a lane then
+// holds four consecutive output columns of one row. A scale byte of 255 gives NaN, whatever the codes.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "entropack.h"
+#include "kernels.h"
+#include "mxfp4.h"
+#include "tiles.h"
+
+namespace ep {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// --------------------------------------------------------------------------- quantizer and inverse
+// A block's scale byte is b = max(0, e - 2), e the biased exponent of max |x| as an fp32 number: 2^(b - 127) = 2^(floor
+// (log2 max |x|) - 2), which puts the largest magnitude into [4, 8) of the codes' range. Codes are x / 2^(b - 127)
+// rounded to nearest, ties to the even code, at most 6 in magnitude (v_cvt_scalef32_pk_fp4_f32 does just that, for
+// subnormal numbers and scales too: checked on the device against the definition at and next to every rounding
+// border of every scale). A block with an infinity or a NaN gets b = 255 and codes 0, so that every product with it
+// is NaN instead of a plausible number.
+//
+// Every block of 32 stands alone, so a wave takes 16 rows x 128 columns: four lanes to a block, eight elements
+// to a lane, four rows to a load; the maximum goes over the four lanes (DPP). The scales of 16 rows
+// leave in one store of 64 bytes.
+template <int SRC> struct Elem { typedef uint16_t type; };
+template <> struct Elem<EP_F32> { typedef uint32_t type; };
+
+template <int SRC>
+__device__ __forceinline__ float elem_value(uint32_t bits) {
+    if constexpr (SRC == EP_F32) return __uint_as_float(bits);
+    if constexpr (SRC == EP_BF16) return __uint_as_float(bits << 16);
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)bits);
+}
+
+template <int SRC>
+struct Eight {
+    typename Elem<SRC>::type e[8];
+};
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+
+// What a wave works on: rows r0 ... of matrix e, the 128 columns of chunk c.
+struct MxPart {
+    int64_t e, r0, c;
+};
+__device__ __forceinline__ MxPart mx_part(int64_t unit, int64_t row_groups, int64_t col_groups) {
+    const int64_t cg = unit % col_groups, rest = unit / col_groups;
+    return MxPart{rest / row_groups, 16 * (rest % row_groups), 4 * cg + (threadIdx.x >> 6)};
+}
+
+template <int SRC>
+__global__ __launch_bounds__(256) void quantize_rows_mx(const void* Xv, int64_t M, int64_t K, int64_t ldx, uint8_t* Q, uint8_t* S,
+                                                        int64_t chunks, int64_t row_groups, int64_t units) {
+    typedef typename Elem<SRC>::type T;
+    const int64_t col_groups = (chunks + 3) / 4;
+    const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const MxPart at = mx_part(u, row_groups, col_groups);
+        if (at.c >= chunks) continue;
+        const int64_t k = 128 * at.c + 8 * p;
+        const int left = (int)(K - k < 8 ? (K - k > 0 ? K - k : 0) : 8);      // elements of the row from k on
+        Eight<SRC> v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = at.r0 + 4 * j + g;
+            const T* x = static_cast<const T*>(Xv) + (at.e * M + m) * ldx + k;
+            if (m < M && left == 8) {
+                __builtin_memcpy(&v[j], x, sizeof v[j]);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[j].e[i] = m < M && i < left ? x[i] : 0;
+            }
+        }
+        uint32_t scale = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = at.r0 + 4 * j + g;
+            float f[8];
+            uint32_t a = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] = elem_value<SRC>(v[j].e[i]);
+                const uint32_t b = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+                a = a > b ? a : b;
+            }
+            uint32_t o = dpp<0xB1>(a);                                      // the lane beside, then the pair beside
+            a = a > o ? a : o;
+            o = dpp<0x4E>(a);
+            a = a > o ? a : o;
+            const bool bad = a >= 0x7F800000u;
+            const uint32_t e8 = a >> 23, b8 = bad ? 255u : e8 > 2 ? e8 - 2 : 0u;
+            const float unit = __uint_as_float((bad ? 127u : b8) << 23);      // exponent bits 0 stand for 2^-127 here
+            uint32_t q = 0;
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[0], f[1], unit, 0);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[2], f[3], unit, 1);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[4], f[5], unit, 2);
+            q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[6], f[7], unit, 3);
+            q = bad ? 0u : q;
+            if (m < M) __builtin_memcpy(Q + (at.e * M + m) * (chunks * 64) + k / 2, &q, 4);
+            uint32_t s = b8 << (8 * (p >> 2));                              // the row's four scales, in all its 16 lanes
+            s |= dpp<0x124>(s);
+            s |= dpp<0x128>(s);
+            if (p == j) scale = s;                                          // lane p < 4 keeps row 4 p + g
+        }
+        const int64_t m = at.r0 + 4 * p + g;
+        if (p < 4 && m < M) __builtin_memcpy(S + ((at.e * chunks + at.c) * M + m) * 4, &scale, 4);
+    }
+}
+
+// The inverse: a lane turns the eight codes of a dword into values, exactly in BF16 and FP32 where they have the
+// range (BF16 and FP32: up to scale bytes of 251), rounded once in FP16.
+template <int DST>
+__device__ __forceinline__ void eight_values(uint32_t q, float unit, Eight<DST>* out) {
+    auto two = [&](auto sel) {
+        constexpr int s = decltype(sel)::value;
+        if constexpr (DST == EP_BF16) {
+            const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, unit, s));
+            out->e[2 * s] = (uint16_t)v, out->e[2 * s + 1] = (uint16_t)(v >> 16);
+        } else if constexpr (DST == EP_F16) {
+            const uint32_t v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(q, unit, s));
+            out->e[2 * s] = (uint16_t)v, out->e[2 * s + 1] = (uint16_t)(v >> 16);
+        } else {
+            const f32x2 v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q, unit, s);
+            out->e[2 * s] = __float_as_uint(v[0]), out->e[2 * s + 1] = __float_as_uint(v[1]);
+        }
+    };
+    two(std::integral_constant<int, 0>{});
+    two(std::integral_constant<int, 1>{});
+    two(std::integral_constant<int, 2>{});
+    two(std::integral_constant<int, 3>{});
+}
+
+template <int DST>
+__global__ __launch_bounds__(256) void dequantize_rows_mx(const uint8_t* Q, const uint8_t* S, int64_t M, int64_t chunks, int64_t K,
+                                                          void* Yv, int64_t row_groups, int64_t units) {
+    typedef typename Elem<DST>::type T;
+    const int64_t col_groups = (chunks + 3) / 4;
+    const int lane = threadIdx.x & 63, p = lane & 15, g = lane >> 4;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const MxPart at = mx_part(u, row_groups, col_groups);
+        const int64_t k = 128 * at.c + 8 * p;
+        if (at.c >= chunks || k >= K) continue;
+        uint32_t q[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = at.r0 + 4 * j + g;
+            q[j] = s[j] = 0;
+            if (m < M) {
+                __builtin_memcpy(&q[j], Q + (at.e * M + m) * (chunks * 64) + k / 2, 4);
+                __builtin_memcpy(&s[j], S + ((at.e * chunks + at.c) * M + m) * 4, 4);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t m = at.r0 + 4 * j + g;
+            if (m >= M) continue;
+            Eight<DST> v;
+            // a byte of 255 makes the unit an infinity, which the conversion takes for the format's NaN
+            eight_values<DST>(q[j], __uint_as_float((s[j] >> (8 * (p >> 2)) & 255u) << 23), &v);
+            T* y = static_cast<T*>(Yv) + (at.e * M + m) * K + k;
+            if (K - k >= 8) {
+                __builtin_memcpy(y, &v, sizeof v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i < K - k) y[i] = v.e[i];
+            }
+        }
+    }
+}
+
+struct MxGrid {
+    int64_t chunks, row_groups, units;
+    unsigned blocks;
+};
+MxGrid mx_grid(int64_t rows, int64_t M, int64_t K) {
+    MxGrid g;
+    g.chunks = (K + 127) / 128;
+    g.row_groups = (M + 15) / 16;
+    g.units = rows / M * g.row_groups * ((g.chunks + 3) / 4);
+    g.blocks = (unsigned)(g.units < (1 << 22) ? g.units : 1 << 22);          // a grid may have at most 2^32 - 1 threads
+    return g;
+}
+
+// ------------------------------------------------------------------------------- tiled product
+// The ring of the INT8 product (int8.hip) on rows of 128 bytes, 256 codes, a step: both operand tiles go from global
+// memory straight into LDS, S stages deep, and the fragments of the next half step are read behind the current
+// MFMAs. A step has two halves of 128 codes; in half h the K group g of a lane takes chunk 2 g + h of the row, so that
+// its scale bytes of both halves are neighbours in one dword, (g % 2) * 16 bits up. The scales of a stage are two
+// dwords per row, loaded into LDS beside the codes: [2][rows], a contiguous piece of each 128 columns.
+template <int ROWS>
+constexpr int scale_words() { return 2 * ROWS < 64 ? 64 : 2 * ROWS; }
+
+// The scale loads of one stage, dealt over the waves: every wave issues kEach loads, of its own part of X's or W's
+// scales or, behind the last, of zeros into the spare KiB.
+template <int BM, int BN, int NW>
+struct ScaleDma {
+    static constexpr int kX = scale_words<BM>() / 64, kW = scale_words<BN>() / 64, kEach = (kX + kW + NW - 1) / NW;
+    const uint8_t *x, *w;           // the scales of the tile's first row, chunk 0
+    int64_t px, pw;                 // bytes between chunks
+    int rx, rw;                     // rows of the tile that are there
+    __device__ __forceinline__ void load(int step, int chunks, uint8_t* lds, uint8_t* spare, int wave) const {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int i = wave + NW * j;                                    // uniform
+            const bool isx = i < kX, any = i < kX + kW;
+            const int at = 64 * (isx ? i : i - kX) + lane, rows = isx ? BM : BN;
+            const int c = isx ? at / BM : at / BN, r = isx ? at % BM : at % BN;
+            const int64_t pitch = isx ? px : pw;
+            const uint8_t* base = (isx ? x : w) + 2 * (int64_t)step * pitch;
+            const bool in = any && at < 2 * rows && r < (isx ? rx : rw) && 2 * step + c < chunks;
+            const uint32_t off = in ? (uint32_t)(c * (int)pitch + 4 * r) : kOob;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, 0x7FFFFFFF, 0x00020000);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void*)(any ? lds + 256 * i : spare), 4, off, 0, 0, 0);
+        }
+    }
+};
+
+// Fragments of T 16-row parts from row r0 of an operand tile, half h of a stage.
+template <int T>
+__device__ __forceinline__ void read_frags(const uint8_t* tile, int r0, int h, i32x4 (&f)[T]) {
+    const int lane = threadIdx.x & 63, r = r0 + (lane & 15);
+    const uint8_t* p = tile + r * 128 + (((2 * (lane >> 4) + h) ^ chunk_swizzle(r)) << 4);
+#pragma unroll
+    for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const i32x4*>(p + 16 * 128 * i);
+}
+
+// Their scales of both halves (bytes 0 and 1); ROWS rows in the tile.
+template <int ROWS, int T>
+__device__ __forceinline__ void read_scales(const uint8_t* scales, int r0, int (&s)[T]) {
+    const int lane = threadIdx.x & 63;
+    const uint8_t* p = scales + 4 * ((lane >> 5) * ROWS + r0 + (lane & 15));
+#pragma unroll
+    for (int i = 0; i < T; ++i) s[i] = *reinterpret_cast<const int*>(p + 64 * i) >> (lane & 16);
+}
+
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
+
+template <int H, int TI, int TJ>
+__device__ __forceinline__ void multiply(const i32x4 (&x)[TI], const i32x4 (&w)[TJ], const int (&sx)[TI], const int (&sw)[TJ],
+                                         f32x4 (&acc)[TI][TJ]) {
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w[j]), widen(x[i]), acc[i][j], 4, 4, H, sw[j], H, sx[i]);
+}
+
+// The epilogue of a wave's TI x TJ parts of 16 x 16: rows m0 + 16 i + lane % 16, columns n0 + 16 j + 4 (lane / 16).
+template <int OUT, int TI, int TJ>
+__device__ __forceinline__ void store_tile(const GemmMxArgs& g, const TileAt& t, int m0, int n0, const f32x4 (&acc)[TI][TJ], bool vec) {
+    const int lane = threadIdx.x & 63;
+    float bias[TJ][4];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = n0 + 16 * j + 4 * (lane >> 4) + i;
+            bias[j][i] = g.bias && n < g.N ? __uint_as_float((uint32_t)g.bias[(int64_t)t.e * g.N + n] << 16) : 0.0f;
+        }
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+        const int m = m0 + 16 * i + (lane & 15);
+        if (m >= t.m_end) continue;
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) {
+            const int n = n0 + 16 * j + 4 * (lane >> 4);
+            if (n >= g.N) continue;
+            float v[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = g.bias ? acc[i][j][c] + bias[j][c] : acc[i][j][c];
+            store4<OUT>(g.Y, (int64_t)m * g.ldy + n, v, g.N - n < 4 ? g.N - n : 4, vec);
+        }
+    }
+}
+
+template <int BM, int BN, int WGM, int WGN, int S, int KS, bool EXPERTS>
+__global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
+    constexpr int NW = WGM * WGN;                            // waves of a K group
+    constexpr int TI = BM / WGM / 16, TJ = BN / WGN / 16;
+    constexpr int kScalesX = (BM + BN) * 128, kScalesW = kScalesX + 4 * scale_words<BM>();
+    constexpr int kStage = kScalesW + 4 * scale_words<BN>();
+    constexpr int kLoads = Dma<BM, NW>::kLoads + Dma<BN, NW>::kLoads + ScaleDma<BM, BN, NW>::kEach;      // per wave and stage
+    constexpr int kRing = S * kStage;                        // of a K group
+    constexpr int kSums = (KS - 1) * BM * BN * 4;
+    static_assert(kSums <= KS * kRing, "the sums of the other K groups reuse the rings");
+    __shared__ __align__(1024) uint8_t smem[KS * kRing + 1024];
+    uint8_t* spare = smem + KS * kRing;
+    TileAt t;
+    if constexpr (EXPERTS) {
+        t = expert_tile<BM, BN>(g);
+        if (!t.any) return;
+        if (t.e == g.experts) {
+            zero_rows(g, t, BM, BN);
+            return;
+        }
+    } else {
+        t = block_tile<BM, BN>(g);
+    }
+    const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) % NW);
+    const int kg = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / NW);   // K group of the wave
+    uint8_t* lds = smem + kg * kRing;
+    const int wm = (wave / WGN) * (BM / WGM), wn = (wave % WGN) * (BN / WGN);
+    const int ld = g.K / 2, chunks = g.K / 128;              // bytes of a row
+    Dma<BM, NW> dx;
+    Dma<BN, NW> dw;
+    dx.init(g.X, ld, t.m0, t.m_end, wave);
+    dw.init(g.W + (int64_t)t.e * g.N * ld, ld, t.n0, g.N, wave);
+    const ScaleDma<BM, BN, NW> ds{g.sx + 4 * (int64_t)t.m0, g.sw + 4 * ((int64_t)t.e * chunks * g.N + t.n0), 4 * (int64_t)g.M,
+                                  4 * (int64_t)g.N, t.m_end - t.m0, g.N - t.n0};
+
+    f32x4 acc[TI][TJ];
+#pragma unroll
+    for (int i = 0; i < TI; ++i)
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int nk = (ld + 128 * KS - 1) / (128 * KS);
+    int step = kg;                                           // of the next loads
+    auto load = [&](uint8_t* stage) {                        // past K zeros are written, so no step has a tail
+        dx.load(128 * step, ld, stage, spare, wave);
+        dw.load(128 * step, ld, stage + BM * 128, spare, wave);
+        ds.load(step, chunks, stage + kScalesX, spare, wave);
+        step += KS;
+    };
+#pragma unroll
+    for (int p = 0; p < S; ++p) load(lds + p * kStage);
+    wait_loads<(S - 1) * kLoads>();                          // this wave's part of the first stage landed
+    __syncthreads();
+    i32x4 x0[TI], w0[TJ], x1[TI], w1[TJ];
+    int sx[TI], sw[TJ];
+    read_frags<TI>(lds, wm, 0, x0);
+    read_frags<TJ>(lds + BM * 128, wn, 0, w0);
+    read_scales<BM, TI>(lds + kScalesX, wm, sx);
+    read_scales<BN, TJ>(lds + kScalesW, wn, sw);
+    uint8_t* cur = lds;
+    for (int kt = 0; kt < nk; ++kt) {
+        uint8_t* nxt = cur + kStage == lds + kRing ? lds : cur + kStage;
+        __builtin_amdgcn_sched_barrier(0);
+        read_frags<TI>(cur, wm, 1, x1);
+        read_frags<TJ>(cur + BM * 128, wn, 1, w1);
+        multiply<0, TI, TJ>(x0, w0, sx, sw, acc);
+        interleave<TI + TJ, TI * TJ, 0x100>();
+        __builtin_amdgcn_sched_barrier(0);
+        wait_loads<(S - 2) * kLoads>();                      // all of this stage read, the next one landed
+        __syncthreads();
+        load(cur);
+        int nsx[TI], nsw[TJ];
+        read_frags<TI>(nxt, wm, 0, x0);
+        read_frags<TJ>(nxt + BM * 128, wn, 0, w0);
+        read_scales<BM, TI>(nxt + kScalesX, wm, nsx);
+        read_scales<BN, TJ>(nxt + kScalesW, wn, nsw);
+        multiply<1, TI, TJ>(x1, w1, sx, sw, acc);
+#pragma unroll
+        for (int i = 0; i < TI; ++i) sx[i] = nsx[i];
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) sw[j] = nsw[j];
+        cur = nxt;
+    }
+    __builtin_amdgcn_s_waitcnt(0x0F70);                      // no load may still write LDS when the block ends
+    if constexpr (KS > 1) {
+        __syncthreads();                                     // every group is done with its ring
+        f32x4* sums = reinterpret_cast<f32x4*>(smem) + (wave * TI * TJ) * 64 + (threadIdx.x & 63);
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) sums[((kg - 1) * NW * TI * TJ + i * TJ + j) * 64] = acc[i][j];
+        }
+        __syncthreads();
+        if (kg > 0) return;
+#pragma unroll
+        for (int q = 0; q < KS - 1; ++q)
+#pragma unroll
+            for (int i = 0; i < TI; ++i)
+#pragma unroll
+                for (int j = 0; j < TJ; ++j) acc[i][j] += sums[(q * NW * TI * TJ + i * TJ + j) * 64];
+    }
+
+    const bool vec = vec_out(g);
+    if (g.out == EP_BF16) store_tile<EP_BF16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+    else if (g.out == EP_F16) store_tile<EP_F16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+    else store_tile<EP_F32, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+}
+
+template <int BM, int BN, int WGM, int WGN, int S, int KS>
+hipError_t tiled_go(const GemmMxArgs& g, hipStream_t stream) {
+    int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
+    if (g.experts) blocks = (blocks + 7) / 8 * 8;              // an eighth of the tiles for each XCD
+    if (blocks * (64 * WGM * WGN * KS) > kMaxThreads) return hipErrorInvalidValue;
+    if (g.experts)
+        hipLaunchKernelGGL((gemm_mx<BM, BN, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
+    else
+        hipLaunchKernelGGL((gemm_mx<BM, BN, WGM, WGN, S, KS, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_rows_mx(const void* X, int src, int64_t rows, int64_t M, int64_t K, int64_t ldx, uint8_t* Q,
+                                   uint8_t* S, hipStream_t stream) {
+    if (rows <= 0 || K <= 0) return hipSuccess;
+    const MxGrid g = mx_grid(rows, M, K);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(g.blocks), dim3(256), 0, stream, X, M, K, ldx, Q, S, g.chunks, g.row_groups, g.units);
+        return hipGetLastError();
+    };
+    switch (src) {
+        case EP_F32: return go(quantize_rows_mx<EP_F32>);
+        case EP_BF16: return go(quantize_rows_mx<EP_BF16>);
+        case EP_F16: return go(quantize_rows_mx<EP_F16>);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_dequantize_rows_mx(const uint8_t* Q, const uint8_t* S, int64_t rows, int64_t M, int64_t Kp, int64_t K,
+                                     int dst, void* Y, hipStream_t stream) {
+    if (rows <= 0 || K <= 0) return hipSuccess;
+    const MxGrid g = mx_grid(rows, M, Kp);
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, dim3(g.blocks), dim3(256), 0, stream, Q, S, M, g.chunks, K, Y, g.row_groups, g.units);
+        return hipGetLastError();
+    };
+    switch (dst) {
+        case EP_F32: return go(dequantize_rows_mx<EP_F32>);
+        case EP_BF16: return go(dequantize_rows_mx<EP_BF16>);
+        case EP_F16: return go(dequantize_rows_mx<EP_F16>);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
+    if (g.M <= 0 || g.N <= 0) return hipSuccess;
+    const int64_t rows = g.experts ? (g.M + g.experts - 1) / g.experts : g.M;
+    if (rows > 64) return tiled_go<128, 128, 4, 4, 2, 1>(g, stream);
+    return tiled_go<16, 64, 1, 4, 4, 1>(g, stream);
+}
+
+}  // namespace ep

@@ -434,6 +434,59 @@ ep_status ep_linear_forward_experts(const ep_handle* const* w, int count, ep_dty
                                     const int64_t* host_offsets, const int32_t* dev_offsets, const void* const* dev_bias,
                                     void* dev_y, void* hip_stream);
 
+/* MXFP4 row quantizer: blocks of 32 consecutive elements of a row share a scale 2^(b - 127), b a byte; an element
+ * becomes a code of four bits, a sign and one of 0, 0.5, 1, 1.5, 2, 3, 4, 6, two codes to a byte, the even element in
+ * the low half.
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates", Abstract
+ * (containers that the computation's matrix units read); the format is the OCP Microscaling one, the layout of the
+ * scales this library's.
+ * b = max(0, floor(log2 a) + 127 - 2), a = max |x| over the block (b = 0 for a block of zeros); codes are x / 2^(b -
+ * 127) rounded to nearest, ties to the even code, at most 6 in magnitude. A block with an infinity or a NaN gets b =
+ * 255 (NaN) and codes 0, so that products with it are NaN. Rows are padded with zero codes to Kp, whole 128
+ * elements. dev_x: `rows` rows of K elements of src (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise), ldx >= K
+ * elements apart, any alignment of the element, taken as matrices of rows_per_matrix rows (a divisor of rows; the
+ * experts' weights, or rows itself); dev_q: [rows][Kp / 2]; dev_scale: [rows / rows_per_matrix][Kp / 128][rows_per_matrix]
+ * [4] bytes, the four scales of a row's 128 elements side by side; both 4-byte aligned. K <= 4194304, rows_per_matrix
+ * <= 2^27, rows < 2^40 (EP_ERANGE). Asynchronous on hip_stream; allocates nothing. */
+ep_status ep_quantize_rows_mxfp4(const void* dev_x, ep_dtype src, int64_t rows, int64_t rows_per_matrix, int64_t K, int64_t ldx,
+                                 uint8_t* dev_q, uint8_t* dev_scale, void* hip_stream);
+
+/* The values of MXFP4 codes: Y [rows][K] of dst (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise) from the first K
+ * columns of codes and scales of Kp columns (Kp % 128 == 0, Kp >= K, EP_EINVAL otherwise), laid out as
+ * ep_quantize_rows_mxfp4 does. Exact in EP_BF16 and EP_F32 up to scale bytes of 251, rounded to nearest even in EP_F16;
+ * a scale byte of 255 gives NaN.
+ * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates", Abstract
+ * (reconstruction of numerical values into a container). Limits as ep_quantize_rows_mxfp4. Asynchronous on
+ * hip_stream; allocates nothing. */
+ep_status ep_dequantize_rows_mxfp4(const uint8_t* dev_q, const uint8_t* dev_scale, int64_t rows, int64_t rows_per_matrix,
+                                   int64_t Kp, int64_t K, ep_dtype dst, void* dev_y, void* hip_stream);
+
+/* MXFP4 GEMM: Y[m][n] = sum over blocks b of 2^(xs[m][b] + ws[n][b] - 254) sum_{k in b} xq[m][k] wq[n][k] (+ bias[n]),
+ * the codes and scales of both operands as ep_quantize_rows_mxfp4 lays them out; fp32 sums on the matrix cores, biased in
+ * fp32 and rounded once to the output type. The same bits on every call; the order of the sum depends on M, N and K.
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one linear
+ * layer before a whole model" (the product of a layer whose weight is held in a container).
+ * xq [M][K / 2] and wq [N][K / 2] 16-byte aligned; xs [K / 128][M][4] and ws [K / 128][N][4] 4-byte aligned; bias [N]
+ * bf16 or NULL; Y [M][N] elements of out (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise). Requires K % 128 == 0
+ * (EP_EINVAL), K <= 4194304, M and N <= 2^27 (EP_ERANGE). The library's own kernels; asynchronous on hip_stream;
+ * allocates nothing. */
+ep_status ep_gemm_mxfp4(const uint8_t* dev_xq, const uint8_t* dev_xs, const uint8_t* dev_wq, const uint8_t* dev_ws, int64_t M,
+                        int64_t N, int64_t K, const void* dev_bias, ep_dtype out, void* dev_y, void* hip_stream);
+
+/* ep_gemm_mxfp4 with a weight per expert: rows [offsets[e], offsets[e + 1]) of xq (ep_sort_tokens' order) are
+ * multiplied by expert e's weight.
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one linear
+ * layer before a whole model". One launch for the experts of a layer is this library's scheduling, not a step of
+ * the method.
+ * xq [R][K / 2], xs [K / 128][R][4], wq [E][N][K / 2], ws [E][K / 128][N][4], offsets [E + 1] int32 in device memory,
+ * ascending, offsets[0] = 0, offsets[E] <= R (read by the kernels: nothing is copied to the host; offsets outside 0 ...
+ * R are clamped, so a wrong one gives wrong rows but no access out of bounds); bias [E][N] bf16 or NULL; Y [R][N] of
+ * out. Rows from offsets[E] on are set to zero. E in 1 ... 1024 (EP_ERANGE otherwise); other checks as ep_gemm_mxfp4.
+ * Asynchronous on hip_stream; allocates nothing. */
+ep_status ep_gemm_mxfp4_experts(const uint8_t* dev_xq, const uint8_t* dev_xs, const uint8_t* dev_wq, const uint8_t* dev_ws,
+                                const int32_t* dev_offsets, int E, int64_t R, int64_t N, int64_t K, const void* dev_bias,
+                                ep_dtype out, void* dev_y, void* hip_stream);
+
 /* Tokens sorted by the experts they chose (the input order of ep_gemm_int8_experts, and of compressed
  * layers run expert by expert).
  * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one

@@ -1,0 +1,120 @@
+"""Refusals of the MXFP4 operators on the CPU: sizes in the C ABI, tensors in the binding, before any device work."""
+import ctypes as C
+
+import pytest
+import torch
+
+import decode_tile_interleaved_rans_amd as ep
+import mx_reference as mx
+
+P = C.c_void_p(1 << 20)               # an aligned address that no call here may reach
+OFF4 = C.c_void_p((1 << 20) + 4)
+ODD = C.c_void_p((1 << 20) + 1)
+N0 = None
+EINVAL, EUNSUPPORTED, ERANGE = -1, -3, -4
+
+
+@pytest.mark.parametrize("rc,args", [
+    (EINVAL, (P, ep.BF16, -1, 1, 8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, -1, 8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, -8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, 3, 8, 8, P, P)),          # not whole matrices
+    (EINVAL, (P, ep.BF16, 4, 0, 8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, 8, 7, P, P)),          # rows overlap
+    (EINVAL, (N0, ep.BF16, 4, 4, 8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, 8, 8, N0, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, 8, 8, P, N0)),
+    (EINVAL, (ODD, ep.BF16, 4, 4, 8, 8, P, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, 8, 8, ODD, P)),
+    (EINVAL, (P, ep.BF16, 4, 4, 8, 8, P, ODD)),
+    (EUNSUPPORTED, (P, ep.I8, 4, 4, 8, 8, P, P)),
+    (EUNSUPPORTED, (P, 77, 4, 4, 8, 8, P, P)),
+    (ERANGE, (P, ep.BF16, 4, 4, 2 ** 22 + 1, 2 ** 22 + 1, P, P)),
+    (ERANGE, (P, ep.BF16, 2 ** 28, 2 ** 28, 8, 8, P, P)),
+    (ERANGE, (P, ep.BF16, 2 ** 40, 1, 8, 8, P, P)),
+    (ERANGE, (P, ep.BF16, 2 ** 30, 2 ** 20, 8, 2 ** 40, P, P)),
+    (0, (N0, ep.BF16, 0, 0, 8, 8, N0, N0)),
+    (0, (N0, ep.BF16, 4, 4, 0, 0, N0, N0)),
+])
+def test_quantizer(rc, args):
+    assert ep.lib().ep_quantize_rows_mxfp4(*args, None) == rc
+
+
+@pytest.mark.parametrize("rc,args", [
+    (EINVAL, (P, P, -1, 1, 128, 8, ep.BF16, P)),
+    (EINVAL, (P, P, 4, 4, 100, 8, ep.BF16, P)),
+    (EINVAL, (P, P, 4, 4, 128, 129, ep.BF16, P)),
+    (EINVAL, (P, P, 4, 4, 128, -1, ep.BF16, P)),
+    (EINVAL, (P, P, 4, 3, 128, 8, ep.BF16, P)),
+    (EINVAL, (N0, P, 4, 4, 128, 8, ep.BF16, P)),
+    (EINVAL, (P, N0, 4, 4, 128, 8, ep.BF16, P)),
+    (EINVAL, (P, P, 4, 4, 128, 8, ep.BF16, N0)),
+    (EINVAL, (P, P, 4, 4, 128, 8, ep.BF16, ODD)),
+    (EINVAL, (ODD, P, 4, 4, 128, 8, ep.BF16, P)),
+    (EINVAL, (P, ODD, 4, 4, 128, 8, ep.BF16, P)),
+    (EUNSUPPORTED, (P, P, 4, 4, 128, 8, ep.F8E4M3, P)),
+    (ERANGE, (P, P, 4, 4, 2 ** 22 + 128, 8, ep.BF16, P)),
+    (0, (N0, N0, 0, 0, 128, 8, ep.BF16, N0)),
+    (0, (P, P, 4, 4, 128, 0, ep.BF16, N0)),
+])
+def test_inverse(rc, args):
+    assert ep.lib().ep_dequantize_rows_mxfp4(*args, None) == rc
+
+
+@pytest.mark.parametrize("rc,M,N,K,out,xq,xs,wq,ws,y", [
+    (EINVAL, -1, 4, 128, ep.BF16, P, P, P, P, P),
+    (EINVAL, 4, 4, 64, ep.BF16, P, P, P, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, OFF4, P, P, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, ODD, P, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, P, OFF4, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, P, P, ODD, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, P, P, P, ODD),
+    (EINVAL, 4, 4, 128, ep.BF16, N0, P, P, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, N0, P, P, P),
+    (EINVAL, 4, 4, 128, ep.BF16, P, P, P, P, N0),
+    (EUNSUPPORTED, 4, 4, 128, ep.I8, P, P, P, P, P),
+    (ERANGE, 4, 4, 2 ** 22 + 128, ep.BF16, P, P, P, P, P),
+    (ERANGE, 2 ** 27 + 1, 4, 128, ep.BF16, P, P, P, P, P),
+    (ERANGE, 4, 2 ** 27 + 1, 128, ep.BF16, P, P, P, P, P),
+    (ERANGE, 2 ** 27, 2 ** 27, 128, ep.BF16, P, P, P, P, P),
+    (0, 0, 4, 128, ep.BF16, N0, N0, N0, N0, N0),
+    (0, 4, 0, 128, ep.BF16, N0, N0, N0, N0, N0),
+])
+def test_products(rc, M, N, K, out, xq, xs, wq, ws, y):
+    assert ep.lib().ep_gemm_mxfp4(xq, xs, wq, ws, M, N, K, None, out, y, None) == rc
+    assert ep.lib().ep_gemm_mxfp4_experts(xq, xs, wq, ws, P, 4, M, N, K, None, out, y, None) == rc
+
+
+def test_experts():
+    f = ep.lib().ep_gemm_mxfp4_experts
+    for E in (0, -1, 1025):
+        assert f(P, P, P, P, P, E, 4, 4, 128, None, ep.BF16, P, None) == ERANGE
+    assert f(P, P, P, P, None, 4, 4, 4, 128, None, ep.BF16, P, None) == EINVAL
+    assert b"offsets" in ep.lib().ep_last_error()
+
+
+def test_tensors_on_the_host():
+    with pytest.raises(ValueError):
+        ep.quantize_rows_mxfp4(torch.zeros((4, 64)))
+    with pytest.raises(ValueError):
+        ep.quantize_rows_mxfp4(torch.zeros((2, 4, 64)))
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        ep.dequantize_rows_mxfp4(u8(4, 64), u8(1, 4, 4))
+    with pytest.raises(ValueError):
+        ep.gemm_mxfp4(u8(4, 64), u8(1, 4, 4), u8(4, 64), u8(1, 4, 4))
+
+
+def test_the_reference_itself():
+    """The definition's codes are the nearest values of the grid: no other code is nearer, and scales put the
+    largest magnitude of a block into [4, 8) units."""
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn((6, 300), generator=g) * torch.exp(3 * torch.randn((6, 1), generator=g))
+    q, s = mx.quantize(x)
+    v = mx.values(q, s)
+    full = torch.nn.functional.pad(x.double(), (0, 84))
+    unit = torch.exp2(s.transpose(0, 1).reshape(6, -1).double() - 127).repeat_interleave(32, 1)
+    all_off = ((full.abs() / unit)[..., None].clamp_max(6.0) - mx.GRID).abs().amin(-1)
+    assert torch.equal(((full - v).abs() / unit).where((full / unit).abs() <= 6, all_off), all_off)
+    top = (full.abs() / unit).reshape(6, -1, 32).amax(-1)
+    assert ((top[:, :9] >= 4) & (top[:, :9] < 8)).all()

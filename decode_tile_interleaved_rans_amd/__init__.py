@@ -44,7 +44,7 @@ EXPORTS = ["ep_compress", "ep_free", "ep_stream_info", "ep_upload", "ep_handle_i
            "ep_pad_rows_int8", "ep_linear_forward_int8", "ep_linear_forward_int8_many",
            "ep_linear_forward_experts", "ep_sort_tokens_scratch", "ep_sort_tokens",
            "ep_combine_tokens", "ep_combine_tokens_grad", "ep_quantize_rows_mxfp4", "ep_dequantize_rows_mxfp4",
-           "ep_gemm_mxfp4", "ep_gemm_mxfp4_experts"]
+           "ep_gemm_mxfp4", "ep_gemm_mxfp4_experts", "ep_mlp_forward_experts_scratch", "ep_mlp_forward_experts"]
 
 
 class EPError(RuntimeError):
@@ -115,6 +115,9 @@ def lib() -> C.CDLL:
         L.ep_dequantize_rows_mxfp4.argtypes = [vp, vp, i64, i64, i64, i64, C.c_int, vp, vp]
         L.ep_gemm_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_gemm_mxfp4_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
+        L.ep_mlp_forward_experts_scratch.argtypes = [i64, C.c_int, i64, C.POINTER(sz)]
+        L.ep_mlp_forward_experts.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp, vp, vp, i64,
+                                             i64, vp, vp, vp]
         L.ep_handle_check.argtypes = [vp, vp]
         L.ep_release.argtypes = [vp]
         L.ep_release.restype = None
@@ -1063,3 +1066,72 @@ def linear_forward_experts(layers, x, expert_ids, weights=None, stream=None):
                                            _current_raw()),
            "ep_linear_forward_experts")
     return combine_tokens(ys, pos, weights)
+
+
+def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out_scales=None, in_bias=None, out_bias=None,
+                        stream=None):
+    """A mixture-of-experts layer of gated MLP experts for up to 64 tokens, in two kernels: y[t] = sum over j of weights[t, j]
+    (W_out[e] h + out_bias[e]), h = silu(g) u, (g, u) = W_in[e] x[t] + in_bias[e], e = expert_ids[t, j].
+
+    x: BF16 or FP16 [T, H] (rows may be further apart than H), T <= 64; expert_ids: [T, k] int32 or int64, T k <= 1024 (a
+    number outside 0 ... experts - 1 drops the choice; the same expert twice in a token counts once, with the sum of the
+    weights); weights: fp32 [T, k] or None (ones). w_in: [experts, 2 I, H], rows 0 ... I - 1 of an expert give g, the others u;
+    w_out: [experts, N, I]; both of x's type, or, with in_scales and out_scales, MXFP4 codes and scales as
+    quantize_rows_mxfp4 gives them (exact in BF16; in FP16 values below 2^-14 lose bits). Biases: BF16 [experts, 2 I] and
+    [experts, N]. fp32 sums; weights[t, j] h is rounded once to x's type, and y [T, N] once.
+
+    The weights of the experts that some token chose are read once; the host waits for nothing, so the call can be captured
+    into a graph. For more tokens use sort_tokens, a product per expert and combine_tokens. It has no gradient: tensors
+    that ask for one are refused. On `stream` (default: the current stream; another stream first waits for the current
+    one)."""
+    torch = _torch()
+    if stream is not None:
+        return _on_stream(stream, lambda: mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales, out_scales, in_bias,
+                                                              out_bias),
+                          x, expert_ids, weights, w_in, w_out, in_scales, out_scales, in_bias, out_bias)
+    if torch.is_grad_enabled():
+        for t in (x, weights, w_in, w_out, in_bias, out_bias):
+            if t is not None and t.requires_grad:
+                raise ValueError("the expert layer for few tokens has no gradient; detach its inputs")
+    _no_tangents(x, weights, w_in, w_out, in_bias, out_bias)
+    if x.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"x must be bfloat16 or float16, got {x.dtype}")
+    T, H, ldx = _need_rows(x, "x", (x.dtype,))
+    dev = x.get_device()
+    if expert_ids.dim() != 2 or expert_ids.shape[0] != T or expert_ids.dtype not in (torch.int32, torch.int64):
+        raise ValueError(f"expert_ids must be an int32 or int64 tensor of shape [{T}, choices]")
+    if T > 64 or expert_ids.numel() > 1024:
+        raise ValueError(f"at most 64 tokens and 1024 choices, got {T} and {expert_ids.numel()}; for more use sort_tokens, a product "
+                         "per expert and combine_tokens")
+    if (in_scales is None) != (out_scales is None):
+        raise ValueError("in_scales and out_scales go together: both weights are MXFP4, or neither")
+    if w_in.dim() != 3 or w_out.dim() != 3 or w_in.shape[0] != w_out.shape[0] or w_in.shape[1] % 2:
+        raise ValueError(f"w_in must be [experts, 2 I, H] and w_out [experts, N, I], got {tuple(w_in.shape)} and {tuple(w_out.shape)}")
+    E, I, N = w_in.shape[0], w_in.shape[1] // 2, w_out.shape[1]
+    if in_scales is None:
+        args = [("w_in", w_in, x.dtype, (E, 2 * I, H)), ("w_out", w_out, x.dtype, (E, N, I))]
+    else:
+        hc, ic = (H + 127) // 128, (I + 127) // 128
+        args = [("w_in", w_in, torch.uint8, (E, 2 * I, 64 * hc)), ("in_scales", in_scales, torch.uint8, (E, hc, 2 * I, 4)),
+                ("w_out", w_out, torch.uint8, (E, N, 64 * ic)), ("out_scales", out_scales, torch.uint8, (E, ic, N, 4))]
+    args.append(("expert_ids", expert_ids, expert_ids.dtype, expert_ids.shape))
+    if weights is not None:
+        args.append(("weights", weights, torch.float32, expert_ids.shape))
+    if in_bias is not None:
+        args.append(("in_bias", in_bias, torch.bfloat16, (E, 2 * I)))
+    if out_bias is not None:
+        args.append(("out_bias", out_bias, torch.bfloat16, (E, N)))
+    for name, t, dtype, shape in args:
+        if not _fits(t, dtype, shape, dev):
+            _need(t, name, dtype, shape=shape)
+    if in_scales is not None:
+        # codes are read in pieces of 16 bytes, scales in pieces of 4
+        w_in, w_out = _mx_aligned(w_in, 16), _mx_aligned(w_out, 16)
+        in_scales, out_scales = _mx_aligned(in_scales, 4), _mx_aligned(out_scales, 4)
+    k = expert_ids.shape[1]
+    y = torch.empty((T, N), dtype=x.dtype, device=x.device)
+    scratch = torch.empty((T * k, (I + 127) // 128 * 128), dtype=x.dtype, device=x.device)
+    _check(lib().ep_mlp_forward_experts(_ptr(x), _dtype_code(x.dtype), T, H, ldx, _ptr(expert_ids), expert_ids.element_size(), k, E,
+                                        _ptr(weights), _ptr(w_in), _ptr(in_scales), _ptr(in_bias), _ptr(w_out), _ptr(out_scales),
+                                        _ptr(out_bias), I, N, _ptr(scratch), _ptr(y), _current_raw()), "ep_mlp_forward_experts")
+    return y

@@ -19,6 +19,7 @@
 #include "gemm.h"
 #include "int8.h"
 #include "kernels.h"
+#include "mlp.h"
 #include "mxfp4.h"
 #include "route.h"
 #include "static_scratch.h"
@@ -618,6 +619,15 @@ ep_status check_combine(ep_dtype dtype, int64_t T, int k, int64_t H, int64_t R) 
         return fail(EP_EUNSUPPORTED, "tokens are summed in BF16, F16 or F32 rows");
     if (R > INT32_MAX || (k > 0 && T > INT32_MAX / k)) return fail(EP_ERANGE, "R and T k must be below 2^31");
     if (H > 0 && ((R > 0 && H > (INT64_MAX / 8) / R) || (T > 0 && H > (INT64_MAX / 8) / T))) return fail(EP_ERANGE, "the rows are too large");
+    return EP_OK;
+}
+
+// Sizes of the expert layer for few tokens.
+ep_status check_mlp(int64_t T, int k, int64_t I) {
+    if (T < 0 || k < 0 || I < 0) return fail(EP_EINVAL, "negative size");
+    if (T > ep::kMlpMaxTokens) return fail(EP_ERANGE, "more than 64 tokens: sort them by expert and use a product per expert");
+    if (T * k > ep::kMlpMaxChoices) return fail(EP_ERANGE, "more than 1024 choices");
+    if (I > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
     return EP_OK;
 }
 
@@ -1622,6 +1632,51 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
         const ep::CombineArgs c{dev_ys, dev_pos, dev_w, T, H, R, k, dtype};
         hipError_t e = ep::launch_combine_tokens_grad(c, dev_dy, dev_d_ys, dev_d_w, static_cast<hipStream_t>(hip_stream));
         return e == hipSuccess ? EP_OK : hip_fail(e, "token sum gradient launch");
+    });
+}
+
+ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int64_t I, size_t* bytes) {
+    return guarded([&]() -> ep_status {
+        if (!bytes) return fail(EP_EINVAL, "null pointer");
+        if (ep_status st = check_mlp(T, k, I); st != EP_OK) return st;
+        *bytes = ep::mlp_scratch(T, k, I);
+        return EP_OK;
+    });
+}
+
+ep_status ep_mlp_forward_experts(const void* dev_x, ep_dtype act, int64_t T, int64_t H, int64_t ldx, const void* dev_ids,
+                                 int id_bytes, int k, int E, const float* dev_w, const void* dev_w_in,
+                                 const uint8_t* dev_in_scales, const void* dev_in_bias, const void* dev_w_out,
+                                 const uint8_t* dev_out_scales, const void* dev_out_bias, int64_t I, int64_t N, void* dev_scratch,
+                                 void* dev_y, void* hip_stream) {
+    return guarded([&]() -> ep_status {
+        if (act != EP_BF16 && act != EP_F16) return fail(EP_EUNSUPPORTED, "the expert layer takes BF16 or F16 activations");
+        if (ep_status st = check_mlp(T, k, I); st != EP_OK) return st;
+        if (ep_status st = check_choices(T, k, E); st != EP_OK) return st;
+        if (H < 0 || N < 0) return fail(EP_EINVAL, "negative size");
+        if (H > 1 << 20 || N > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
+        if (ldx < H) return fail(EP_EINVAL, "rows of X overlap (ldx < H)");
+        if (ldx > INT64_MAX / 1024) return fail(EP_ERANGE, "X is too large");
+        if (id_bytes != 4 && id_bytes != 8) return fail(EP_EINVAL, "expert numbers must be int32 or int64");
+        const bool mx = dev_in_scales || dev_out_scales;
+        if (mx && ((H > 0 && I > 0 && !dev_in_scales) || (I > 0 && N > 0 && !dev_out_scales)))
+            return fail(EP_EINVAL, "both weights need scales, or neither");
+        if (T == 0 || N == 0) return EP_OK;
+        const bool any = k > 0;
+        if (!dev_y || (any && (!dev_ids || (I > 0 && (!dev_w_out || !dev_scratch)) || (I > 0 && H > 0 && (!dev_x || !dev_w_in)))))
+            return fail(EP_EINVAL, "null pointer");
+        const auto at = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+        if ((at(dev_x) | at(dev_y)) & 1) return fail(EP_EINVAL, "X or Y is not aligned to its elements");
+        if (at(dev_ids) & (uintptr_t)(id_bytes - 1)) return fail(EP_EINVAL, "the expert numbers are not aligned");
+        if (mx ? ((at(dev_w_in) | at(dev_w_out)) & 15 || (at(dev_in_scales) | at(dev_out_scales)) & 3) : ((at(dev_w_in) | at(dev_w_out)) & 1))
+            return fail(EP_EINVAL, "the weights are not aligned: codes to 16 bytes, scales to 4, others to their elements");
+        if (at(dev_scratch) & 15) return fail(EP_EINVAL, "the scratch must be 16-byte aligned");
+        const ep::MlpArgs a{dev_x, dev_ids, dev_w, dev_w_in, dev_in_scales, static_cast<const uint16_t*>(dev_in_bias), dev_w_out,
+                            dev_out_scales, static_cast<const uint16_t*>(dev_out_bias), dev_scratch, dev_y, ldx, (int)T, k, E, (int)H,
+                            (int)I, (int)N, id_bytes, act};
+        const hipError_t e = ep::launch_mlp(a, static_cast<hipStream_t>(hip_stream));
+        if (e == hipErrorInvalidValue) return fail(EP_ERANGE, "the layer is too large for one launch");
+        return e == hipSuccess ? EP_OK : hip_fail(e, "expert layer launch");
     });
 }
 

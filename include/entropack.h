@@ -534,6 +534,35 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
                                  const void* dev_dy, int64_t T, int k, int64_t H, int64_t R, void* dev_d_ys,
                                  float* dev_d_w, void* hip_stream);
 
+/* A mixture-of-experts layer of gated MLP experts for few tokens, in two kernels: y[t] = sum over j of w[t][j] (W_out[e] h
+ * + b_out[e]), h = silu(g) u, (g, u) = W_in[e] x[t] + b_in[e], e = ids[t][j], silu(g) = g / (1 + exp(-g)). The weights of
+ * the experts that some token chose are read once, nothing is sorted and nothing copied to the host.
+ * Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Replace one linear
+ * layer before a whole model" (layers inside a model's forward). Running an expert layer in two kernels is this
+ * library's scheduling, not a step of the method.
+ *   x: T rows of H elements of act (EP_BF16 or EP_F16; EP_EUNSUPPORTED otherwise), ldx >= H elements apart; y: [T][N] of act.
+ *   ids: [T][k] int32 or int64 (id_bytes 4 or 8); a number outside 0 ... E - 1 drops the choice. The same expert twice in
+ * a token counts once, with the sum of the weights. w: [T][k] fp32 or NULL (ones).
+ *   w_in: [E][2 I][H], rows 0 ... I - 1 of an expert give g, the others u; w_out: [E][N][I]. Elements of act, or, with
+ * in_scales and out_scales (both or neither, EP_EINVAL otherwise), MXFP4 codes [E][2 I][Hp / 2] and [E][N][Ip / 2] with
+ * scales [E][Hp / 128][2 I][4] and [E][Ip / 128][N][4] as ep_quantize_rows_mxfp4 lays them out (codes 16-byte, scales
+ * 4-byte aligned, EP_EINVAL); MXFP4 weights meet the activations in act's type (exact in EP_BF16 up to scale bytes of 251;
+ * in EP_F16 from 2^-14 to 65504). in_bias: [E][2 I], out_bias: [E][N], bf16 or NULL.
+ * fp32 sums; w h is rounded once to act's type, y once. The same bits on every call.
+ *   scratch: ep_mlp_forward_experts_scratch(T, k, I) bytes of device memory, 16-byte aligned (NULL when that is 0), read and
+ * written by this call's kernels only. T in 0 ... 64, T k <= 1024, E in 1 ... 1024, H, I and N <= 2^20 (EP_ERANGE): for more
+ * tokens sort them (ep_sort_tokens) and use a product per expert. Asynchronous on hip_stream; allocates nothing. */
+ep_status ep_mlp_forward_experts(const void* dev_x, ep_dtype act, int64_t T, int64_t H, int64_t ldx, const void* dev_ids,
+                                 int id_bytes, int k, int E, const float* dev_w, const void* dev_w_in,
+                                 const uint8_t* dev_in_scales, const void* dev_in_bias, const void* dev_w_out,
+                                 const uint8_t* dev_out_scales, const void* dev_out_bias, int64_t I, int64_t N, void* dev_scratch,
+                                 void* dev_y, void* hip_stream);
+
+/* Bytes of device scratch ep_mlp_forward_experts needs in *bytes. Source: "EntroPack PyTorch Guide: Lossless Weights,
+ * Bitrates and Memory Checks", section "Measure memory with clear boundaries" (temporary buffers of a call are part
+ * of its memory). */
+ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int64_t I, size_t* bytes);
+
 /* Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Test
  * saved artifacts and reloads before deployment" (a failed step must stop with a clear error);
  * reading R12 (every lane ends at its initial state: a free integrity check).

@@ -118,3 +118,32 @@ def test_the_reference_itself():
     assert torch.equal(((full - v).abs() / unit).where((full / unit).abs() <= 6, all_off), all_off)
     top = (full.abs() / unit).reshape(6, -1, 32).amax(-1)
     assert ((top[:, :9] >= 4) & (top[:, :9] < 8)).all()
+
+
+def test_expert_layer():
+    f, n = ep.lib().ep_mlp_forward_experts, C.c_size_t()
+
+    def call(x=P, act=ep.BF16, T=4, H=64, ldx=64, ids=P, ib=8, k=2, E=3, w=P, win=P, si=None, bi=None, wout=P, so=None, bo=None, I=32, N=16,
+             scr=P, y=P):
+        return f(x, act, T, H, ldx, ids, ib, k, E, w, win, si, bi, wout, so, bo, I, N, scr, y, None)
+
+    assert call(act=ep.F32) == EUNSUPPORTED and call(act=99) == EUNSUPPORTED
+    for c in (dict(T=-1), dict(k=-1), dict(H=-1), dict(I=-1), dict(N=-1), dict(ldx=63), dict(ib=2), dict(ids=None), dict(x=None), dict(y=None),
+              dict(win=None), dict(wout=None), dict(scr=None), dict(scr=OFF4), dict(x=ODD), dict(y=ODD), dict(win=ODD), dict(wout=ODD),
+              dict(ids=OFF4), dict(si=P), dict(so=P), dict(si=P, so=P, win=OFF4), dict(si=P, so=P, wout=OFF4), dict(si=ODD, so=P)):
+        assert call(**c) == EINVAL, c
+    for c in (dict(T=65), dict(T=64, k=17), dict(E=0), dict(E=1025), dict(H=2 ** 20 + 1, ldx=2 ** 21), dict(I=2 ** 20 + 1), dict(N=2 ** 20 + 1),
+              dict(ldx=2 ** 62)):
+        assert call(**c) == ERANGE, c
+    assert call(T=0, x=None, ids=None, y=None, scr=None) == 0 and call(N=0, y=None) == 0
+    s = ep.lib().ep_mlp_forward_experts_scratch
+    assert s(4, 2, 32, None) == EINVAL and s(65, 1, 32, C.byref(n)) == ERANGE and s(-1, 1, 32, C.byref(n)) == EINVAL
+    assert s(4, 2, 130, C.byref(n)) == 0 and n.value == 8 * 256 * 2
+    assert s(0, 2, 130, C.byref(n)) == 0 and n.value == 0
+
+
+def test_expert_layer_tensors_on_the_host():
+    t = torch.zeros
+    with pytest.raises(ValueError):
+        ep.mlp_forward_experts(t((4, 64), dtype=torch.bfloat16), t((4, 2), dtype=torch.int64), None, t((3, 64, 64), dtype=torch.bfloat16),
+                               t((3, 16, 32), dtype=torch.bfloat16))

@@ -635,40 +635,41 @@ def quantize_rows_mxfp4(x, stream=None):
     waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: quantize_rows_mxfp4(x), x)
-    torch = _torch()
-    lead = ()
-    if x.dim() == 3:
-        _need(x, "x", x.dtype)
-        lead = x.shape[:1]
-        M, K = x.shape[1:]
-        x = x.reshape(lead[0] * M, K)
-    elif x.dim() == 2:
+    dims = x.dim()
+    if dims == 2:
         M, K = x.shape
+    elif dims == 3:
+        _need(x, "x", x.dtype)
+        E, M, K = x.shape
+        x = x.reshape(E * M, K)
     else:
         raise ValueError(f"x must be [M, K] or [E, M, K], got shape {tuple(x.shape)}")
     rows, _, ldx = _need_rows(x, "x", _float_types())
-    chunks = (K + 127) // 128
-    q = torch.empty((*lead, M, 64 * chunks), dtype=torch.uint8, device=x.device)
-    s = torch.empty((*lead, chunks, M, 4), dtype=torch.uint8, device=x.device)
-    _check(lib().ep_quantize_rows_mxfp4(_ptr(x), _dtype_code(x.dtype), rows, M, K, ldx, _ptr(q), _ptr(s), _current_raw()),
-           "ep_quantize_rows_mxfp4")
+    u8, chunks = _torch().uint8, (K + 127) // 128
+    q = x.new_empty((M, 64 * chunks) if dims == 2 else (E, M, 64 * chunks), dtype=u8)
+    s = x.new_empty((chunks, M, 4) if dims == 2 else (E, chunks, M, 4), dtype=u8)
+    _check(lib().ep_quantize_rows_mxfp4(x.data_ptr(), _dtype_code(x.dtype), rows, M, K, ldx, q.data_ptr(), s.data_ptr(),
+                                        _current_raw()), "ep_quantize_rows_mxfp4")
     return q, s
 
 
-def _mx_shapes(q, s, qname: str, sname: str, dims):
-    """Shape checks of MXFP4 codes and scales; their padded width."""
-    if q.dim() not in dims or q.shape[-1] % 64:
-        raise ValueError(f"{qname} must be codes {' or '.join('[rows, Kp / 2]' if d == 2 else '[experts, rows, Kp / 2]' for d in dims)}"
-                         f", Kp a multiple of 128, got shape {tuple(q.shape)}")
-    torch = _torch()
-    chunks = q.shape[-1] // 64
-    shape = (*q.shape[:-2], chunks, q.shape[-2], 4)
-    dev = torch.cuda.current_device() if q.is_cuda else -1
-    if not _fits(q, torch.uint8, q.shape, dev):
-        _need(q, qname, torch.uint8)
-    if not _fits(s, torch.uint8, shape, dev):
-        _need(s, sname, torch.uint8, shape=shape)
-    return 128 * chunks
+def _mx_shapes(q, s, qname: str, sname: str, dims: int, dev):
+    """Checks of MXFP4 codes and scales of `dims` dimensions on the current device `dev` (None: the codes are not
+    on a GPU); their padded width. One quick test, as in _fits; where it fails, the reason is looked for."""
+    u8, shape = _torch().uint8, q.shape
+    half = shape[-1] if len(shape) == dims else 1
+    if dims == 2:
+        want = (half >> 6, shape[0], 4) if half != 1 else ()
+    else:
+        want = (shape[0], half >> 6, shape[1], 4) if half != 1 else ()
+    if not (half % 64 == 0 and s.shape == want and q.dtype is u8 and s.dtype is u8 and q.get_device() == dev == s.get_device()
+            and q.is_contiguous() and s.is_contiguous()):
+        if half % 64:
+            raise ValueError(f"{qname} must be codes {'[rows, Kp / 2]' if dims == 2 else '[experts, rows, Kp / 2]'}, Kp a multiple of "
+                             f"128, got shape {tuple(shape)}")
+        _need(q, qname, u8)
+        _need(s, sname, u8, shape=want)
+    return 2 * half
 
 
 def dequantize_rows_mxfp4(codes, scales, out_dtype=None, columns=None, stream=None):
@@ -682,12 +683,14 @@ def dequantize_rows_mxfp4(codes, scales, out_dtype=None, columns=None, stream=No
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in _float_types():
         raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-    Kp = _mx_shapes(codes, scales, "codes", "scales", (2, 3))
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"codes must be [M, Kp / 2] or [E, M, Kp / 2], got shape {tuple(codes.shape)}")
+    Kp = _mx_shapes(codes, scales, "codes", "scales", codes.dim(), torch.cuda.current_device() if codes.is_cuda else None)
     K = Kp if columns is None else columns
     if not 0 <= K <= Kp:
         raise ValueError(f"columns must be 0 ... {Kp}, got {columns}")
     M = codes.shape[-2]
-    y = torch.empty((*codes.shape[:-1], K), dtype=out_dtype, device=codes.device)
+    y = codes.new_empty((*codes.shape[:-1], K), dtype=out_dtype)
     codes, scales = _mx_aligned(codes, 4), _mx_aligned(scales, 4)
     _check(lib().ep_dequantize_rows_mxfp4(_ptr(codes), _ptr(scales), M * (codes.shape[0] if codes.dim() == 3 else 1), M, Kp, K,
                                           _dtype_code(out_dtype), _ptr(y), _current_raw()), "ep_dequantize_rows_mxfp4")
@@ -704,25 +707,27 @@ def _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype):
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in _float_types():
         raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-    K = _mx_shapes(xq, xs, "xq", "xs", (2,))
-    if _mx_shapes(wq, ws, "wq", "ws", (2 if offsets is None else 3,)) != K:
+    dev = torch.cuda.current_device() if xq.is_cuda else None
+    K = _mx_shapes(xq, xs, "xq", "xs", 2, dev)
+    if _mx_shapes(wq, ws, "wq", "ws", 2 if offsets is None else 3, dev) != K:
         raise ValueError(f"xq and wq must have the same width, got {K} and {2 * wq.shape[-1]}")
-    M, N = xq.shape[0], wq.shape[-2]
-    lead = tuple(wq.shape[:-1])
-    dev = torch.cuda.current_device()
+    M, lead = xq.shape[0], wq.shape[:-1]
+    N = lead[-1]
     if bias is not None and not _fits(bias, torch.bfloat16, lead, dev):
         _need(bias, "bias", torch.bfloat16, shape=lead)
     if offsets is not None and not _fits(offsets, torch.int32, (lead[0] + 1,), dev):
         _need(offsets, "offsets", torch.int32, shape=(lead[0] + 1,))
     # codes are read in pieces of 16 bytes, scales in pieces of 4
-    xq, wq, xs, ws = _mx_aligned(xq, 16), _mx_aligned(wq, 16), _mx_aligned(xs, 4), _mx_aligned(ws, 4)
-    y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-    tail = (_ptr(bias), _dtype_code(out_dtype), _ptr(y), _current_raw())
+    xp, wp, xsp, wsp = xq.data_ptr(), wq.data_ptr(), xs.data_ptr(), ws.data_ptr()
+    if (xp | wp) & 15 or (xsp | wsp) & 3:
+        xq, wq, xs, ws = _mx_aligned(xq, 16), _mx_aligned(wq, 16), _mx_aligned(xs, 4), _mx_aligned(ws, 4)
+        xp, wp, xsp, wsp = xq.data_ptr(), wq.data_ptr(), xs.data_ptr(), ws.data_ptr()
+    y = xq.new_empty((M, N), dtype=out_dtype)
+    tail = (_ptr(bias), _dtype_code(out_dtype), y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev))
     if offsets is None:
-        _check(lib().ep_gemm_mxfp4(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), M, N, K, *tail), "ep_gemm_mxfp4")
+        _check(lib().ep_gemm_mxfp4(xp, xsp, wp, wsp, M, N, K, *tail), "ep_gemm_mxfp4")
     else:
-        _check(lib().ep_gemm_mxfp4_experts(_ptr(xq), _ptr(xs), _ptr(wq), _ptr(ws), _ptr(offsets), lead[0], M, N, K, *tail),
-               "ep_gemm_mxfp4_experts")
+        _check(lib().ep_gemm_mxfp4_experts(xp, xsp, wp, wsp, offsets.data_ptr(), lead[0], M, N, K, *tail), "ep_gemm_mxfp4_experts")
     return y
 
 
@@ -1094,44 +1099,47 @@ def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out
             if t is not None and t.requires_grad:
                 raise ValueError("the expert layer for few tokens has no gradient; detach its inputs")
     _no_tangents(x, weights, w_in, w_out, in_bias, out_bias)
-    if x.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"x must be bfloat16 or float16, got {x.dtype}")
-    T, H, ldx = _need_rows(x, "x", (x.dtype,))
-    dev = x.get_device()
-    if expert_ids.dim() != 2 or expert_ids.shape[0] != T or expert_ids.dtype not in (torch.int32, torch.int64):
+    dtype, f32, bf16, u8 = x.dtype, torch.float32, torch.bfloat16, torch.uint8
+    if dtype is not bf16 and dtype is not torch.float16:
+        raise ValueError(f"x must be bfloat16 or float16, got {dtype}")
+    T, H, ldx = _need_rows(x, "x", (dtype,))
+    dev, chosen = x.get_device(), expert_ids.shape
+    if len(chosen) != 2 or chosen[0] != T or expert_ids.dtype not in (torch.int32, torch.int64):
         raise ValueError(f"expert_ids must be an int32 or int64 tensor of shape [{T}, choices]")
-    if T > 64 or expert_ids.numel() > 1024:
-        raise ValueError(f"at most 64 tokens and 1024 choices, got {T} and {expert_ids.numel()}; for more use sort_tokens, a product "
-                         "per expert and combine_tokens")
+    k = chosen[1]
+    if T > 64 or T * k > 1024:
+        raise ValueError(f"at most 64 tokens and 1024 choices, got {T} and {T * k}; for more use sort_tokens, a product per expert and "
+                         "combine_tokens")
     if (in_scales is None) != (out_scales is None):
         raise ValueError("in_scales and out_scales go together: both weights are MXFP4, or neither")
-    if w_in.dim() != 3 or w_out.dim() != 3 or w_in.shape[0] != w_out.shape[0] or w_in.shape[1] % 2:
-        raise ValueError(f"w_in must be [experts, 2 I, H] and w_out [experts, N, I], got {tuple(w_in.shape)} and {tuple(w_out.shape)}")
-    E, I, N = w_in.shape[0], w_in.shape[1] // 2, w_out.shape[1]
+    ins, outs = w_in.shape, w_out.shape
+    if len(ins) != 3 or len(outs) != 3 or ins[0] != outs[0] or ins[1] % 2:
+        raise ValueError(f"w_in must be [experts, 2 I, H] and w_out [experts, N, I], got {tuple(ins)} and {tuple(outs)}")
+    E, I, N = ins[0], ins[1] // 2, outs[1]
+    ic = (I + 127) // 128
     if in_scales is None:
-        args = [("w_in", w_in, x.dtype, (E, 2 * I, H)), ("w_out", w_out, x.dtype, (E, N, I))]
+        args = [("w_in", w_in, dtype, (E, 2 * I, H)), ("w_out", w_out, dtype, (E, N, I))]
     else:
-        hc, ic = (H + 127) // 128, (I + 127) // 128
-        args = [("w_in", w_in, torch.uint8, (E, 2 * I, 64 * hc)), ("in_scales", in_scales, torch.uint8, (E, hc, 2 * I, 4)),
-                ("w_out", w_out, torch.uint8, (E, N, 64 * ic)), ("out_scales", out_scales, torch.uint8, (E, ic, N, 4))]
-    args.append(("expert_ids", expert_ids, expert_ids.dtype, expert_ids.shape))
+        hc = (H + 127) // 128
+        args = [("w_in", w_in, u8, (E, 2 * I, 64 * hc)), ("in_scales", in_scales, u8, (E, hc, 2 * I, 4)),
+                ("w_out", w_out, u8, (E, N, 64 * ic)), ("out_scales", out_scales, u8, (E, ic, N, 4))]
+    args.append(("expert_ids", expert_ids, expert_ids.dtype, chosen))
     if weights is not None:
-        args.append(("weights", weights, torch.float32, expert_ids.shape))
+        args.append(("weights", weights, f32, chosen))
     if in_bias is not None:
-        args.append(("in_bias", in_bias, torch.bfloat16, (E, 2 * I)))
+        args.append(("in_bias", in_bias, bf16, (E, 2 * I)))
     if out_bias is not None:
-        args.append(("out_bias", out_bias, torch.bfloat16, (E, N)))
-    for name, t, dtype, shape in args:
-        if not _fits(t, dtype, shape, dev):
-            _need(t, name, dtype, shape=shape)
+        args.append(("out_bias", out_bias, bf16, (E, N)))
+    for name, t, kind, shape in args:
+        if not (t.dtype is kind and t.shape == shape and t.get_device() == dev and t.is_contiguous()):
+            _need(t, name, kind, shape=shape)
     if in_scales is not None:
         # codes are read in pieces of 16 bytes, scales in pieces of 4
         w_in, w_out = _mx_aligned(w_in, 16), _mx_aligned(w_out, 16)
         in_scales, out_scales = _mx_aligned(in_scales, 4), _mx_aligned(out_scales, 4)
-    k = expert_ids.shape[1]
-    y = torch.empty((T, N), dtype=x.dtype, device=x.device)
-    scratch = torch.empty((T * k, (I + 127) // 128 * 128), dtype=x.dtype, device=x.device)
-    _check(lib().ep_mlp_forward_experts(_ptr(x), _dtype_code(x.dtype), T, H, ldx, _ptr(expert_ids), expert_ids.element_size(), k, E,
-                                        _ptr(weights), _ptr(w_in), _ptr(in_scales), _ptr(in_bias), _ptr(w_out), _ptr(out_scales),
-                                        _ptr(out_bias), I, N, _ptr(scratch), _ptr(y), _current_raw()), "ep_mlp_forward_experts")
+    y, scratch = x.new_empty((T, N)), x.new_empty(T * k * 128 * ic)
+    _check(lib().ep_mlp_forward_experts(x.data_ptr(), _dtype_code(dtype), T, H, ldx, expert_ids.data_ptr(), expert_ids.element_size(),
+                                        k, E, _ptr(weights), w_in.data_ptr(), _ptr(in_scales), _ptr(in_bias), w_out.data_ptr(),
+                                        _ptr(out_scales), _ptr(out_bias), I, N, scratch.data_ptr(), y.data_ptr(),
+                                        torch._C._cuda_getCurrentRawStream(dev)), "ep_mlp_forward_experts")
     return y

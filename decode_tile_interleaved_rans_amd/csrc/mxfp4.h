@@ -41,7 +41,7 @@ struct GemmMxArgs {
     int M, N, K, ldy;       // K a multiple of 128
     int experts;            // 0: one weight for all rows
     int out;                // ep_dtype EP_BF16, EP_F16 or EP_F32
-    int rows;               // rows that the tile and the grid are made for: M
+    int rows;               // rows that the grid is made for: M
 };
 
 // Requires 16-byte aligned X and W, 4-byte aligned scales, K at most kMxMaxK, M and N at most kMxMaxRows. With

@@ -200,10 +200,14 @@ MxGrid mx_grid(int64_t rows, int64_t M, int64_t K) {
 
 // ------------------------------------------------------------------------------- tiled product
 // The ring of the INT8 product (int8.hip) on rows of 128 bytes, 256 codes, a step: both operand tiles go from global
-// memory straight into LDS, S stages deep, and the fragments of the next half step are read behind the current
-// MFMAs. A step has two halves of 128 codes; in half h the K group g of a lane takes chunk 2 g + h of the row, so that
-// its scale bytes of both halves are neighbours in one dword, (g % 2) * 16 bits up. The scales of a stage are two
-// dwords per row, loaded into LDS beside the codes: [2][rows], a contiguous piece of each 128 columns.
+// memory straight into LDS, S stages deep, and the fragments of the next sub-step are read behind the current
+// MFMAs. The K group of a lane takes neighbouring chunks of the row in the sub-steps of a step, so that its scale bytes
+// are neighbours in one dword and the instruction picks the byte. The scales of a stage are two dwords per row, loaded
+// into LDS beside the codes: [2][rows], a contiguous piece of each 128 columns.
+//
+// 4096 x 8192 x 8192 takes 122-138 us (boxes differ), 4.0-4.5 PFLOP/s, of which 20 go to the starts of the two rounds of
+// tiles and their 67 MB of outputs. Per 4096 of K it takes 53 us, 5.1 PFLOP/s: the matrix cores alone, without any memory,
+// reach 7.2 on random codes, where the card holds 1.7-1.9 GHz (9.9 on zeros).
 template <int ROWS>
 constexpr int scale_words() { return 2 * ROWS < 64 ? 64 : 2 * ROWS; }
 
@@ -233,68 +237,144 @@ struct ScaleDma {
     }
 };
 
-// Fragments of T 16-row parts from row r0 of an operand tile, half h of a stage.
-template <int T>
-__device__ __forceinline__ void read_frags(const uint8_t* tile, int r0, int h, i32x4 (&f)[T]) {
-    const int lane = threadIdx.x & 63, r = r0 + (lane & 15);
-    const uint8_t* p = tile + r * 128 + (((2 * (lane >> 4) + h) ^ chunk_swizzle(r)) << 4);
+// The matrix instruction of a tile: MR = 16 (v_mfma_scale_f32_16x16x128_f8f6f4) or 32 (v_mfma_scale_f32_32x32x64_f8f6f4,
+// lane l with row l % 32, K group l / 32 of two, C[8 (i / 4) + 4 (l / 32) + i % 4][l % 32]). A step of 256 codes takes
+// kSub sub-steps; in sub-step s a lane of K group g reads chunk kSub g + s of the row.
+template <int MR>
+struct Instr {
+    static constexpr int kSub = MR == 16 ? 2 : 4, kQuads = MR * MR / 256;    // quads: four consecutive rows of C in a lane
+    typedef float Acc __attribute__((ext_vector_type(4 * kQuads)));
+    static __device__ __forceinline__ int row() { return threadIdx.x & (MR - 1); }
+    static __device__ __forceinline__ int group() { return (threadIdx.x & 63) / MR; }
+};
+
+// Slot (before the swizzle) of the chunk that K group g reads in sub-step s: the groups of one sub-step side by side for
+// MR = 16, whose 64 lanes cover all banks only then (a third of the cycles of LDS went to conflicts with the chunks in
+// their own order); chunk_of is the inverse.
+template <int MR>
+__device__ __forceinline__ int slot_of(int g, int s) { return MR == 16 ? 4 * s + g : 4 * g + s; }
+template <int MR>
+__device__ __forceinline__ int chunk_of(int slot) { return MR == 16 ? 2 * (slot & 3) + (slot >> 2) : slot; }
+
+// Fragments of T parts of MR rows from row r0 of an operand tile, sub-step s of a stage.
+template <int MR, int T>
+__device__ __forceinline__ void read_frags(const uint8_t* tile, int r0, int s, i32x4 (&f)[T]) {
+    const int r = r0 + Instr<MR>::row();
+    const uint8_t* p = tile + r * 128 + ((slot_of<MR>(Instr<MR>::group(), s) ^ chunk_swizzle(r)) << 4);
 #pragma unroll
-    for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const i32x4*>(p + 16 * 128 * i);
+    for (int i = 0; i < T; ++i) f[i] = *reinterpret_cast<const i32x4*>(p + MR * 128 * i);
 }
 
-// Their scales of both halves (bytes 0 and 1); ROWS rows in the tile.
-template <int ROWS, int T>
+// Their scales, byte s for sub-step s; ROWS rows in the tile.
+template <int MR, int ROWS, int T>
 __device__ __forceinline__ void read_scales(const uint8_t* scales, int r0, int (&s)[T]) {
-    const int lane = threadIdx.x & 63;
-    const uint8_t* p = scales + 4 * ((lane >> 5) * ROWS + r0 + (lane & 15));
+    const int g = Instr<MR>::group();
+    const uint8_t* p = scales + 4 * ((MR == 16 ? g >> 1 : g) * ROWS + r0 + Instr<MR>::row());
 #pragma unroll
-    for (int i = 0; i < T; ++i) s[i] = *reinterpret_cast<const int*>(p + 64 * i) >> (lane & 16);
+    for (int i = 0; i < T; ++i) s[i] = *reinterpret_cast<const int*>(p + 4 * MR * i) >> (MR == 16 ? 16 * (g & 1) : 0);
 }
 
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return __builtin_shufflevector(v, v, 0, 1, 2, 3, -1, -1, -1, -1); }
 
-template <int H, int TI, int TJ>
+template <int MR, int H, int TI, int TJ>
 __device__ __forceinline__ void multiply(const i32x4 (&x)[TI], const i32x4 (&w)[TJ], const int (&sx)[TI], const int (&sw)[TJ],
-                                         f32x4 (&acc)[TI][TJ]) {
+                                         typename Instr<MR>::Acc (&acc)[TI][TJ]) {
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
         for (int j = 0; j < TJ; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w[j]), widen(x[i]), acc[i][j], 4, 4, H, sw[j], H, sx[i]);
+            if constexpr (MR == 16)
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w[j]), widen(x[i]), acc[i][j], 4, 4, H, sw[j], H, sx[i]);
+            else
+                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(w[j]), widen(x[i]), acc[i][j], 4, 4, H, sw[j], H, sx[i]);
 }
 
-// The epilogue of a wave's TI x TJ parts of 16 x 16: rows m0 + 16 i + lane % 16, columns n0 + 16 j + 4 (lane / 16).
-template <int OUT, int TI, int TJ>
-__device__ __forceinline__ void store_tile(const GemmMxArgs& g, const TileAt& t, int m0, int n0, const f32x4 (&acc)[TI][TJ], bool vec) {
-    const int lane = threadIdx.x & 63;
-    float bias[TJ][4];
+// Four consecutive columns of a part, from column n of the matrix on, with the bias; count of them are in the matrix.
+__device__ __forceinline__ void load_bias(const GemmMxArgs& g, int e, int n, int count, float (&bias)[4]) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) bias[c] = c < count ? __uint_as_float((uint32_t)g.bias[(int64_t)e * g.N + n + c] << 16) : 0.0f;
+}
+
+// The epilogue of a wave's TI x TJ parts of MR x MR: rows m0 + MR i + the lane's, columns n0 + MR j + 8 q + 4 (K group),
+// stored from the registers, four columns a lane: the small tiles.
+template <int OUT, int MR, int TI, int TJ>
+__device__ __forceinline__ void store_tile(const GemmMxArgs& g, const TileAt& t, int m0, int n0,
+                                           const typename Instr<MR>::Acc (&acc)[TI][TJ]) {
+    const bool vec = vec_out(g);
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int n = n0 + 16 * j + 4 * (lane >> 4) + i;
-            bias[j][i] = g.bias && n < g.N ? __uint_as_float((uint32_t)g.bias[(int64_t)t.e * g.N + n] << 16) : 0.0f;
+        for (int q = 0; q < Instr<MR>::kQuads; ++q) {
+            const int n = n0 + MR * j + 8 * q + 4 * Instr<MR>::group(), count = g.N - n < 4 ? g.N - n : 4;
+            if (count <= 0) continue;
+            float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (g.bias) load_bias(g, t.e, n, count, bias);
+#pragma unroll
+            for (int i = 0; i < TI; ++i) {
+                const int m = m0 + MR * i + Instr<MR>::row();
+                if (m >= t.m_end) continue;
+                float v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = g.bias ? acc[i][j][4 * q + c] + bias[c] : acc[i][j][4 * q + c];
+                store4<OUT>(g.Y, (int64_t)m * g.ldy + n, v, count, vec);
+            }
         }
+}
+
+// The same through LDS, MR rows at a time in a region of the wave's own, so that it stores whole rows of its columns, 16
+// bytes a lane (of any alignment): from the registers a store instruction touches 16 or 32 rows with 32 or 16 bytes each,
+// and 4096 x 8192 outputs of a single step of K took 31 us, now 20 (4096 x 8192 x 8192: 149 and 129).
+template <int OUT, int MR, int TJ>
+constexpr int stage_pitch() { return MR * TJ * (OUT == EP_F32 ? 4 : 2) + 16; }
+template <int OUT, int MR, int TI, int TJ>
+__device__ __forceinline__ void store_staged(const GemmMxArgs& g, const TileAt& t, int m0, int n0,
+                                             const typename Instr<MR>::Acc (&acc)[TI][TJ], uint8_t* lds) {
+    constexpr int kEs = OUT == EP_F32 ? 4 : 2, kPitch = stage_pitch<OUT, MR, TJ>(), kPieces = MR * TJ * kEs / 16, kOf = 16 / kEs;
+    const int lane = threadIdx.x & 63, cols = g.N - n0;
+    float bias[TJ][Instr<MR>::kQuads][4];
+    if (g.bias) {
+#pragma unroll
+        for (int j = 0; j < TJ; ++j)
+#pragma unroll
+            for (int q = 0; q < Instr<MR>::kQuads; ++q) {
+                const int c = MR * j + 8 * q + 4 * Instr<MR>::group();
+                load_bias(g, t.e, n0 + c, cols - c, bias[j][q]);
+            }
+    }
 #pragma unroll
     for (int i = 0; i < TI; ++i) {
-        const int m = m0 + 16 * i + (lane & 15);
-        if (m >= t.m_end) continue;
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) {
-            const int n = n0 + 16 * j + 4 * (lane >> 4);
-            if (n >= g.N) continue;
-            float v[4];
+        for (int j = 0; j < TJ; ++j)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) v[c] = g.bias ? acc[i][j][c] + bias[j][c] : acc[i][j][c];
-            store4<OUT>(g.Y, (int64_t)m * g.ldy + n, v, g.N - n < 4 ? g.N - n : 4, vec);
+            for (int q = 0; q < Instr<MR>::kQuads; ++q) {
+                float v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = g.bias ? acc[i][j][4 * q + c] + bias[j][q][c] : acc[i][j][4 * q + c];
+                uint8_t* at = lds + Instr<MR>::row() * kPitch + (MR * j + 8 * q + 4 * Instr<MR>::group()) * kEs;
+                store4<OUT>(at, 0, v, 4, true);
+            }
+        __builtin_amdgcn_wave_barrier();                     // LDS serves a wave's instructions in their order
+        const int rows = t.m_end - (m0 + MR * i);
+#pragma unroll
+        for (int p = 0; p < (MR * kPieces + 63) / 64; ++p) {
+            const int at = 64 * p + lane, r = at / kPieces, c = at % kPieces;
+            if (r >= MR || r >= rows || kOf * c >= cols) continue;
+            const uint8_t* from = lds + r * kPitch + 16 * c;
+            uint8_t* to = static_cast<uint8_t*>(g.Y) + ((int64_t)(m0 + MR * i + r) * g.ldy + n0) * kEs + 16 * c;
+            if (kOf * (c + 1) <= cols)
+                __builtin_memcpy(to, __builtin_assume_aligned(from, 16), 16);
+            else
+                for (int e = 0; e < cols - kOf * c; ++e) __builtin_memcpy(to + kEs * e, from + kEs * e, kEs);
         }
+        __builtin_amdgcn_wave_barrier();
     }
 }
 
-template <int BM, int BN, int WGM, int WGN, int S, int KS, bool EXPERTS>
+template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS, bool EXPERTS>
 __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
     constexpr int NW = WGM * WGN;                            // waves of a K group
-    constexpr int TI = BM / WGM / 16, TJ = BN / WGN / 16;
+    constexpr int TI = BM / WGM / MR, TJ = BN / WGN / MR, SUB = Instr<MR>::kSub, Q = Instr<MR>::kQuads;
+    static_assert(TI * WGM * MR == BM && TJ * WGN * MR == BN, "whole parts per wave");
     constexpr int kScalesX = (BM + BN) * 128, kScalesW = kScalesX + 4 * scale_words<BM>();
     constexpr int kStage = kScalesW + 4 * scale_words<BN>();
     constexpr int kLoads = Dma<BM, NW>::kLoads + Dma<BN, NW>::kLoads + ScaleDma<BM, BN, NW>::kEach;      // per wave and stage
@@ -323,14 +403,16 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
     Dma<BN, NW> dw;
     dx.init(g.X, ld, t.m0, t.m_end, wave);
     dw.init(g.W + (int64_t)t.e * g.N * ld, ld, t.n0, g.N, wave);
+    dx.chunk = 16 * chunk_of<MR>(dx.chunk / 16);
+    dw.chunk = 16 * chunk_of<MR>(dw.chunk / 16);
     const ScaleDma<BM, BN, NW> ds{g.sx + 4 * (int64_t)t.m0, g.sw + 4 * ((int64_t)t.e * chunks * g.N + t.n0), 4 * (int64_t)g.M,
                                   4 * (int64_t)g.N, t.m_end - t.m0, g.N - t.n0};
 
-    f32x4 acc[TI][TJ];
+    typename Instr<MR>::Acc acc[TI][TJ];
 #pragma unroll
     for (int i = 0; i < TI; ++i)
 #pragma unroll
-        for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j = 0; j < TJ; ++j) acc[i][j] = 0.0f;
 
     const int nk = (ld + 128 * KS - 1) / (128 * KS);
     int step = kg;                                           // of the next loads
@@ -344,30 +426,40 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
     for (int p = 0; p < S; ++p) load(lds + p * kStage);
     wait_loads<(S - 1) * kLoads>();                          // this wave's part of the first stage landed
     __syncthreads();
-    i32x4 x0[TI], w0[TJ], x1[TI], w1[TJ];
+    i32x4 x[2][TI], w[2][TJ];
     int sx[TI], sw[TJ];
-    read_frags<TI>(lds, wm, 0, x0);
-    read_frags<TJ>(lds + BM * 128, wn, 0, w0);
-    read_scales<BM, TI>(lds + kScalesX, wm, sx);
-    read_scales<BN, TJ>(lds + kScalesW, wn, sw);
+    read_frags<MR, TI>(lds, wm, 0, x[0]);
+    read_frags<MR, TJ>(lds + BM * 128, wn, 0, w[0]);
+    read_scales<MR, BM, TI>(lds + kScalesX, wm, sx);
+    read_scales<MR, BN, TJ>(lds + kScalesW, wn, sw);
     uint8_t* cur = lds;
     for (int kt = 0; kt < nk; ++kt) {
         uint8_t* nxt = cur + kStage == lds + kRing ? lds : cur + kStage;
-        __builtin_amdgcn_sched_barrier(0);
-        read_frags<TI>(cur, wm, 1, x1);
-        read_frags<TJ>(cur + BM * 128, wn, 1, w1);
-        multiply<0, TI, TJ>(x0, w0, sx, sw, acc);
-        interleave<TI + TJ, TI * TJ, 0x100>();
+        auto within = [&](auto at) {                         // sub-step s, the fragments of s + 1 read behind its MFMAs
+            constexpr int s = decltype(at)::value;
+            __builtin_amdgcn_sched_barrier(0);
+            read_frags<MR, TI>(cur, wm, s + 1, x[(s + 1) & 1]);
+            read_frags<MR, TJ>(cur + BM * 128, wn, s + 1, w[(s + 1) & 1]);
+            multiply<MR, s, TI, TJ>(x[s & 1], w[s & 1], sx, sw, acc);
+            interleave<TI + TJ, TI * TJ, 0x100>();
+        };
+        within(std::integral_constant<int, 0>{});
+        if constexpr (SUB == 4) {
+            within(std::integral_constant<int, 1>{});
+            within(std::integral_constant<int, 2>{});
+        }
         __builtin_amdgcn_sched_barrier(0);
         wait_loads<(S - 2) * kLoads>();                      // all of this stage read, the next one landed
         __syncthreads();
         load(cur);
         int nsx[TI], nsw[TJ];
-        read_frags<TI>(nxt, wm, 0, x0);
-        read_frags<TJ>(nxt + BM * 128, wn, 0, w0);
-        read_scales<BM, TI>(nxt + kScalesX, wm, nsx);
-        read_scales<BN, TJ>(nxt + kScalesW, wn, nsw);
-        multiply<1, TI, TJ>(x1, w1, sx, sw, acc);
+        read_frags<MR, TI>(nxt, wm, 0, x[0]);
+        read_frags<MR, TJ>(nxt + BM * 128, wn, 0, w[0]);
+        read_scales<MR, BM, TI>(nxt + kScalesX, wm, nsx);
+        read_scales<MR, BN, TJ>(nxt + kScalesW, wn, nsw);
+        multiply<MR, SUB - 1, TI, TJ>(x[1], w[1], sx, sw, acc);
+        interleave<kLoads, TI * TJ * 3 / 4, 0x20>();
+        interleave<TI + TJ + (TI + 1) / 2 + (TJ + 1) / 2, TI * TJ - TI * TJ * 3 / 4, 0x100>();
 #pragma unroll
         for (int i = 0; i < TI; ++i) sx[i] = nsx[i];
 #pragma unroll
@@ -376,6 +468,7 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
     }
     __builtin_amdgcn_s_waitcnt(0x0F70);                      // no load may still write LDS when the block ends
     if constexpr (KS > 1) {
+        static_assert(Q == 1, "small tiles");
         __syncthreads();                                     // every group is done with its ring
         f32x4* sums = reinterpret_cast<f32x4*>(smem) + (wave * TI * TJ) * 64 + (threadIdx.x & 63);
         if (kg > 0) {
@@ -394,21 +487,29 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
                 for (int j = 0; j < TJ; ++j) acc[i][j] += sums[(q * NW * TI * TJ + i * TJ + j) * 64];
     }
 
-    const bool vec = vec_out(g);
-    if (g.out == EP_BF16) store_tile<EP_BF16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
-    else if (g.out == EP_F16) store_tile<EP_F16, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
-    else store_tile<EP_F32, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, vec);
+    auto store = [&](auto out) {
+        constexpr int OUT = decltype(out)::value, kRegion = MR * stage_pitch<OUT, MR, TJ>();
+        if constexpr (KS == 1 && NW * kRegion <= kRing) {
+            __syncthreads();                                 // every wave is done with the ring
+            store_staged<OUT, MR, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc, smem + wave * kRegion);
+        } else {
+            store_tile<OUT, MR, TI, TJ>(g, t, t.m0 + wm, t.n0 + wn, acc);
+        }
+    };
+    if (g.out == EP_BF16) store(std::integral_constant<int, EP_BF16>{});
+    else if (g.out == EP_F16) store(std::integral_constant<int, EP_F16>{});
+    else store(std::integral_constant<int, EP_F32>{});
 }
 
-template <int BM, int BN, int WGM, int WGN, int S, int KS>
+template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS>
 hipError_t tiled_go(const GemmMxArgs& g, hipStream_t stream) {
     int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
     if (g.experts) blocks = (blocks + 7) / 8 * 8;              // an eighth of the tiles for each XCD
     if (blocks * (64 * WGM * WGN * KS) > kMaxThreads) return hipErrorInvalidValue;
     if (g.experts)
-        hipLaunchKernelGGL((gemm_mx<BM, BN, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
+        hipLaunchKernelGGL((gemm_mx<BM, BN, MR, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
     else
-        hipLaunchKernelGGL((gemm_mx<BM, BN, WGM, WGN, S, KS, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
+        hipLaunchKernelGGL((gemm_mx<BM, BN, MR, WGM, WGN, S, KS, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -446,11 +547,63 @@ hipError_t launch_dequantize_rows_mx(const uint8_t* Q, const uint8_t* S, int64_t
     }
 }
 
+// Tile of a product with one weight: the least of (1 + share (rounds - 1)) (steps step_us + tile_us), rounds of tiles over the
+// CUs, steps of 256 KS columns; share is below 1 where a CU holds several blocks. The figures are fitted to 120 products (M 1 ...
+// 4096; N x K 1024 x 2048 ... 8192 x 8192 and 4096 x 16384, weights that come from HBM), where the tile that they pick takes
+// 1.6% longer than the fastest of 20 on average and 15% at most. They pick, e.g., 256 x 256 for 4096 x 8192 x 8192 (122 us; 256
+// x 192: 145, 256 x 128: 154, 128 x 128: 165), 256 x 192 for 1024 x 11520 x 3840 (28; 256 x 256: 29, 256 x 128: 39), 128 x 128 for
+// 512 x 8192 x 8192 (25; 128 x 64: 31), 128 x 64 for 333 x 5003 x 3968 (11.3; 64 x 64: 11.8, 128 x 128: 12.0), 64 x 64 for 256 x 4096 x
+// 4096 (7.7; 128 x 64: 10.5), 32 x 32 for 64 x 8192 x 8192 (13.1; 64 x 64: 14.5), 16 x 32 with two K groups for 1 x 11520 x 3840 (7.0;
+// 32 x 32: 7.3) and with four for 1 x 4096 x 16384 (10.4; two: 11.6). The instruction of 16 rows takes less power than that
+// of 32 (7.2 PFLOP/s of random codes without memory, 6.4), which tells in the largest tiles; in 128 x 128 and 64 x 64, where
+// waves have 64 x 32 or 32 x 32 of them, the one of 32 rows is ahead by 4 to 10%.
+struct TileCost {
+    int bm, bn, ks;
+    float step_us, tile_us, share;
+    hipError_t (*go)(const GemmMxArgs&, hipStream_t);
+};
+const TileCost kTiles[] = {
+    {256, 256, 1, 1.309f, 3.06f, 1.0f, tiled_go<256, 256, 16, 2, 4, 2, 1>}, {256, 192, 1, 1.088f, 2.90f, 1.0f, tiled_go<256, 192, 16, 2, 4, 2, 1>},
+    {256, 128, 1, 0.848f, 2.22f, 1.0f, tiled_go<256, 128, 16, 4, 2, 3, 1>}, {128, 128, 1, 0.553f, 0.76f, 1.0f, tiled_go<128, 128, 32, 2, 4, 3, 1>},
+    {128, 64, 1, 0.431f, 0.91f, 0.86f, tiled_go<128, 64, 16, 4, 2, 3, 1>},  {64, 64, 1, 0.257f, 0.25f, 0.91f, tiled_go<64, 64, 32, 2, 2, 4, 1>},
+    {32, 32, 2, 0.246f, 0.53f, 0.95f, tiled_go<32, 32, 16, 1, 2, 4, 2>},    {16, 32, 2, 0.259f, 0.10f, 0.65f, tiled_go<16, 32, 16, 1, 2, 3, 2>},
+    {16, 32, 4, 0.436f, 1.42f, 1.0f, tiled_go<16, 32, 16, 1, 2, 4, 4>},
+};
+
 hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
-    const int64_t rows = g.experts ? (g.M + g.experts - 1) / g.experts : g.M;
-    if (rows > 64) return tiled_go<128, 128, 4, 4, 2, 1>(g, stream);
-    return tiled_go<16, 64, 1, 4, 4, 1>(g, stream);
+    const int64_t cus = device_cus();
+    auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
+    auto cost = [&](const TileCost& t, int64_t row_tiles) {
+        const int64_t rounds = over(row_tiles * over(g.N, t.bn), cus);
+        return (1.0f + t.share * (float)(rounds - 1)) * ((float)over(g.K, 256 * t.ks) * t.step_us + t.tile_us);
+    };
+    if (!g.experts) {
+        const TileCost* best = nullptr;
+        float least = 0.0f;
+        for (const TileCost& t : kTiles) {
+            const float us = cost(t, over(g.M, t.bm));
+            if (!best || us < least) best = &t, least = us;
+        }
+        return best->go(g, stream);
+    }
+    // Experts: how many rows each has is known to the device only, so the tile goes by the average. Measured with rows
+    // spread unevenly (a factor of e^0.5 as standard deviation), weights that come from HBM, in us: 2 rows each on 16 x 64 23.2 (32
+    // experts of 4096 x 2048; 64 x 128: 24.1) and 12.1 at 1 row each of 64 of 1024 x 2048 (64 x 128: 14.2); 8 rows on 64 x 128 28.8 (16 x 64:
+    // 30.8) and 81.6 (128 of 2816 x 2048; 16 x 64: 88.4); 24 rows on 128 x 128, two blocks to a CU, 33.3 and 17.2 (64 of 1024 x 2048; 64 x 128:
+    // 36.2 and 21.3); 64 rows on 64 x 128 40.0 and 34.1 (32 of 2048 x 4096; 128 x 128, where the larger experts begin a second
+    // row tile: 45.7 and over 40); 100 rows on 128 x 128 43.3 and 121 (128 of 2816 x 2048; 64 x 128: 50.6, 256 x 256: 136). Above that
+    // whichever of 256 x 256 and 256 x 192 fills its rounds better: 200 rows 62 and 56 (128 x 128: 66 and 63), 400 rows of 8 of
+    // 8192 x 4096 on 256 x 192 86 (256 x 256: 99), 800 rows of 128 of 2816 x 2048 on 256 x 256 505 (256 x 192: 545).
+    const int64_t used = g.M < g.experts ? g.M : g.experts, rows = over(g.M, used);
+    if (rows > 150) {
+        // a partly filled tile per expert: half a tile on average
+        const int64_t tiles = (2 * g.M + 256 * used) / 512;
+        return cost(kTiles[1], tiles) < cost(kTiles[0], tiles) ? kTiles[1].go(g, stream) : kTiles[0].go(g, stream);
+    }
+    if (rows <= 2) return tiled_go<16, 64, 16, 1, 4, 4, 1>(g, stream);
+    if (rows <= 20 || (rows > 40 && rows <= 64)) return tiled_go<64, 128, 32, 2, 4, 3, 1>(g, stream);
+    return tiled_go<128, 128, 32, 2, 4, 2, 1>(g, stream);
 }
 
 }  // namespace ep

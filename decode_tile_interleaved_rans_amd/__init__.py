@@ -12,6 +12,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import os
 
 import numpy as np
@@ -115,7 +116,7 @@ def lib() -> C.CDLL:
         L.ep_dequantize_rows_mxfp4.argtypes = [vp, vp, i64, i64, i64, i64, C.c_int, vp, vp]
         L.ep_gemm_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, vp, C.c_int, vp, vp]
         L.ep_gemm_mxfp4_experts.argtypes = [vp, vp, vp, vp, vp, C.c_int, i64, i64, i64, vp, C.c_int, vp, vp]
-        L.ep_mlp_forward_experts_scratch.argtypes = [i64, C.c_int, i64, C.POINTER(sz)]
+        L.ep_mlp_forward_experts_scratch.argtypes = [i64, C.c_int, C.c_int, i64, i64, C.c_int, C.POINTER(sz)]
         L.ep_mlp_forward_experts.argtypes = [vp, C.c_int, i64, i64, i64, vp, C.c_int, C.c_int, C.c_int, vp, vp, vp, vp, vp, vp, vp, i64,
                                              i64, vp, vp, vp]
         L.ep_handle_check.argtypes = [vp, vp]
@@ -1073,6 +1074,14 @@ def linear_forward_experts(layers, x, expert_ids, weights=None, stream=None):
     return combine_tokens(ys, pos, weights)
 
 
+@functools.lru_cache(maxsize=256)
+def _mlp_scratch(T: int, k: int, E: int, I: int, N: int, mxfp4: bool) -> int:
+    """Bytes of scratch that mlp_forward_experts needs for these sizes."""
+    need = C.c_size_t()
+    _check(lib().ep_mlp_forward_experts_scratch(T, k, E, I, N, mxfp4, C.byref(need)), "ep_mlp_forward_experts")
+    return need.value
+
+
 def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out_scales=None, in_bias=None, out_bias=None,
                         stream=None):
     """A mixture-of-experts layer of gated MLP experts for up to 64 tokens, in two kernels: y[t] = sum over j of weights[t, j]
@@ -1137,7 +1146,7 @@ def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out
         # codes are read in pieces of 16 bytes, scales in pieces of 4
         w_in, w_out = _mx_aligned(w_in, 16), _mx_aligned(w_out, 16)
         in_scales, out_scales = _mx_aligned(in_scales, 4), _mx_aligned(out_scales, 4)
-    y, scratch = x.new_empty((T, N)), x.new_empty(T * k * 128 * ic)
+    y, scratch = x.new_empty((T, N)), x.new_empty(_mlp_scratch(T, k, E, I, N, in_scales is not None), dtype=u8)
     _check(lib().ep_mlp_forward_experts(x.data_ptr(), _dtype_code(dtype), T, H, ldx, expert_ids.data_ptr(), expert_ids.element_size(),
                                         k, E, _ptr(weights), w_in.data_ptr(), _ptr(in_scales), _ptr(in_bias), w_out.data_ptr(),
                                         _ptr(out_scales), _ptr(out_bias), I, N, scratch.data_ptr(), y.data_ptr(),

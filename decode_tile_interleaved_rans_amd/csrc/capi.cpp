@@ -623,12 +623,12 @@ ep_status check_combine(ep_dtype dtype, int64_t T, int k, int64_t H, int64_t R) 
 }
 
 // Sizes of the expert layer for few tokens.
-ep_status check_mlp(int64_t T, int k, int64_t I) {
-    if (T < 0 || k < 0 || I < 0) return fail(EP_EINVAL, "negative size");
+ep_status check_mlp(int64_t T, int k, int E, int64_t I, int64_t N) {
+    if (T < 0 || k < 0 || I < 0 || N < 0) return fail(EP_EINVAL, "negative size");
     if (T > ep::kMlpMaxTokens) return fail(EP_ERANGE, "more than 64 tokens: sort them by expert and use a product per expert");
     if (T * k > ep::kMlpMaxChoices) return fail(EP_ERANGE, "more than 1024 choices");
-    if (I > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
-    return EP_OK;
+    if (I > 1 << 20 || N > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
+    return check_choices(T, k, E);
 }
 
 }  // namespace
@@ -1635,11 +1635,11 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
     });
 }
 
-ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int64_t I, size_t* bytes) {
+ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int E, int64_t I, int64_t N, int mxfp4, size_t* bytes) {
     return guarded([&]() -> ep_status {
         if (!bytes) return fail(EP_EINVAL, "null pointer");
-        if (ep_status st = check_mlp(T, k, I); st != EP_OK) return st;
-        *bytes = ep::mlp_scratch(T, k, I);
+        if (ep_status st = check_mlp(T, k, E, I, N); st != EP_OK) return st;
+        *bytes = ep::mlp_scratch(T, k, E, I, N, mxfp4 != 0);
         return EP_OK;
     });
 }
@@ -1651,10 +1651,9 @@ ep_status ep_mlp_forward_experts(const void* dev_x, ep_dtype act, int64_t T, int
                                  void* dev_y, void* hip_stream) {
     return guarded([&]() -> ep_status {
         if (act != EP_BF16 && act != EP_F16) return fail(EP_EUNSUPPORTED, "the expert layer takes BF16 or F16 activations");
-        if (ep_status st = check_mlp(T, k, I); st != EP_OK) return st;
-        if (ep_status st = check_choices(T, k, E); st != EP_OK) return st;
-        if (H < 0 || N < 0) return fail(EP_EINVAL, "negative size");
-        if (H > 1 << 20 || N > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
+        if (H < 0) return fail(EP_EINVAL, "negative size");
+        if (ep_status st = check_mlp(T, k, E, I, N); st != EP_OK) return st;
+        if (H > 1 << 20) return fail(EP_ERANGE, "H, I and N must be at most 2^20");
         if (ldx < H) return fail(EP_EINVAL, "rows of X overlap (ldx < H)");
         if (ldx > INT64_MAX / 1024) return fail(EP_ERANGE, "X is too large");
         if (id_bytes != 4 && id_bytes != 8) return fail(EP_EINVAL, "expert numbers must be int32 or int64");

@@ -22,7 +22,7 @@ struct MlpArgs {
     const void* w_out;          // [E][N][I] of `act` or codes [E][N][Ip / 2]
     const uint8_t* s_out;       // null, or [E][Ip / 128][N][4]
     const uint16_t* b_out;      // [E][N] bf16 or null
-    void* h;                    // scratch: mlp_scratch() bytes, 16-byte aligned
+    void* scratch;              // mlp_scratch() bytes, 16-byte aligned
     void* y;                    // [T][N] of `act`
     int64_t ldx;
     int T, k, E, H, I, N;
@@ -30,7 +30,8 @@ struct MlpArgs {
     int act;                    // ep_dtype EP_BF16 or EP_F16
 };
 
-size_t mlp_scratch(int64_t T, int64_t k, int64_t I);
+// mx: the weights are MXFP4.
+size_t mlp_scratch(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N, bool mx);
 
 // T at most kMlpMaxTokens, T k at most kMlpMaxChoices, E at most kRouteMaxExperts.
 hipError_t launch_mlp(const MlpArgs& a, hipStream_t stream);

@@ -1,12 +1,17 @@
 // gfx950 expert layer for few tokens: y[t] = sum over j of w[t][j] (W_out[e] h + b_out[e]), h = silu(g) u, (g, u) = W_in[e] x[t] +
-// b_in[e], e = ids[t][j], in two kernels, without a sort, a host wait or atomics on memory. With few tokens the weights of
-// the experts that some token chose are all that counts: both kernels stream them once from memory straight into the
-// matrix operands and split K over the waves of a block.
+// b_in[e], e = ids[t][j], in two kernels, without a sort or a host wait. With few tokens the weights of the experts that
+// some token chose are all that counts: both kernels stream them from memory straight into the matrix operands and split K
+// over the waves of a block, whose sums are added in a fixed order.
 //
 // A token that names an expert twice meets it once, with the sum of the two weights. w[t][j] goes into h before its one
-// rounding to the activations' type (the same relative error as rounding h itself): a column of the second
-// product is then a token, not a choice, its sum runs over all experts in the matrix accumulators, and nothing has to
-// be added up afterwards.
+// rounding to the activations' type (the same relative error as rounding h itself), so that the second product's sums
+// over the experts need no further factors.
+//
+// What bounds it: 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16 read 1.4 GB in 229 us, 6.1 TB/s (a read of 400 MB in
+// this pattern alone reaches 6.0). In MXFP4 the tokens' loads count as well: 64 tokens on 8 of 128 experts of 2048 x 1408
+// take 188 us for 0.58 GB, 110 of them the first product, which without the tokens' loads and products would take 95. Small
+// layers are bound by latency: each kernel takes 6 to 8 us beside the transfer of its weights (one token on 4 of 32 experts
+// of 2048 x 1408 in BF16 28 us for 69 MB).
 //
 // Operand lane layout (v_mfma_f32_16x16x32, checked on the device): lane l supplies eight elements of A row l % 16 and
 // of B column l % 16, K group l / 16, and receives C[4 (l / 16) + i][l % 16], i < 4. A and B take the same K positions per
@@ -29,49 +34,90 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
 // ------------------------------------------------------------------------------------ the choices
-// The tokens of every expert as a mask of 64 bits, in LDS.
 __device__ __forceinline__ int64_t choice(const MlpArgs& a, int c) {
     return a.id_bytes == 8 ? static_cast<const int64_t*>(a.ids)[c] : (int64_t) static_cast<const int32_t*>(a.ids)[c];
 }
-__device__ __forceinline__ void fill_masks(const MlpArgs& a, unsigned long long* masks) {
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) masks[e] = 0;
+
+// s_waitcnt lgkmcnt(0) and a barrier: what waves exchange through LDS is there, and loads from memory stay in flight.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// The routing of a call, in LDS of every block of the first kernel. The experts with tokens, in ascending order, are the
+// slots; the tokens of a slot, in ascending order, are consecutive rows of h.
+struct Routing {
+    float weight[kMlpMaxChoices];                   // of a row: its choices' weights, added in their order
+    uint16_t expert[kMlpMaxChoices];                // of a slot
+    uint16_t first[kMlpMaxChoices + 1];             // a slot's first row; behind the last slot, the number of rows
+    uint8_t token[kMlpMaxChoices];                  // of a row
+    int slots;
+};
+struct RoutingWork {
+    unsigned long long masks[kRouteMaxExperts];     // the tokens of an expert
+    int16_t id[kMlpMaxChoices];                     // of a choice, -1 where it is dropped
+    uint16_t slot[kRouteMaxExperts];                // of an expert with tokens
+};
+__device__ __forceinline__ void route(const MlpArgs& a, Routing& r, RoutingWork& w) {
+    const int n = a.T * a.k;
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) w.masks[e] = 0;
     __syncthreads();
-    for (int c = threadIdx.x; c < a.T * a.k; c += blockDim.x) {
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
         const int64_t e = choice(a, c);
-        if (e >= 0 && e < a.E) atomicOr(&masks[e], 1ull << (c / a.k));
+        const bool in = e >= 0 && e < a.E;
+        w.id[c] = in ? (int16_t)e : (int16_t)-1;
+        if (in) atomicOr(&w.masks[e], 1ull << (c / a.k));
+    }
+    __syncthreads();
+    if (threadIdx.x < 64) {                          // 64 experts at a time, one per lane
+        const int lane = threadIdx.x;
+        int slots = 0, rows = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 64) {
+            const unsigned long long m = e0 + lane < a.E ? w.masks[e0 + lane] : 0;
+            const uint64_t hit = __ballot(m != 0);
+            if (!hit) continue;
+            int upto = __popcll(m);
+#pragma unroll
+            for (int o = 1; o < 64; o <<= 1) {
+                const int v = __shfl_up(upto, o);
+                if (lane >= o) upto += v;
+            }
+            if (m) {
+                const int slot = slots + __popcll(hit & ((1ull << lane) - 1));
+                r.expert[slot] = (uint16_t)(e0 + lane);
+                r.first[slot] = (uint16_t)(rows + upto - __popcll(m));
+                w.slot[e0 + lane] = (uint16_t)slot;
+            }
+            slots += __popcll(hit);
+            rows += __builtin_amdgcn_readlane(upto, 63);
+        }
+        if (lane == 0) r.slots = slots, r.first[slots] = (uint16_t)rows;
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < n; c += blockDim.x) {
+        const int e = w.id[c], t = c / a.k;
+        if (e < 0) continue;
+        bool again = false;                          // the token has named the expert before
+        for (int o = t * a.k; o < c; ++o) again |= w.id[o] == e;
+        if (again) continue;
+        float sum = a.w ? a.w[c] : 1.0f;
+        for (int o = c + 1; o < (t + 1) * a.k; ++o)
+            if (w.id[o] == e) sum += a.w ? a.w[o] : 1.0f;
+        const int row = r.first[w.slot[e]] + __popcll(w.masks[e] & ((1ull << t) - 1));
+        r.weight[row] = sum;
+        r.token[row] = (uint8_t)t;
     }
     __syncthreads();
 }
 
-// The experts with tokens, in ascending order, are the slots; a slot's tokens have consecutive rows in h. One
-// expert per lane, 64 at a time: f(lane has one, e, mask, slot, first row) for every one; returns their number.
-template <typename F>
-__device__ __forceinline__ int each_slot(const MlpArgs& a, const unsigned long long* masks, F&& f) {
-    const int lane = threadIdx.x & 63;
-    int slots = 0, rows = 0;
-    for (int e0 = 0; e0 < a.E; e0 += 64) {
-        const unsigned long long m = e0 + lane < a.E ? masks[e0 + lane] : 0;
-        const uint64_t hit = __ballot(m != 0);
-        int upto = __popcll(m);
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const int v = __shfl_up(upto, o);
-            if (lane >= o) upto += v;
-        }
-        f(m != 0, e0 + lane, m, slots + __popcll(hit & ((1ull << lane) - 1)), rows + upto - __popcll(m));
-        slots += __popcll(hit);
-        rows += __builtin_amdgcn_readlane(upto, 63);
-    }
-    return slots;
-}
-
-// The weight of token t's choices of expert e together, added in their order.
-__device__ __forceinline__ float share(const MlpArgs& a, int t, int e) {
-    float s = 0.0f;
-    for (int j = 0; j < a.k; ++j)
-        if (choice(a, t * a.k + j) == e) s += a.w ? a.w[t * a.k + j] : 1.0f;
-    return s;
-}
+// What the first kernel leaves for the second, before h in the scratch.
+struct Plan {
+    int slots;
+    uint16_t expert[kMlpMaxChoices], first[kMlpMaxChoices + 1];              // of a slot, as in Routing
+    uint8_t token[kMlpMaxChoices];                                          // of a row
+};
 
 // ------------------------------------------------------------------------------------ the operands
 template <int ACT>
@@ -80,19 +126,6 @@ __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), c, 0, 0, 0);
     else
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, w), __builtin_bit_cast(f16x8, x), c, 0, 0, 0);
-}
-
-// Eight elements of a row of K from k on, zeros past its end; rows at any alignment of the element.
-__device__ __forceinline__ u32x4 row_piece(const uint16_t* row, int64_t k, int64_t K) {
-    u32x4 v = {0, 0, 0, 0};
-    if (k + 8 <= K) {
-        __builtin_memcpy(&v, row + k, 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (k + i < K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
-    }
-    return v;
 }
 
 // K goes in chunks of 128, four MFMA steps each. In step s the lane's eight elements are 32 s + 8 (l / 16) + i of the
@@ -104,44 +137,82 @@ __device__ __forceinline__ int k_of(int s) {
     return MX ? 32 * g + 8 * s : 32 * s + 8 * g;
 }
 
+// One row of K 16-bit elements per lane, at any alignment of the element. load() reads what the lane needs of chunk c without
+// a branch, so that the loads of the next piece stay in flight behind the current products: a lane whose eight elements
+// reach past the row's end reads its last eight. fix() puts those right where they are used: zeros past the end.
+struct Row16 {
+    const uint16_t* p;
+    int K;
+    template <bool MX>
+    __device__ __forceinline__ void load(int c, u32x4 (&v)[4]) const {
+        if (K >= 8) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const int k = 128 * c + k_of<MX>(s);
+                __builtin_memcpy(&v[s], p + (k < K - 8 ? k : K - 8), 16);
+            }
+        } else {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) v[s] = u32x4{0, 0, 0, 0};
+            if (c == 0 && k_of<MX>(0) == 0) {        // the one lane of a row that has any
+#pragma unroll
+                for (int i = 0; i < 7; ++i)
+                    if (i < K) v[0][i / 2] |= (uint32_t)p[i] << (16 * (i % 2));
+            }
+        }
+    }
+    template <bool MX>
+    __device__ __forceinline__ void fix(int c, u32x4 (&v)[4]) const {
+        if (128 * (c + 1) <= K) return;
+        const int r = K >= 8 ? -K & 7 : 0;           // elements before those of the lane that straddles the end
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int left = K - (128 * c + k_of<MX>(s));
+            u32x4 t = v[s];
+            if (r & 4) t = u32x4{t[2], t[3], 0, 0};
+            if (r & 2) t = u32x4{t[1], t[2], t[3], 0};
+            if (r & 1) t = u32x4{t[0] >> 16 | t[1] << 16, t[1] >> 16 | t[2] << 16, t[2] >> 16 | t[3] << 16, t[3] >> 16};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[s][i] = left >= 8 ? v[s][i] : left > 0 ? t[i] : 0;
+        }
+    }
+};
+
 // A chunk of a weight row per lane, as it comes from memory.
 template <bool MX>
-struct Piece {
+struct Chunk {
     u32x4 v[MX ? 1 : 4];
     uint32_t scale;
 };
 // One row per lane (l % 16) of a weight matrix.
-template <int ACT, bool MX>
+template <bool MX>
 struct Rows {
-    const uint8_t* w;
-    const uint8_t* s;
-    int64_t K, apart;           // apart: bytes between the scales of two chunks
+    Row16 r;
+    const uint8_t *w, *s;
+    int64_t apart;              // bytes between the scales of two chunks
     // row `row` of expert e's [n][K] matrix
-    __device__ __forceinline__ void init(const void* W, const uint8_t* S, int e, int64_t n, int64_t K_, int64_t row) {
-        K = K_;
+    __device__ __forceinline__ void init(const void* W, const uint8_t* S, int e, int64_t n, int K, int64_t row) {
         if constexpr (MX) {
             const int64_t chunks = (K + 127) / 128;
             w = static_cast<const uint8_t*>(W) + (e * n + row) * chunks * 64 + 16 * ((threadIdx.x & 63) >> 4);
             s = S + (e * chunks * n + row) * 4;
             apart = 4 * n;
         } else {
-            w = static_cast<const uint8_t*>(W) + (e * n + row) * K * 2;
+            r = Row16{static_cast<const uint16_t*>(W) + (e * n + row) * K, K};
         }
     }
-    __device__ __forceinline__ void load(int c, Piece<MX>* p) const {
+    __device__ __forceinline__ void load(int c, Chunk<MX>* p) const {
         if constexpr (MX) {
             p->v[0] = *reinterpret_cast<const u32x4*>(w + 64 * (int64_t)c);
             p->scale = *reinterpret_cast<const uint32_t*>(s + c * apart);
         } else {
-            const int64_t k0 = 128 * (int64_t)c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) p->v[i] = row_piece(reinterpret_cast<const uint16_t*>(w), k0 + k_of<false>(i), K);
+            r.load<false>(c, p->v);
         }
     }
 };
 // The operand of step s. MXFP4 values are exact in BF16, and in FP16 from 2^-14 to 65504.
 template <int ACT, bool MX>
-__device__ __forceinline__ u32x4 operand(const Piece<MX>& p, int s) {
+__device__ __forceinline__ u32x4 operand(const Chunk<MX>& p, int s) {
     if constexpr (!MX) {
         return p.v[s];
     } else {
@@ -171,169 +242,339 @@ __device__ __forceinline__ float bf16_at(const uint16_t* p, int64_t i) { return 
 
 __host__ __device__ inline int64_t padded(int64_t n) { return (n + 127) / 128 * 128; }
 
-// ----------------------------------------------------------------------------------- first product
-// A block: 16 columns of h (their gate and up rows) of one slot's expert, for up to 16 TT of its tokens at a time. Its
-// waves take the chunks of K in turn; their sums meet in LDS.
-template <int ACT, bool MX, int TT, int NW>
-__global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a) {
-    __shared__ unsigned long long masks[kRouteMaxExperts];
-    __shared__ float sums[NW][2 * TT][256];
-    __shared__ int tokens[kMlpMaxTokens];
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int tiles = (int)(padded(a.I) / 16);
-    const int slot = blockIdx.x / tiles, i0 = 16 * (int)(blockIdx.x % tiles);
-    fill_masks(a, masks);
-    int e = -1, base = 0;
-    unsigned long long mask = 0;
-    each_slot(a, masks, [&](bool any, int e_, unsigned long long m, int s, int row) {
-        const uint64_t mine = __ballot(any && s == slot);
-        if (mine) {
-            const int l = __builtin_ctzll(mine);
-            e = __builtin_amdgcn_readlane(e_, l);
-            base = __builtin_amdgcn_readlane(row, l);
-            mask = (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)m, l) |
-                   (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(m >> 32), l) << 32;
+// The scratch: Plan, a counter for every tile of y's columns, the splits' sums of y, h.
+struct Layout {
+    int tiles, width, splits;   // of the second product: tiles of columns, their columns together, splits of K
+};
+struct Scratch {
+    Plan* plan;
+    int* done;
+    float* part;                // [splits][T][width]
+    uint16_t* h;                // [rows][ldh]
+};
+__host__ __device__ inline int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+__host__ __device__ inline int64_t part_at(const Layout& l) { return up16(sizeof(Plan)) + up16(4 * (int64_t)l.tiles); }
+__host__ __device__ inline int64_t h_at(const Layout& l, int64_t T) {
+    return part_at(l) + (l.splits > 1 ? l.splits * T * l.width * 4 : 0);
+}
+__device__ __forceinline__ Scratch scratch_of(const MlpArgs& a, const Layout& l) {
+    uint8_t* p = static_cast<uint8_t*>(a.scratch);
+    return Scratch{reinterpret_cast<Plan*>(p), reinterpret_cast<int*>(p + up16(sizeof(Plan))), reinterpret_cast<float*>(p + part_at(l)),
+                   reinterpret_cast<uint16_t*>(p + h_at(l, a.T))};
+}
+
+// The operands of a piece, SC chunks of M weight tiles of 16 rows and of 16 TT tokens. A wave has two sets of them and
+// fills one while it multiplies the other.
+template <int ACT, bool MX, int M, int SC, int TT>
+struct Piece {
+    Chunk<MX> w[M][SC];
+    u32x4 x[TT][SC][4];
+    // piece p of rows of `chunks` chunks; a chunk past the last one reads that again, and its tokens count as zeros
+    __device__ __forceinline__ void load(const Rows<MX> (&rows)[M], const Row16 (&xs)[TT], int p, int chunks) {
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int c = SC * p + i < chunks ? SC * p + i : chunks - 1;
+#pragma unroll
+            for (int m = 0; m < M; ++m) rows[m].load(c, &w[m][i]);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) xs[t].template load<MX>(c, x[t][i]);
         }
-    });
-    if (e < 0) return;
-    const int n = __popcll(mask);
-    if (threadIdx.x < 64 && (mask >> lane & 1)) tokens[__popcll(mask & ((1ull << lane) - 1))] = lane;
-    __syncthreads();
-    const int64_t ldh = padded(a.I);
-    const int chunks = (a.H + 127) / 128;
-    const int r = i0 + (lane & 15), row = r < a.I ? r : a.I - 1;            // columns past I: zeros, stored below
-    Rows<ACT, MX> gate, up;
-    gate.init(a.w_in, a.s_in, e, 2 * (int64_t)a.I, a.H, row);
-    up.init(a.w_in, a.s_in, e, 2 * (int64_t)a.I, a.H, a.I + (int64_t)row);
-    for (int n0 = 0; n0 < n; n0 += 16 * TT) {
-        const uint16_t* x[TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int at = n0 + 16 * i + (lane & 15);
-            x[i] = at < n ? static_cast<const uint16_t*>(a.x) + tokens[at] * a.ldx : nullptr;
-        }
-        f32x4 g[TT], u[TT];
-#pragma unroll
-        for (int i = 0; i < TT; ++i) g[i] = u[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (i0 < a.I) {
-            Piece<MX> pg, pu;
-            if (wave < chunks) gate.load(wave, &pg), up.load(wave, &pu);
-            for (int c = wave; c < chunks; c += NW) {
-                u32x4 xv[TT][4];
-#pragma unroll
-                for (int i = 0; i < TT; ++i)
-#pragma unroll
-                    for (int s = 0; s < 4; ++s)
-                        xv[i][s] = x[i] ? row_piece(x[i], 128 * (int64_t)c + k_of<MX>(s), a.H) : u32x4{0, 0, 0, 0};
-                Piece<MX> ng = pg, nu = pu;
-                if (c + NW < chunks) gate.load(c + NW, &ng), up.load(c + NW, &nu);
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const u32x4 wg = operand<ACT, MX>(pg, s), wu = operand<ACT, MX>(pu, s);
-#pragma unroll
-                    for (int i = 0; i < TT; ++i) {
-                        g[i] = mfma<ACT>(wg, xv[i][s], g[i]);
-                        u[i] = mfma<ACT>(wu, xv[i][s], u[i]);
-                    }
-                }
-                pg = ng, pu = nu;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            *reinterpret_cast<f32x4*>(&sums[wave][2 * i][4 * lane]) = g[i];
-            *reinterpret_cast<f32x4*>(&sums[wave][2 * i + 1][4 * lane]) = u[i];
-        }
-        __syncthreads();
-        for (int i = wave; i < TT; i += NW) {
-            const int at = n0 + 16 * i + (lane & 15), col = i0 + 4 * (lane >> 4);
-            if (at < n) {
-                f32x4 gs = {0.0f, 0.0f, 0.0f, 0.0f}, us = gs;
-#pragma unroll
-                for (int v = 0; v < NW; ++v) {
-                    gs += *reinterpret_cast<const f32x4*>(&sums[v][2 * i][4 * lane]);
-                    us += *reinterpret_cast<const f32x4*>(&sums[v][2 * i + 1][4 * lane]);
-                }
-                const float part = share(a, tokens[at], e);
-                uint16_t o[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t b = (int64_t)e * 2 * a.I + col + q;
-                    const bool in = col + q < a.I;
-                    const float gv = in ? gs[q] + bf16_at(a.b_in, b) : 0.0f, uv = in ? us[q] + bf16_at(a.b_in, b + a.I) : 0.0f;
-                    o[q] = in ? to_act<ACT>(part * (gv / (1.0f + expf(-gv)) * uv)) : 0;
-                }
-                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.h) + (base + at) * ldh + col) =
-                    make_uint2(o[0] | (uint32_t)o[1] << 16, o[2] | (uint32_t)o[3] << 16);
-            }
-        }
-        __syncthreads();                                                    // the sums are free for the next tokens
     }
+    // rows of Kw (16-bit weights) and Kx elements
+    __device__ __forceinline__ void multiply(int Kw, int Kx, int p, f32x4 (&acc)[M][TT]) {
+#pragma unroll
+        for (int i = 0; i < SC; ++i) {
+            const int c = SC * p + i;
+            if constexpr (!MX) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) Row16{nullptr, Kw}.fix<false>(c, w[m][i].v);
+            }
+#pragma unroll
+            for (int t = 0; t < TT; ++t) Row16{nullptr, Kx}.template fix<MX>(c, x[t][i]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+                    const u32x4 o = operand<ACT, MX>(w[m][i], s);
+#pragma unroll
+                    for (int t = 0; t < TT; ++t) acc[m][t] = mfma<ACT>(o, x[t][i][s], acc[m][t]);
+                }
+        }
+    }
+};
+
+// ----------------------------------------------------------------------------------- first product
+// A unit of work is 16 P columns of h (their gate and up rows) of one slot's expert for all its tokens, 16 TT in a pass over
+// the weights (more tokens take further passes, whose weights come from L2). A block takes a contiguous range of the
+// units; in each its waves take the pieces of K in turn, those of the next unit in flight behind the current one's
+// products, and their sums meet in LDS, where one wave finishes 16 columns of 16 tokens while the others go on.
+template <int ACT, bool MX, int P, int SC, int TT, int NW>
+__global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
+    constexpr int COLS = 16 * P, kSums = NW * 2 * P * TT * 1024;
+    __shared__ Routing r;
+    __shared__ __align__(16) uint8_t work[sizeof(RoutingWork) > kSums ? sizeof(RoutingWork) : kSums];
+    float (*sums)[2 * P * TT][256] = reinterpret_cast<float (*)[2 * P * TT][256]>(work);
+    const Scratch to = scratch_of(a, lay);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int64_t ldh = padded(a.I);
+    const int tiles = (int)(ldh / COLS), chunks = (a.H + 127) / 128, pieces = (chunks + SC - 1) / SC;
+    route(a, r, *reinterpret_cast<RoutingWork*>(work));
+    if (blockIdx.x == 0) {
+        for (int s = threadIdx.x; s < r.slots; s += blockDim.x) to.plan->expert[s] = r.expert[s];
+        for (int s = threadIdx.x; s <= r.slots; s += blockDim.x) to.plan->first[s] = r.first[s];
+        for (int i = threadIdx.x; i < r.first[r.slots]; i += blockDim.x) to.plan->token[i] = r.token[i];
+        for (int i = threadIdx.x; i < lay.tiles; i += blockDim.x) to.done[i] = 0;
+        if (threadIdx.x == 0) to.plan->slots = r.slots;
+    }
+    const int units = r.slots * tiles;
+    const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+    if (u0 >= u1) return;
+
+    // Unit, first token of the pass, piece: what is loaded next, and what is multiplied next, in the same order. All waves
+    // take as many steps per pass; those without a piece left in it do nothing in the last.
+    struct At {
+        int u, from, p, e, base, n;
+    };
+    auto open = [&](At& t) {
+        const int s = t.u / tiles;
+        t.e = __builtin_amdgcn_readfirstlane((int)r.expert[s]);
+        t.base = __builtin_amdgcn_readfirstlane((int)r.first[s]);
+        t.n = __builtin_amdgcn_readfirstlane((int)r.first[s + 1]) - t.base;
+        t.from = 0;
+    };
+    auto next = [&](At& t) {                         // true at the end of a pass
+        t.p += NW;
+        if (t.p - wave < pieces) return false;
+        t.p = wave;
+        t.from += 16 * TT;
+        if (t.from >= t.n && ++t.u < u1) open(t);
+        return true;
+    };
+    At l{u0, 0, wave, 0, 0, 0};
+    Rows<MX> rows[2 * P];
+    Row16 x[TT];
+    auto point = [&]() {                             // the rows of l
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
+            const int c = COLS * (l.u % tiles) + 16 * i + (lane & 15);
+            const int row = c < a.I ? c : a.I - 1;   // columns past I are not used
+            rows[2 * i].init(a.w_in, a.s_in, l.e, 2 * (int64_t)a.I, a.H, row);
+            rows[2 * i + 1].init(a.w_in, a.s_in, l.e, 2 * (int64_t)a.I, a.H, a.I + (int64_t)row);
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {               // lanes without a token read the last one's
+            const int at = l.from + 16 * i + (lane & 15);
+            x[i] = Row16{static_cast<const uint16_t*>(a.x) + r.token[l.base + (at < l.n ? at : l.n - 1)] * a.ldx, a.H};
+        }
+    };
+    typedef Piece<ACT, MX, 2 * P, SC, TT> Ops;
+    auto load = [&](Ops& o) {
+        if (l.u >= u1 || pieces == 0) return;
+        o.load(rows, x, l.p < pieces ? l.p : pieces - 1, chunks);
+        if (next(l) && l.u < u1) point();
+    };
+    open(l);
+    At m = l;
+    point();
+    f32x4 acc[2 * P][TT];
+    auto clear = [&]() {
+#pragma unroll
+        for (int q = 0; q < 2 * P; ++q)
+#pragma unroll
+            for (int i = 0; i < TT; ++i) acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    };
+    clear();
+    int turn = 0;                                    // of the waves at finishing
+    auto step = [&](Ops& o) {                        // false at the end of the range
+        if (m.p < pieces) o.multiply(a.H, a.H, m.p, acc);
+        const At t = m;
+        const bool end = next(m);
+        load(o);
+        if (!end) return true;
+        lds_barrier();                               // the last pass's sums are read
+#pragma unroll
+        for (int q = 0; q < 2 * P; ++q)
+#pragma unroll
+            for (int i = 0; i < TT; ++i) *reinterpret_cast<f32x4*>(&sums[wave][q * TT + i][4 * lane]) = acc[q][i];
+        clear();
+        lds_barrier();
+#pragma unroll
+        for (int j = 0; j < P * TT; ++j) {           // 16 columns of 16 tokens
+            if (wave != (turn + j) % NW) continue;
+            const int q = j / TT, i = j % TT;
+            const int at = t.from + 16 * i + (lane & 15), col = COLS * (t.u % tiles) + 16 * q + 4 * (lane >> 4);
+            if (at >= t.n) continue;
+            f32x4 gs = {0.0f, 0.0f, 0.0f, 0.0f}, us = gs;
+#pragma unroll
+            for (int v = 0; v < NW; ++v) {
+                gs += *reinterpret_cast<const f32x4*>(&sums[v][2 * q * TT + i][4 * lane]);
+                us += *reinterpret_cast<const f32x4*>(&sums[v][(2 * q + 1) * TT + i][4 * lane]);
+            }
+            if (a.b_in) {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    const int64_t b = (int64_t)t.e * 2 * a.I + (col + v < a.I ? col + v : a.I - 1);
+                    gs[v] += bf16_at(a.b_in, b);
+                    us[v] += bf16_at(a.b_in, b + a.I);
+                }
+            }
+            const float part = r.weight[t.base + at];
+            uint16_t o4[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) o4[v] = col + v < a.I ? to_act<ACT>(part * (gs[v] / (1.0f + expf(-gs[v])) * us[v])) : 0;
+            *reinterpret_cast<uint2*>(to.h + (t.base + at) * ldh + col) = make_uint2(o4[0] | (uint32_t)o4[1] << 16, o4[2] | (uint32_t)o4[3] << 16);
+        }
+        turn += P * TT;
+        return m.u < u1;
+    };
+    Ops o0, o1;
+    load(o0);
+    load(o1);
+    while (step(o0) && step(o1)) {}
 }
 
 // ---------------------------------------------------------------------------------- second product
-// A block: 16 columns of y for all tokens, column t of the product being token t. Its waves take the chunks of all
-// slots' K in turn; a token that did not choose a slot's expert has zeros there.
-template <int ACT, bool MX, int TT, int NW>
-__global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a) {
-    __shared__ unsigned long long masks[kRouteMaxExperts];
-    __shared__ unsigned long long slot_mask[kMlpMaxChoices];
-    __shared__ int slot_at[kMlpMaxChoices];                                 // expert << 11 | first row
-    __shared__ float sums[NW][TT][256];
+// A block: 16 M columns of y and one of the splits of all slots' pieces of K, of which each wave takes a contiguous
+// part. A wave multiplies a slot's rows of h, 16 TT in a pass, and adds the sums to its own y [token][columns] in LDS when
+// it leaves the slot. The waves' y are added in their order; with several splits the block that finishes last adds the
+// splits' in theirs.
+template <int ACT, bool MX, int M, int SC, int TT, int NW>
+__global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
+    constexpr int COLS = 16 * M;
+    extern __shared__ __align__(16) float ys[];      // [NW][T][COLS]
+    __shared__ uint16_t expert[kMlpMaxChoices], first[kMlpMaxChoices + 1];
+    __shared__ uint8_t token[kMlpMaxChoices];
+    __shared__ bool last;
+    const Scratch from = scratch_of(a, lay);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const int n0 = 16 * (int)blockIdx.x;
-    fill_masks(a, masks);
-    const int slots = each_slot(a, masks, [&](bool any, int e, unsigned long long m, int s, int row) {
-        if (any && wave == 0) slot_mask[s] = m, slot_at[s] = e << 11 | row;
-    });
-    __syncthreads();
+    const int n0 = COLS * (int)blockIdx.x, split = (int)blockIdx.y, splits = lay.splits;
     const int64_t ldh = padded(a.I);
-    const int chunks = (int)(ldh / 128);
-    const int r = n0 + (lane & 15), row = r < a.N ? r : a.N - 1;
-    f32x4 acc[TT];
-#pragma unroll
-    for (int i = 0; i < TT; ++i) acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto load = [&](int s, int c, Piece<MX>* p) {
-        Rows<ACT, MX> w;
-        w.init(a.w_out, a.s_out, slot_at[s] >> 11, a.N, a.I, row);
-        w.load(c, p);
-    };
-    int s = chunks > 0 ? wave / chunks : slots, c = chunks > 0 ? wave % chunks : 0;
-    Piece<MX> p;
-    if (s < slots) load(s, c, &p);
-    while (s < slots) {
-        int ns = s, nc = c + NW;
-        while (nc >= chunks) nc -= chunks, ++ns;
-        const unsigned long long m = slot_mask[s];
-        const int base = slot_at[s] & 2047;
-        u32x4 hv[TT][4];
-#pragma unroll
-        for (int i = 0; i < TT; ++i) {
-            const int t = 16 * i + (lane & 15);
-            const uint16_t* h = static_cast<const uint16_t*>(a.h) + (base + __popcll(m & ((1ull << t) - 1))) * ldh + 128 * (int64_t)c;
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                hv[i][q] = m >> t & 1 ? *reinterpret_cast<const u32x4*>(h + k_of<MX>(q)) : u32x4{0, 0, 0, 0};
-        }
-        Piece<MX> np = p;
-        if (ns < slots) load(ns, nc, &np);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const u32x4 w = operand<ACT, MX>(p, q);
-#pragma unroll
-            for (int i = 0; i < TT; ++i) acc[i] = mfma<ACT>(w, hv[i][q], acc[i]);
-        }
-        p = np, s = ns, c = nc;
+    const int chunks = (int)(ldh / 128), pieces = (chunks + SC - 1) / SC;
+    int slots = 0;
+    if (a.I > 0 && a.k > 0) {
+        const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
+        for (int i = threadIdx.x; i < most; i += blockDim.x) expert[i] = from.plan->expert[i], first[i + 1] = from.plan->first[i + 1];
+        for (int i = threadIdx.x; i < a.T * a.k; i += blockDim.x) token[i] = from.plan->token[i];
+        if (threadIdx.x == 0) first[0] = 0;
+        slots = __builtin_amdgcn_readfirstlane(from.plan->slots);
     }
-#pragma unroll
-    for (int i = 0; i < TT; ++i) *reinterpret_cast<f32x4*>(&sums[wave][i][4 * lane]) = acc[i];
+    for (int i = threadIdx.x; i < NW * a.T * COLS; i += blockDim.x) ys[i] = 0.0f;
     __syncthreads();
-    for (int i = wave; i < TT; i += NW) {
-        const int t = 16 * i + (lane & 15), col = n0 + 4 * (lane >> 4);
-        if (t >= a.T || col >= a.N) continue;
-        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+    const int items = slots * pieces, parts = NW * splits, part = split * NW + wave;
+    const int begin = (int)((int64_t)items * part / parts), end = (int)((int64_t)items * (part + 1) / parts);
+
+    // Item (slot and piece) and first token of the pass: what is loaded next, and what is multiplied next. A slot's items of
+    // this wave are first ... stop - 1, taken once per pass.
+    struct At {
+        int it, first, stop, s, from, base, n;
+    };
+    auto open = [&](At& t) {
+        t.first = t.it;
+        t.s = t.it / pieces;
+        t.stop = t.s * pieces + pieces < end ? t.s * pieces + pieces : end;
+        t.base = __builtin_amdgcn_readfirstlane((int)first[t.s]);
+        t.n = __builtin_amdgcn_readfirstlane((int)first[t.s + 1]) - t.base;
+        t.from = 0;
+    };
+    auto next = [&](At& t) {                         // true at the end of a pass
+        if (++t.it < t.stop) return false;
+        t.from += 16 * TT;
+        if (t.from < t.n) t.it = t.first;
+        else if (t.it < end) open(t);
+        return true;
+    };
+    At l{begin, 0, 0, 0, 0, 0, 0};
+    Rows<MX> rows[M];
+    Row16 h[TT];
+    auto point = [&]() {
+        const int e = __builtin_amdgcn_readfirstlane((int)expert[l.s]);
 #pragma unroll
-        for (int v = 0; v < NW; ++v) y += *reinterpret_cast<const f32x4*>(&sums[v][i][4 * lane]);
+        for (int i = 0; i < M; ++i) {
+            const int c = n0 + 16 * i + (lane & 15);
+            rows[i].init(a.w_out, a.s_out, e, a.N, a.I, c < a.N ? c : a.N - 1);
+        }
+#pragma unroll
+        for (int i = 0; i < TT; ++i) {               // lanes without a token read the last one's
+            const int at = l.from + 16 * i + (lane & 15);
+            h[i] = Row16{from.h + (l.base + (at < l.n ? at : l.n - 1)) * ldh, (int)ldh};
+        }
+    };
+    typedef Piece<ACT, MX, M, SC, TT> Ops;
+    auto load = [&](Ops& o) {
+        if (l.it >= end) return;
+        o.load(rows, h, l.it - l.s * pieces, chunks);
+        if (next(l) && l.it < end) point();
+    };
+    f32x4 acc[M][TT];
+#pragma unroll
+    for (int q = 0; q < M; ++q)
+#pragma unroll
+        for (int i = 0; i < TT; ++i) acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (begin < end) {
+        open(l);
+        At m = l;
+        point();
+        auto step = [&](Ops& o) {                    // false at the end
+            o.multiply(a.I, (int)ldh, m.it - m.s * pieces, acc);
+            const At t = m;
+            const bool left = next(m);
+            load(o);
+            if (left) {
+#pragma unroll
+                for (int i = 0; i < TT; ++i) {
+                    const int at = t.from + 16 * i + (lane & 15);
+                    float* y = ys + (wave * a.T + token[t.base + (at < t.n ? at : t.n - 1)]) * COLS + 4 * (lane >> 4);
+#pragma unroll
+                    for (int q = 0; q < M; ++q) {
+                        if (at < t.n) *reinterpret_cast<f32x4*>(y + 16 * q) += acc[q][i];
+                        acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                }
+            }
+            return m.it < end;
+        };
+        Ops o0, o1;
+        load(o0);
+        load(o1);
+        while (step(o0) && step(o1)) {}
+    }
+    __syncthreads();
+    const int quads = 4 * M, width = lay.width;
+    if (splits > 1) {
+        for (int i = threadIdx.x; i < quads * a.T; i += blockDim.x) {
+            const int t = i / quads, c = 4 * (i % quads);
+            f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int v = 0; v < NW; ++v) y += *reinterpret_cast<const f32x4*>(ys + (v * a.T + t) * COLS + c);
+            *reinterpret_cast<f32x4*>(from.part + ((int64_t)split * a.T + t) * width + n0 + c) = y;
+        }
+        // the splits' blocks may run on other XCDs: what this block wrote has reached its L2 (vmcnt(0)) and is released
+        // before it counts itself done, and what the others wrote is acquired with the count
+        __builtin_amdgcn_s_waitcnt(0x0F70);
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = __hip_atomic_fetch_add(&from.done[blockIdx.x], 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == splits - 1;
+        __syncthreads();
+        if (!last) return;
+    }
+    for (int i = threadIdx.x; i < quads * a.T; i += blockDim.x) {
+        const int t = i / quads, c = 4 * (i % quads), col = n0 + c;
+        if (col >= a.N) continue;
+        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (splits > 1) {
+            for (int v0 = 0; v0 < splits; v0 += 8) {  // eight loads in flight; added in order
+                f32x4 p[8];
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    p[v] = *reinterpret_cast<const f32x4*>(from.part + ((int64_t)(v0 + v < splits ? v0 + v : v0) * a.T + t) * width + col);
+#pragma unroll
+                for (int v = 0; v < 8; ++v)
+                    if (v0 + v < splits) y += p[v];
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < NW; ++v) y += *reinterpret_cast<const f32x4*>(ys + (v * a.T + t) * COLS + c);
+        }
         if (a.b_out)
             for (int j = 0; j < a.k; ++j) {
                 const int64_t e = choice(a, t * a.k + j);
@@ -348,26 +589,76 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a) {
     }
 }
 
+// Launch shapes, measured with weights that come from HBM (graph of six calls, us per call).
+//
+// First product: MXFP4 weights take two pairs of tiles and 256 columns of K at a time (64 tokens, 8 of 128 experts of 2048 x
+// 1408: 188 with it, one pair 232), tokens 16 to a pass (two tiles of tokens at once: 209). 16-bit weights take one pair
+// and 128 columns, 256 bytes of each row; from 17 tokens on 32 to a pass, however few an expert has (same layer in BF16: 411,
+// 16 to a pass 436; 2 of 8 experts of 4096 x 2048: 113 and 133). Blocks of four waves, 16 waves to a CU, or, where few units come
+// to a block, 8 (8 tokens, 4 of 32 of 4096 x 2048 in MXFP4: 80, with 16 93; the 64 tokens above 202 with 8); for 16-bit weights and
+// up to 16 tokens from 1024 units on one block of eight waves a CU (16 tokens, 4 of 32 of 4096 x 2048: 229 for 239; 4 tokens,
+// 8 of 128 of 2048 x 768: 66 for 71).
+//
+// Second product: blocks of eight waves. Few pieces go whole to the blocks of 16 columns (one token, 8 of 128 of 2048 x 1408 in
+// MXFP4: 25.8, with 32 columns and four splits 27.9; 4 of 32 in BF16: 28.5, with two splits 30.0). More are split until
+// there are 256 blocks, in MXFP4 of 32 columns, which halves the loads of h (the 64 tokens above: 188, 16 columns in two
+// splits 213; 4 tokens, 8 of 128 of 2048 x 768 in BF16: 66, unsplit 73).
+template <bool MX> constexpr int kInPairs = MX ? 2 : 1;
+template <bool MX> constexpr int kPieceChunks = MX ? 2 : 1;
+
+struct Shape {
+    Layout lay;
+    int outs;                   // tiles of 16 columns in a block of the second product
+    int64_t slots, units;       // most there can be
+};
+Shape shape_of(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N, bool mx) {
+    Shape s;
+    s.slots = T * k < E ? T * k : E;
+    s.units = s.slots * (padded(I) / (16 * (mx ? kInPairs<true> : kInPairs<false>)));
+    const int64_t wide = 128 * (mx ? kPieceChunks<true> : kPieceChunks<false>);
+    const bool many = s.slots * ((I + wide - 1) / wide) >= (mx ? 96 : 128);
+    s.outs = mx && many ? 2 : 1;
+    s.lay.tiles = (int)((N + 16 * s.outs - 1) / (16 * s.outs));
+    s.lay.width = s.lay.tiles * 16 * s.outs;
+    s.lay.splits = many && s.lay.tiles <= 128 ? (s.lay.tiles > 32 ? 256 / s.lay.tiles : 8) : 1;
+    return s;
+}
+
+template <int ACT, bool MX, int TT, int NW>
+hipError_t in_go(const MlpArgs& a, const Shape& s, int waves, hipStream_t stream) {
+    const int64_t room = (int64_t)device_cus() * waves / NW;
+    hipLaunchKernelGGL((mlp_in<ACT, MX, kInPairs<MX>, kPieceChunks<MX>, TT, NW>), dim3((unsigned)(s.units < room ? s.units : room)),
+                       dim3(64 * NW), 0, stream, a, s.lay);
+    return hipGetLastError();
+}
+template <int ACT, bool MX, int M, int TT>
+hipError_t out_go(const MlpArgs& a, const Layout& lay, hipStream_t stream) {
+    constexpr int NW = 8;
+    hipLaunchKernelGGL((mlp_out<ACT, MX, M, kPieceChunks<MX>, TT, NW>), dim3((unsigned)lay.tiles, (unsigned)lay.splits), dim3(64 * NW),
+                       (size_t)NW * a.T * 64 * M, stream, a, lay);
+    return hipGetLastError();
+}
 template <int ACT, bool MX>
 hipError_t mlp_go(const MlpArgs& a, hipStream_t stream) {
-    const int64_t slots = (int64_t)a.T * a.k < a.E ? (int64_t)a.T * a.k : a.E;
-    const int64_t in_blocks = slots * (padded(a.I) / 16), out_blocks = ((int64_t)a.N + 15) / 16;
-    if (in_blocks * 256 > kMaxThreads || out_blocks * 512 > kMaxThreads) return hipErrorInvalidValue;
-    if (in_blocks > 0) {
-        if (a.T <= 16) hipLaunchKernelGGL((mlp_in<ACT, MX, 1, 4>), dim3((unsigned)in_blocks), dim3(256), 0, stream, a);
-        else if (a.T <= 32) hipLaunchKernelGGL((mlp_in<ACT, MX, 2, 4>), dim3((unsigned)in_blocks), dim3(256), 0, stream, a);
-        else hipLaunchKernelGGL((mlp_in<ACT, MX, 4, 4>), dim3((unsigned)in_blocks), dim3(256), 0, stream, a);
-        if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const Shape s = shape_of(a.T, a.k, a.E, a.I, a.N, MX);
+    if (s.units > 0) {
+        hipError_t e;
+        if constexpr (MX) e = in_go<ACT, true, 1, 4>(a, s, s.units >= 4096 ? 16 : 8, stream);
+        else if (a.T > 16) e = in_go<ACT, false, 2, 4>(a, s, 16, stream);
+        else if (s.units >= 1024) e = in_go<ACT, false, 1, 8>(a, s, 8, stream);
+        else e = in_go<ACT, false, 1, 4>(a, s, 16, stream);
+        if (e != hipSuccess) return e;
     }
-    if (a.T <= 16) hipLaunchKernelGGL((mlp_out<ACT, MX, 1, 8>), dim3((unsigned)out_blocks), dim3(512), 0, stream, a);
-    else if (a.T <= 32) hipLaunchKernelGGL((mlp_out<ACT, MX, 2, 8>), dim3((unsigned)out_blocks), dim3(512), 0, stream, a);
-    else hipLaunchKernelGGL((mlp_out<ACT, MX, 4, 8>), dim3((unsigned)out_blocks), dim3(512), 0, stream, a);
-    return hipGetLastError();
+    if constexpr (MX) return s.outs == 2 ? out_go<ACT, true, 2, 1>(a, s.lay, stream) : out_go<ACT, true, 1, 1>(a, s.lay, stream);
+    else return a.T > 16 ? out_go<ACT, false, 1, 2>(a, s.lay, stream) : out_go<ACT, false, 1, 1>(a, s.lay, stream);
 }
 
 }  // namespace
 
-size_t mlp_scratch(int64_t T, int64_t k, int64_t I) { return (size_t)(T * k * padded(I) * 2); }
+size_t mlp_scratch(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N, bool mx) {
+    if (T * k == 0 || I == 0) return 0;
+    return (size_t)(h_at(shape_of(T, k, E, I, N, mx).lay, T) + T * k * padded(I) * 2);
+}
 
 hipError_t launch_mlp(const MlpArgs& a, hipStream_t stream) {
     if (a.T <= 0 || a.N <= 0) return hipSuccess;

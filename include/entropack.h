@@ -549,8 +549,8 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
  * 4-byte aligned, EP_EINVAL); MXFP4 weights meet the activations in act's type (exact in EP_BF16 up to scale bytes of 251;
  * in EP_F16 from 2^-14 to 65504). in_bias: [E][2 I], out_bias: [E][N], bf16 or NULL.
  * fp32 sums; w h is rounded once to act's type, y once. The same bits on every call.
- *   scratch: ep_mlp_forward_experts_scratch(T, k, I) bytes of device memory, 16-byte aligned (NULL when that is 0), read and
- * written by this call's kernels only. T in 0 ... 64, T k <= 1024, E in 1 ... 1024, H, I and N <= 2^20 (EP_ERANGE): for more
+ *   scratch: ep_mlp_forward_experts_scratch bytes of device memory, 16-byte aligned (NULL when that is 0), read and written
+ * by this call's kernels only. T in 0 ... 64, T k <= 1024, E in 1 ... 1024, H, I and N <= 2^20 (EP_ERANGE): for more
  * tokens sort them (ep_sort_tokens) and use a product per expert. Asynchronous on hip_stream; allocates nothing. */
 ep_status ep_mlp_forward_experts(const void* dev_x, ep_dtype act, int64_t T, int64_t H, int64_t ldx, const void* dev_ids,
                                  int id_bytes, int k, int E, const float* dev_w, const void* dev_w_in,
@@ -558,10 +558,10 @@ ep_status ep_mlp_forward_experts(const void* dev_x, ep_dtype act, int64_t T, int
                                  const uint8_t* dev_out_scales, const void* dev_out_bias, int64_t I, int64_t N, void* dev_scratch,
                                  void* dev_y, void* hip_stream);
 
-/* Bytes of device scratch ep_mlp_forward_experts needs in *bytes. Source: "EntroPack PyTorch Guide: Lossless Weights,
+/* Bytes of device scratch ep_mlp_forward_experts needs in *bytes; mxfp4: whether the weights have scales. Source: "EntroPack PyTorch Guide: Lossless Weights,
  * Bitrates and Memory Checks", section "Measure memory with clear boundaries" (temporary buffers of a call are part
  * of its memory). */
-ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int64_t I, size_t* bytes);
+ep_status ep_mlp_forward_experts_scratch(int64_t T, int k, int E, int64_t I, int64_t N, int mxfp4, size_t* bytes);
 
 /* Source: "EntroPack PyTorch Guide: Lossless Weights, Bitrates and Memory Checks", section "Test
  * saved artifacts and reloads before deployment" (a failed step must stop with a clear error);

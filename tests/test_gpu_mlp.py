@@ -71,7 +71,8 @@ class Layer:
 
 CASES = [(1, 1, 1, 128, 16, 16), (1, 4, 8, 256, 128, 256), (2, 2, 4, 100, 33, 70), (7, 2, 8, 333, 150, 129), (16, 4, 16, 512, 96, 320),
          (17, 3, 5, 130, 257, 64), (33, 2, 70, 64, 40, 33), (64, 8, 16, 256, 128, 128), (64, 4, 4, 384, 130, 96), (5, 1, 3, 1, 1, 1),
-         (3, 2, 4, 2048, 640, 200), (40, 1, 2, 1025, 64, 15), (64, 16, 200, 32, 16, 24), (9, 2, 1024, 16, 8, 8)]
+         (3, 2, 4, 2048, 640, 200), (40, 1, 2, 1025, 64, 15), (64, 16, 200, 32, 16, 24), (9, 2, 1024, 16, 8, 8),
+         (64, 8, 128, 256, 256, 512), (48, 4, 48, 300, 700, 130), (16, 8, 128, 64, 128, 64), (16, 8, 128, 64, 1024, 16), (2, 1, 4, 4104, 24, 40)]
 
 
 @pytest.mark.parametrize("mxfp4", [False, True])

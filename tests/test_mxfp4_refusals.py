@@ -137,9 +137,11 @@ def test_expert_layer():
         assert call(**c) == ERANGE, c
     assert call(T=0, x=None, ids=None, y=None, scr=None) == 0 and call(N=0, y=None) == 0
     s = ep.lib().ep_mlp_forward_experts_scratch
-    assert s(4, 2, 32, None) == EINVAL and s(65, 1, 32, C.byref(n)) == ERANGE and s(-1, 1, 32, C.byref(n)) == EINVAL
-    assert s(4, 2, 130, C.byref(n)) == 0 and n.value == 8 * 256 * 2
-    assert s(0, 2, 130, C.byref(n)) == 0 and n.value == 0
+    assert s(4, 2, 3, 32, 16, 0, None) == EINVAL and s(65, 1, 3, 32, 16, 0, C.byref(n)) == ERANGE and s(-1, 1, 3, 32, 16, 0, C.byref(n)) == EINVAL
+    assert s(4, 2, 3, 2 ** 20 + 1, 16, 0, C.byref(n)) == ERANGE and s(4, 2, 0, 32, 16, 1, C.byref(n)) == ERANGE
+    assert s(4, 2, 3, 130, 16, 1, C.byref(n)) == 0 and n.value >= 8 * 256 * 2
+    for T, k, I in ((0, 2, 130), (4, 0, 130), (4, 2, 0)):
+        assert s(T, k, 3, I, 16, 0, C.byref(n)) == 0 and n.value == 0
 
 
 def test_expert_layer_tensors_on_the_host():

@@ -636,21 +636,25 @@ def quantize_rows_mxfp4(x, stream=None):
     waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: quantize_rows_mxfp4(x), x)
-    dims = x.dim()
+    torch = _torch()
+    dims, dtype, dev = x.dim(), x.dtype, torch.cuda.current_device() if x.is_cuda else None
     if dims == 2:
-        M, K = x.shape
+        M, K = rows, ldx = x.shape
+        if not (dtype in _float_types() and x.get_device() == dev and x.is_contiguous()):
+            rows, _, ldx = _need_rows(x, "x", _float_types())
     elif dims == 3:
-        _need(x, "x", x.dtype)
         E, M, K = x.shape
-        x = x.reshape(E * M, K)
+        rows, ldx = E * M, K
+        if dtype not in _float_types():
+            raise ValueError(f"x must be one of {', '.join(map(str, _float_types()))}, got {dtype}")
+        _need(x, "x", dtype)
     else:
         raise ValueError(f"x must be [M, K] or [E, M, K], got shape {tuple(x.shape)}")
-    rows, _, ldx = _need_rows(x, "x", _float_types())
-    u8, chunks = _torch().uint8, (K + 127) // 128
+    u8, chunks = torch.uint8, (K + 127) // 128
     q = x.new_empty((M, 64 * chunks) if dims == 2 else (E, M, 64 * chunks), dtype=u8)
     s = x.new_empty((chunks, M, 4) if dims == 2 else (E, chunks, M, 4), dtype=u8)
-    _check(lib().ep_quantize_rows_mxfp4(x.data_ptr(), _dtype_code(x.dtype), rows, M, K, ldx, q.data_ptr(), s.data_ptr(),
-                                        _current_raw()), "ep_quantize_rows_mxfp4")
+    _check(lib().ep_quantize_rows_mxfp4(x.data_ptr(), _dtype_code(dtype), rows, M, K, ldx, q.data_ptr(), s.data_ptr(),
+                                        torch._C._cuda_getCurrentRawStream(dev)), "ep_quantize_rows_mxfp4")
     return q, s
 
 
@@ -684,17 +688,20 @@ def dequantize_rows_mxfp4(codes, scales, out_dtype=None, columns=None, stream=No
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in _float_types():
         raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
-    if codes.dim() not in (2, 3):
-        raise ValueError(f"codes must be [M, Kp / 2] or [E, M, Kp / 2], got shape {tuple(codes.shape)}")
-    Kp = _mx_shapes(codes, scales, "codes", "scales", codes.dim(), torch.cuda.current_device() if codes.is_cuda else None)
+    shape, dims = codes.shape, codes.dim()
+    if dims not in (2, 3):
+        raise ValueError(f"codes must be [M, Kp / 2] or [E, M, Kp / 2], got shape {tuple(shape)}")
+    dev = torch.cuda.current_device() if codes.is_cuda else None
+    Kp = _mx_shapes(codes, scales, "codes", "scales", dims, dev)
     K = Kp if columns is None else columns
     if not 0 <= K <= Kp:
         raise ValueError(f"columns must be 0 ... {Kp}, got {columns}")
-    M = codes.shape[-2]
-    y = codes.new_empty((*codes.shape[:-1], K), dtype=out_dtype)
+    M = shape[-2]
+    y = codes.new_empty((M, K) if dims == 2 else (shape[0], M, K), dtype=out_dtype)
     codes, scales = _mx_aligned(codes, 4), _mx_aligned(scales, 4)
-    _check(lib().ep_dequantize_rows_mxfp4(_ptr(codes), _ptr(scales), M * (codes.shape[0] if codes.dim() == 3 else 1), M, Kp, K,
-                                          _dtype_code(out_dtype), _ptr(y), _current_raw()), "ep_dequantize_rows_mxfp4")
+    _check(lib().ep_dequantize_rows_mxfp4(codes.data_ptr(), scales.data_ptr(), M if dims == 2 else M * shape[0], M, Kp, K,
+                                          _dtype_code(out_dtype), y.data_ptr(), torch._C._cuda_getCurrentRawStream(dev)),
+           "ep_dequantize_rows_mxfp4")
     return y
 
 

@@ -57,17 +57,21 @@ struct Routing {
 };
 struct RoutingWork {
     unsigned long long masks[kRouteMaxExperts];     // the tokens of an expert
+    float weight[kMlpMaxChoices];                   // of a choice
     int16_t id[kMlpMaxChoices];                     // of a choice, -1 where it is dropped
     uint16_t slot[kRouteMaxExperts];                // of an expert with tokens
 };
 __device__ __forceinline__ void route(const MlpArgs& a, Routing& r, RoutingWork& w) {
     const int n = a.T * a.k;
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) w.masks[e] = 0;
+    int64_t e = -1;
+    if (threadIdx.x < n) e = choice(a, threadIdx.x);  // in flight while the masks are cleared
+    for (int i = threadIdx.x; i < a.E; i += blockDim.x) w.masks[i] = 0;
     __syncthreads();
     for (int c = threadIdx.x; c < n; c += blockDim.x) {
-        const int64_t e = choice(a, c);
+        if (c >= (int)blockDim.x) e = choice(a, c);
         const bool in = e >= 0 && e < a.E;
         w.id[c] = in ? (int16_t)e : (int16_t)-1;
+        w.weight[c] = a.w ? a.w[c] : 1.0f;
         if (in) atomicOr(&w.masks[e], 1ull << (c / a.k));
     }
     __syncthreads();
@@ -102,14 +106,20 @@ __device__ __forceinline__ void route(const MlpArgs& a, Routing& r, RoutingWork&
         bool again = false;                          // the token has named the expert before
         for (int o = t * a.k; o < c; ++o) again |= w.id[o] == e;
         if (again) continue;
-        float sum = a.w ? a.w[c] : 1.0f;
+        float sum = w.weight[c];
         for (int o = c + 1; o < (t + 1) * a.k; ++o)
-            if (w.id[o] == e) sum += a.w ? a.w[o] : 1.0f;
+            if (w.id[o] == e) sum += w.weight[o];
         const int row = r.first[w.slot[e]] + __popcll(w.masks[e] & ((1ull << t) - 1));
         r.weight[row] = sum;
         r.token[row] = (uint8_t)t;
     }
     __syncthreads();
+}
+
+// The start of part i of n things in `parts` parts whose sizes differ by one at most.
+__device__ __forceinline__ int part_start(int n, int parts, int i) {
+    const int each = n / parts, more = n - each * parts;
+    return i * each + (i < more ? i : more);
 }
 
 // What the first kernel leaves for the second, before h in the scratch.
@@ -327,7 +337,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
         if (threadIdx.x == 0) to.plan->slots = r.slots;
     }
     const int units = r.slots * tiles;
-    const int u0 = (int)((int64_t)units * blockIdx.x / gridDim.x), u1 = (int)((int64_t)units * (blockIdx.x + 1) / gridDim.x);
+    const int u0 = part_start(units, (int)gridDim.x, (int)blockIdx.x), u1 = part_start(units, (int)gridDim.x, (int)blockIdx.x + 1);
     if (u0 >= u1) return;
 
     // Unit, first token of the pass, piece: what is loaded next, and what is multiplied next, in the same order. All waves
@@ -461,7 +471,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     for (int i = threadIdx.x; i < NW * a.T * COLS; i += blockDim.x) ys[i] = 0.0f;
     __syncthreads();
     const int items = slots * pieces, parts = NW * splits, part = split * NW + wave;
-    const int begin = (int)((int64_t)items * part / parts), end = (int)((int64_t)items * (part + 1) / parts);
+    const int begin = part_start(items, parts, part), end = part_start(items, parts, part + 1);
 
     // Item (slot and piece) and first token of the pass: what is loaded next, and what is multiplied next. A slot's items of
     // this wave are first ... stop - 1, taken once per pass.
@@ -599,7 +609,8 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
 // up to 16 tokens from 1024 units on one block of eight waves a CU (16 tokens, 4 of 32 of 4096 x 2048: 229 for 239; 4 tokens,
 // 8 of 128 of 2048 x 768: 66 for 71).
 //
-// Second product: blocks of eight waves. Few pieces go whole to the blocks of 16 columns (one token, 8 of 128 of 2048 x 1408 in
+// Second product: blocks of 16 waves for up to 16 tokens and 16 columns (16 tokens, 4 of 32 of 4096 x 2048 in BF16: 228, with
+// eight 242; one token, 4 of 32 of 2048 x 1408: 28.6 for 29.7), else of eight. Few pieces go whole to the blocks of 16 columns (one token, 8 of 128 of 2048 x 1408 in
 // MXFP4: 25.8, with 32 columns and four splits 27.9; 4 of 32 in BF16: 28.5, with two splits 30.0). More are split until
 // there are 256 blocks, in MXFP4 of 32 columns, which halves the loads of h (the 64 tokens above: 188, 16 columns in two
 // splits 213; 4 tokens, 8 of 128 of 2048 x 768 in BF16: 66, unsplit 73).
@@ -631,9 +642,8 @@ hipError_t in_go(const MlpArgs& a, const Shape& s, int waves, hipStream_t stream
                        dim3(64 * NW), 0, stream, a, s.lay);
     return hipGetLastError();
 }
-template <int ACT, bool MX, int M, int TT>
+template <int ACT, bool MX, int M, int TT, int NW>
 hipError_t out_go(const MlpArgs& a, const Layout& lay, hipStream_t stream) {
-    constexpr int NW = 8;
     hipLaunchKernelGGL((mlp_out<ACT, MX, M, kPieceChunks<MX>, TT, NW>), dim3((unsigned)lay.tiles, (unsigned)lay.splits), dim3(64 * NW),
                        (size_t)NW * a.T * 64 * M, stream, a, lay);
     return hipGetLastError();
@@ -649,8 +659,8 @@ hipError_t mlp_go(const MlpArgs& a, hipStream_t stream) {
         else e = in_go<ACT, false, 1, 4>(a, s, 16, stream);
         if (e != hipSuccess) return e;
     }
-    if constexpr (MX) return s.outs == 2 ? out_go<ACT, true, 2, 1>(a, s.lay, stream) : out_go<ACT, true, 1, 1>(a, s.lay, stream);
-    else return a.T > 16 ? out_go<ACT, false, 1, 2>(a, s.lay, stream) : out_go<ACT, false, 1, 1>(a, s.lay, stream);
+    if constexpr (MX) return s.outs == 2 ? out_go<ACT, true, 2, 1, 8>(a, s.lay, stream) : out_go<ACT, true, 1, 1, 16>(a, s.lay, stream);
+    else return a.T > 16 ? out_go<ACT, false, 1, 2, 8>(a, s.lay, stream) : out_go<ACT, false, 1, 1, 16>(a, s.lay, stream);
 }
 
 }  // namespace

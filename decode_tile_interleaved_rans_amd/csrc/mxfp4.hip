@@ -48,6 +48,18 @@ __device__ __forceinline__ float elem_value(uint32_t bits) {
 template <int SRC>
 struct Eight {
     typename Elem<SRC>::type e[8];
+    typedef uint32_t Words __attribute__((ext_vector_type(2 * sizeof(typename Elem<SRC>::type)), aligned(sizeof(typename Elem<SRC>::type))));
+    // rows of any alignment of the element, past the caches: 4096 x 10240 BF16 quantized in 20 us for 23.5 with ordinary loads
+    // and stores, the values of the codes written in 17 for 25
+    __device__ __forceinline__ void load(const void* p) {
+        const Words w = __builtin_nontemporal_load(static_cast<const Words*>(p));
+        __builtin_memcpy(e, &w, sizeof e);
+    }
+    __device__ __forceinline__ void store(void* p) const {
+        Words w;
+        __builtin_memcpy(&w, e, sizeof e);
+        __builtin_nontemporal_store(w, static_cast<Words*>(p));
+    }
 };
 
 template <int CTRL>
@@ -81,7 +93,7 @@ __global__ __launch_bounds__(256) void quantize_rows_mx(const void* Xv, int64_t 
             const int64_t m = at.r0 + 4 * j + g;
             const T* x = static_cast<const T*>(Xv) + (at.e * M + m) * ldx + k;
             if (m < M && left == 8) {
-                __builtin_memcpy(&v[j], x, sizeof v[j]);
+                v[j].load(x);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) v[j].e[i] = m < M && i < left ? x[i] : 0;
@@ -112,7 +124,7 @@ __global__ __launch_bounds__(256) void quantize_rows_mx(const void* Xv, int64_t 
             q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[4], f[5], unit, 2);
             q = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(q, f[6], f[7], unit, 3);
             q = bad ? 0u : q;
-            if (m < M) __builtin_memcpy(Q + (at.e * M + m) * (chunks * 64) + k / 2, &q, 4);
+            if (m < M) __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(Q + (at.e * M + m) * (chunks * 64) + k / 2));
             uint32_t s = b8 << (8 * (p >> 2));                              // the row's four scales, in all its 16 lanes
             s |= dpp<0x124>(s);
             s |= dpp<0x128>(s);
@@ -175,7 +187,7 @@ __global__ __launch_bounds__(256) void dequantize_rows_mx(const uint8_t* Q, cons
             eight_values<DST>(q[j], __uint_as_float((s[j] >> (8 * (p >> 2)) & 255u) << 23), &v);
             T* y = static_cast<T*>(Yv) + (at.e * M + m) * K + k;
             if (K - k >= 8) {
-                __builtin_memcpy(y, &v, sizeof v);
+                v.store(y);
             } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i)

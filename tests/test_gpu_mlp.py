@@ -1,4 +1,6 @@
 """The expert layer for few tokens on the GPU, against its formula in 64 bits."""
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -191,6 +193,50 @@ def test_other_stream_and_threads():
     got = [ep.mlp_forward_experts(*a, stream=side[i % 3]) for i in range(12)]
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in got)
+
+    def work(i):
+        with torch.cuda.stream(side[i]):
+            return [ep.mlp_forward_experts(*a) for _ in range(20)]
+
+    with ThreadPoolExecutor(3) as pool:
+        done = list(pool.map(work, range(3)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for ys in done for y in ys)
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
+def test_weights_past_32_bits(mxfp4):
+    """The last of the experts lies 2^32 elements (16 bits each, or bytes of codes) behind the first."""
+    H, I, N = 32768, 2048, 64
+    E = 65 if mxfp4 else 33
+    l = Layer(2, 1, 1, H, I, N, mxfp4=mxfp4, ids=torch.zeros((2, 1), dtype=torch.int64))
+    a = l.args()
+    for i in range(3, 7):
+        if a[i] is not None:
+            room = torch.zeros((E, *a[i].shape[1:]), dtype=a[i].dtype, device="cuda")
+            room[E - 1] = a[i][0]
+            a[i] = room
+    assert a[3][:E - 1].numel() == 2 ** 32
+    a[1] += E - 1
+    l.check(ep.mlp_forward_experts(*a))
+
+
+def test_two_graphs_in_turn():
+    """Two graphs of the layer that share a memory pool, replayed in turn, keep to their own inputs."""
+    layers = [Layer(64, 4, 16, 256, 1024, 64, mxfp4=True, seed=s) for s in (1, 2)]
+    args = [l.args() for l in layers]
+    want = [ep.mlp_forward_experts(*a) for a in args]
+    torch.cuda.synchronize()
+    graphs, out, pool = [], [], torch.cuda.graph_pool_handle()
+    for a in args:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], pool=pool):
+            out.append(ep.mlp_forward_experts(*a))
+    for i in (0, 1, 1, 0, 0, 1):
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out[i], want[i])
+        assert torch.equal(ep.mlp_forward_experts(*args[1 - i]), want[1 - i])
 
 
 @pytest.mark.parametrize("mxfp4", [False, True])

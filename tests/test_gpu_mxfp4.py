@@ -1,5 +1,7 @@
 """MXFP4 on the GPU: the quantizer bit for bit against the format's definition, its inverse, and the products of two
 MXFP4 matrices, with one weight and with one per expert, against sums in 64 bits."""
+from concurrent.futures import ThreadPoolExecutor
+
 import pytest
 import torch
 
@@ -323,3 +325,71 @@ def test_refusals_of_tensors():
         ep.dequantize_rows_mxfp4(*ok[:2], columns=129)
     with pytest.raises(ValueError):
         ep.dequantize_rows_mxfp4(*ok[:2], torch.int8)
+
+
+def test_threads():
+    """Calls from several threads at once, each on a stream of its own."""
+    g = gen(17)
+    sets = []
+    for i in range(4):
+        x, w = torch.randn((70 + i, 640), generator=g).cuda().to(torch.bfloat16), torch.randn((130, 640), generator=g).cuda()
+        sets.append((x, *ep.quantize_rows_mxfp4(w)))
+    layer = lambda i: ep.gemm_mxfp4(*ep.quantize_rows_mxfp4(sets[i][0]), *sets[i][1:])
+    want = [layer(i) for i in range(4)]
+    side = [torch.cuda.Stream() for _ in range(4)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        with torch.cuda.stream(side[i]):
+            return [layer(i) for _ in range(20)]
+
+    with ThreadPoolExecutor(4) as pool:
+        done = list(pool.map(work, range(4)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(4) for y in done[i])
+
+
+# ---------------------------------------------------------------------------- offsets past 32 bits
+def repeats(y, rows):
+    """All rows of y (its first dimension) repeat the first `rows`, bit for bit."""
+    v = y.view(torch.int16) if y.dtype == torch.bfloat16 else y
+    return all(torch.equal(v[i:i + rows], v[:rows]) for i in range(rows, y.shape[0], rows))
+
+
+def test_many_rows():
+    """9.2e9 elements, 4.6e9 bytes of codes: rows that repeat give codes, values and products that repeat."""
+    base = torch.randn((1000, 65536), generator=gen(18)).to(torch.bfloat16).cuda()
+    x = base.repeat(140, 1)
+    q, s = ep.quantize_rows_mxfp4(x)
+    assert q.numel() > 2 ** 32 and repeats(q, 1000) and repeats(s.transpose(0, 1), 1000)
+    q0, s0 = ep.quantize_rows_mxfp4(base)
+    assert torch.equal(q[:1000], q0) and torch.equal(s[:, :1000], s0)
+    same_codes(base[:50], *ep.quantize_rows_mxfp4(base[:50]))
+    del x
+    v = ep.dequantize_rows_mxfp4(q, s)
+    assert repeats(v, 1000) and torch.equal(v[:1000], ep.dequantize_rows_mxfp4(q0, s0))
+    del v
+    wq, ws = mx.random_matrix(gen(19), 64, 65536)
+    y = ep.gemm_mxfp4(q, s, wq.cuda(), ws.cuda())
+    assert repeats(y, 1000)
+    mx.check_product(y[:50], mx.values(q[:50], s[:, :50]), mx.values(wq, ws))
+
+
+def test_many_outputs():
+    """4.9e9 outputs."""
+    (xq, xs), (wq, ws) = mx.random_matrix(gen(20), 1000, 128), mx.random_matrix(gen(21), 16384, 128)
+    y = ep.gemm_mxfp4(xq.cuda().repeat(300, 1), xs.cuda().repeat(1, 300, 1), wq.cuda(), ws.cuda())
+    assert y.numel() > 2 ** 32 and repeats(y, 1000)
+    mx.check_product(y[:200, -300:], mx.values(xq[:200], xs[:, :200]), mx.values(wq[-300:], ws[:, -300:]))
+
+
+def test_experts_past_32_bits():
+    """5.4e9 bytes of the experts' codes."""
+    E, N, K = 20, 8192, 65536
+    (xq, xs), (wq, ws) = mx.random_matrix(gen(22), 5, K), mx.random_matrix(gen(23), N, K)
+    allq, alls = (torch.zeros((E, *t.shape), dtype=torch.uint8, device="cuda") for t in (wq, ws))
+    allq[E - 1], alls[E - 1] = wq.cuda(), ws.cuda()
+    assert allq[:E - 1].numel() > 2 ** 32
+    offsets = torch.tensor([0] * E + [5], dtype=torch.int32).cuda()
+    y = ep.gemm_mxfp4_experts(xq.cuda(), xs.cuda(), allq, alls, offsets)
+    mx.check_product(y[:, -40:], mx.values(xq, xs), mx.values(wq[-40:], ws[:, -40:]))

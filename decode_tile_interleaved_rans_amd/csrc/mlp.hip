@@ -7,11 +7,10 @@
 // rounding to the activations' type (the same relative error as rounding h itself), so that the second product's sums
 // over the experts need no further factors.
 //
-// What bounds it: 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16 read 1.4 GB in 229 us, 6.1 TB/s (a read of 400 MB in
+// What bounds it: 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16 read 1.4 GB in 214-226 us, over 6 TB/s (a read of 400 MB in
 // this pattern alone reaches 6.0). In MXFP4 the tokens' loads count as well: 64 tokens on 8 of 128 experts of 2048 x 1408
-// take 188 us for 0.58 GB, 110 of them the first product, which without the tokens' loads and products would take 95. Small
-// layers are bound by latency: each kernel takes 6 to 8 us beside the transfer of its weights (one token on 4 of 32 experts
-// of 2048 x 1408 in BF16 28 us for 69 MB).
+// take 160-172 us (boxes differ) for 0.58 GB. Small layers are bound by latency: each kernel takes 6 to 8 us beside the transfer of
+// its weights (one token on 4 of 32 experts of 2048 x 1408 in BF16 27 us for 69 MB).
 //
 // Operand lane layout (v_mfma_f32_16x16x32, checked on the device): lane l supplies eight elements of A row l % 16 and
 // of B column l % 16, K group l / 16, and receives C[4 (l / 16) + i][l % 16], i < 4. A and B take the same K positions per
@@ -148,7 +147,7 @@ __device__ __forceinline__ int k_of(int s) {
 }
 
 // One row of K 16-bit elements per lane, at any alignment of the element. load() reads what the lane needs of chunk c without
-// a branch, so that the loads of the next piece stay in flight behind the current products: a lane whose eight elements
+// a branch, so that the loads of the next chunk stay in flight behind the current products: a lane whose eight elements
 // reach past the row's end reads its last eight. fix() puts those right where they are used: zeros past the end.
 struct Row16 {
     const uint16_t* p;
@@ -273,52 +272,43 @@ __device__ __forceinline__ Scratch scratch_of(const MlpArgs& a, const Layout& l)
                    reinterpret_cast<uint16_t*>(p + h_at(l, a.T))};
 }
 
-// The operands of a piece, SC chunks of M weight tiles of 16 rows and of 16 TT tokens. A wave has two sets of them and
-// fills one while it multiplies the other.
-template <int ACT, bool MX, int M, int SC, int TT>
+// The operands of a chunk of K: M weight tiles of 16 rows and 16 TT tokens. A wave has two sets of them and fills one
+// while it multiplies the other.
+template <int ACT, bool MX, int M, int TT>
 struct Piece {
-    Chunk<MX> w[M][SC];
-    u32x4 x[TT][SC][4];
-    // piece p of rows of `chunks` chunks; a chunk past the last one reads that again, and its tokens count as zeros
-    __device__ __forceinline__ void load(const Rows<MX> (&rows)[M], const Row16 (&xs)[TT], int p, int chunks) {
+    Chunk<MX> w[M];
+    u32x4 x[TT][4];
+    __device__ __forceinline__ void load(const Rows<MX> (&rows)[M], const Row16 (&xs)[TT], int c) {
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
-            const int c = SC * p + i < chunks ? SC * p + i : chunks - 1;
+        for (int m = 0; m < M; ++m) rows[m].load(c, &w[m]);
 #pragma unroll
-            for (int m = 0; m < M; ++m) rows[m].load(c, &w[m][i]);
-#pragma unroll
-            for (int t = 0; t < TT; ++t) xs[t].template load<MX>(c, x[t][i]);
-        }
+        for (int t = 0; t < TT; ++t) xs[t].template load<MX>(c, x[t]);
     }
     // rows of Kw (16-bit weights) and Kx elements
-    __device__ __forceinline__ void multiply(int Kw, int Kx, int p, f32x4 (&acc)[M][TT]) {
+    __device__ __forceinline__ void multiply(int Kw, int Kx, int c, f32x4 (&acc)[M][TT]) {
+        if constexpr (!MX) {
 #pragma unroll
-        for (int i = 0; i < SC; ++i) {
-            const int c = SC * p + i;
-            if constexpr (!MX) {
-#pragma unroll
-                for (int m = 0; m < M; ++m) Row16{nullptr, Kw}.fix<false>(c, w[m][i].v);
-            }
-#pragma unroll
-            for (int t = 0; t < TT; ++t) Row16{nullptr, Kx}.template fix<MX>(c, x[t][i]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int m = 0; m < M; ++m) {
-                    const u32x4 o = operand<ACT, MX>(w[m][i], s);
-#pragma unroll
-                    for (int t = 0; t < TT; ++t) acc[m][t] = mfma<ACT>(o, x[t][i][s], acc[m][t]);
-                }
+            for (int m = 0; m < M; ++m) Row16{nullptr, Kw}.fix<false>(c, w[m].v);
         }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) Row16{nullptr, Kx}.template fix<MX>(c, x[t]);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                const u32x4 o = operand<ACT, MX>(w[m], s);
+#pragma unroll
+                for (int t = 0; t < TT; ++t) acc[m][t] = mfma<ACT>(o, x[t][s], acc[m][t]);
+            }
     }
 };
 
 // ----------------------------------------------------------------------------------- first product
 // A unit of work is 16 P columns of h (their gate and up rows) of one slot's expert for all its tokens, 16 TT in a pass over
 // the weights (more tokens take further passes, whose weights come from L2). A block takes a contiguous range of the
-// units; in each its waves take the pieces of K in turn, those of the next unit in flight behind the current one's
+// units; in each its waves take the chunks of K in turn, those of the next unit in flight behind the current one's
 // products, and their sums meet in LDS, where one wave finishes 16 columns of 16 tokens while the others go on.
-template <int ACT, bool MX, int P, int SC, int TT, int NW>
+template <int ACT, bool MX, int P, int TT, int NW>
 __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
     constexpr int COLS = 16 * P, kSums = NW * 2 * P * TT * 1024;
     __shared__ Routing r;
@@ -327,7 +317,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
     const Scratch to = scratch_of(a, lay);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int64_t ldh = padded(a.I);
-    const int tiles = (int)(ldh / COLS), chunks = (a.H + 127) / 128, pieces = (chunks + SC - 1) / SC;
+    const int tiles = (int)(ldh / COLS), chunks = (a.H + 127) / 128;
     route(a, r, *reinterpret_cast<RoutingWork*>(work));
     if (blockIdx.x == 0) {
         for (int s = threadIdx.x; s < r.slots; s += blockDim.x) to.plan->expert[s] = r.expert[s];
@@ -340,10 +330,10 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
     const int u0 = part_start(units, (int)gridDim.x, (int)blockIdx.x), u1 = part_start(units, (int)gridDim.x, (int)blockIdx.x + 1);
     if (u0 >= u1) return;
 
-    // Unit, first token of the pass, piece: what is loaded next, and what is multiplied next, in the same order. All waves
-    // take as many steps per pass; those without a piece left in it do nothing in the last.
+    // Unit, first token of the pass, chunk: what is loaded next, and what is multiplied next, in the same order. All waves
+    // take as many steps per pass; those without a chunk left in it do nothing in the last.
     struct At {
-        int u, from, p, e, base, n;
+        int u, from, c, e, base, n;
     };
     auto open = [&](At& t) {
         const int s = t.u / tiles;
@@ -353,9 +343,9 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
         t.from = 0;
     };
     auto next = [&](At& t) {                         // true at the end of a pass
-        t.p += NW;
-        if (t.p - wave < pieces) return false;
-        t.p = wave;
+        t.c += NW;
+        if (t.c - wave < chunks) return false;
+        t.c = wave;
         t.from += 16 * TT;
         if (t.from >= t.n && ++t.u < u1) open(t);
         return true;
@@ -377,10 +367,10 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
             x[i] = Row16{static_cast<const uint16_t*>(a.x) + r.token[l.base + (at < l.n ? at : l.n - 1)] * a.ldx, a.H};
         }
     };
-    typedef Piece<ACT, MX, 2 * P, SC, TT> Ops;
+    typedef Piece<ACT, MX, 2 * P, TT> Ops;
     auto load = [&](Ops& o) {
-        if (l.u >= u1 || pieces == 0) return;
-        o.load(rows, x, l.p < pieces ? l.p : pieces - 1, chunks);
+        if (l.u >= u1 || chunks == 0) return;
+        o.load(rows, x, l.c < chunks ? l.c : chunks - 1);
         if (next(l) && l.u < u1) point();
     };
     open(l);
@@ -396,7 +386,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
     clear();
     int turn = 0;                                    // of the waves at finishing
     auto step = [&](Ops& o) {                        // false at the end of the range
-        if (m.p < pieces) o.multiply(a.H, a.H, m.p, acc);
+        if (m.c < chunks) o.multiply(a.H, a.H, m.c, acc);
         const At t = m;
         const bool end = next(m);
         load(o);
@@ -444,11 +434,11 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
 }
 
 // ---------------------------------------------------------------------------------- second product
-// A block: 16 M columns of y and one of the splits of all slots' pieces of K, of which each wave takes a contiguous
+// A block: 16 M columns of y and one of the splits of all slots' chunks of K, of which each wave takes a contiguous
 // part. A wave multiplies a slot's rows of h, 16 TT in a pass, and adds the sums to its own y [token][columns] in LDS when
 // it leaves the slot. The waves' y are added in their order; with several splits the block that finishes last adds the
 // splits' in theirs.
-template <int ACT, bool MX, int M, int SC, int TT, int NW>
+template <int ACT, bool MX, int M, int TT, int NW>
 __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     constexpr int COLS = 16 * M;
     extern __shared__ __align__(16) float ys[];      // [NW][T][COLS]
@@ -459,7 +449,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int n0 = COLS * (int)blockIdx.x, split = (int)blockIdx.y, splits = lay.splits;
     const int64_t ldh = padded(a.I);
-    const int chunks = (int)(ldh / 128), pieces = (chunks + SC - 1) / SC;
+    const int chunks = (int)(ldh / 128);
     int slots = 0;
     if (a.I > 0 && a.k > 0) {
         const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
@@ -470,18 +460,18 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     }
     for (int i = threadIdx.x; i < NW * a.T * COLS; i += blockDim.x) ys[i] = 0.0f;
     __syncthreads();
-    const int items = slots * pieces, parts = NW * splits, part = split * NW + wave;
+    const int items = slots * chunks, parts = NW * splits, part = split * NW + wave;
     const int begin = part_start(items, parts, part), end = part_start(items, parts, part + 1);
 
-    // Item (slot and piece) and first token of the pass: what is loaded next, and what is multiplied next. A slot's items of
+    // Item (slot and chunk) and first token of the pass: what is loaded next, and what is multiplied next. A slot's items of
     // this wave are first ... stop - 1, taken once per pass.
     struct At {
         int it, first, stop, s, from, base, n;
     };
     auto open = [&](At& t) {
         t.first = t.it;
-        t.s = t.it / pieces;
-        t.stop = t.s * pieces + pieces < end ? t.s * pieces + pieces : end;
+        t.s = t.it / chunks;
+        t.stop = t.s * chunks + chunks < end ? t.s * chunks + chunks : end;
         t.base = __builtin_amdgcn_readfirstlane((int)first[t.s]);
         t.n = __builtin_amdgcn_readfirstlane((int)first[t.s + 1]) - t.base;
         t.from = 0;
@@ -509,10 +499,10 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
             h[i] = Row16{from.h + (l.base + (at < l.n ? at : l.n - 1)) * ldh, (int)ldh};
         }
     };
-    typedef Piece<ACT, MX, M, SC, TT> Ops;
+    typedef Piece<ACT, MX, M, TT> Ops;
     auto load = [&](Ops& o) {
         if (l.it >= end) return;
-        o.load(rows, h, l.it - l.s * pieces, chunks);
+        o.load(rows, h, l.it - l.s * chunks);
         if (next(l) && l.it < end) point();
     };
     f32x4 acc[M][TT];
@@ -525,7 +515,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
         At m = l;
         point();
         auto step = [&](Ops& o) {                    // false at the end
-            o.multiply(a.I, (int)ldh, m.it - m.s * pieces, acc);
+            o.multiply(a.I, (int)ldh, m.it - m.s * chunks, acc);
             const At t = m;
             const bool left = next(m);
             load(o);
@@ -599,68 +589,77 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     }
 }
 
-// Launch shapes, measured with weights that come from HBM (graph of six calls, us per call).
+// Launch shapes. Measured on 19 layers of MXFP4 and as many of 16-bit weights, one to 64 tokens on 2 of 8 ... 8 of 128 experts of 1024
+// x 512 ... 8192 x 4096, weights that come from HBM, in us; "a / b" stands for a as chosen and b as the alternative.
 //
-// First product: MXFP4 weights take two pairs of tiles and 256 columns of K at a time (64 tokens, 8 of 128 experts of 2048 x
-// 1408: 188 with it, one pair 232), tokens 16 to a pass (two tiles of tokens at once: 209). 16-bit weights take one pair
-// and 128 columns, 256 bytes of each row; from 17 tokens on 32 to a pass, however few an expert has (same layer in BF16: 411,
-// 16 to a pass 436; 2 of 8 experts of 4096 x 2048: 113 and 133). Blocks of four waves, 16 waves to a CU, or, where few units come
-// to a block, 8 (8 tokens, 4 of 32 of 4096 x 2048 in MXFP4: 80, with 16 93; the 64 tokens above 202 with 8); for 16-bit weights and
-// up to 16 tokens from 1024 units on one block of eight waves a CU (16 tokens, 4 of 32 of 4096 x 2048: 229 for 239; 4 tokens,
-// 8 of 128 of 2048 x 768: 66 for 71).
+// From 12 tokens per expert on, a pass takes 32 tokens in both products (64 tokens, 2 of 8 of 4096 x 2048: MXFP4 58 / 66, BF16
+// 110 / 117; 32 x 2048 x 1408 on 8 of 128, 2 per expert: 112, with 32 tokens 120). In the first product of 16-bit weights it does so for
+// more than 16 tokens however few an expert has (64 tokens, 4 of 32 of 4096 x 2048: 362 / 381).
 //
-// Second product: blocks of 16 waves for up to 16 tokens and 16 columns (16 tokens, 4 of 32 of 4096 x 2048 in BF16: 228, with
-// eight 242; one token, 4 of 32 of 2048 x 1408: 28.6 for 29.7), else of eight. Few pieces go whole to the blocks of 16 columns (one token, 8 of 128 of 2048 x 1408 in
-// MXFP4: 25.8, with 32 columns and four splits 27.9; 4 of 32 in BF16: 28.5, with two splits 30.0). More are split until
-// there are 256 blocks, in MXFP4 of 32 columns, which halves the loads of h (the 64 tokens above: 188, 16 columns in two
-// splits 213; 4 tokens, 8 of 128 of 2048 x 768 in BF16: 66, unsplit 73).
-template <bool MX> constexpr int kInPairs = MX ? 2 : 1;
-template <bool MX> constexpr int kPieceChunks = MX ? 2 : 1;
-
+// First product: blocks of two waves with 32 columns of h, 24 waves to a CU where tokens are many (64 x 2048 x 1408 on 8
+// of 128 in MXFP4: 185 / 192 with 12) and experts differ in their passes, else 12, which are resident together (16 tokens:
+// 96 / 98; blocks of four waves 102; two chunks of K at a time for four waves 105). Below 512 units blocks of eight waves with 16
+// columns (one token, 4096 x 2048, 2 of 8: 17.0 / 19.4). 16-bit weights take 16 columns, up to 16 tokens from 1024 units on in blocks of
+// eight waves, one to a CU (16 tokens, 4 of 32 of 4096 x 2048: 214 / 217), else of four, 16 waves to a CU.
+//
+// Second product: 16 columns in blocks of 16 waves where there is little work for 256 blocks, unsplit (one token, 8 of 128 of
+// 2048 x 1408 in MXFP4: 22.3, 64 columns 23.9; 16 tokens, 2 of 8 of 4096 x 2048: 36.0 / 39.7), and for 16-bit weights in
+// splits until there are 256 blocks (4 x 2048 x 768 on 8 of 128 in BF16: 63.7, unsplit 66.6). More work in MXFP4 takes 64 columns
+// of y in blocks of eight waves, which reads h four times less often (64 x 2048 x 1408 on 8 of 128: 160 / 168), and
+// passes of 32 tokens take 32 columns (64 tokens, 2 of 8 of 8192 x 4096 in BF16: 356, 16 columns 385).
 struct Shape {
     Layout lay;
+    bool two;                   // 32 tokens to a pass
     int outs;                   // tiles of 16 columns in a block of the second product
-    int64_t slots, units;       // most there can be
+    int64_t slots;              // most there can be
 };
 Shape shape_of(int64_t T, int64_t k, int64_t E, int64_t I, int64_t N, bool mx) {
     Shape s;
     s.slots = T * k < E ? T * k : E;
-    s.units = s.slots * (padded(I) / (16 * (mx ? kInPairs<true> : kInPairs<false>)));
-    const int64_t wide = 128 * (mx ? kPieceChunks<true> : kPieceChunks<false>);
-    const bool many = s.slots * ((I + wide - 1) / wide) >= (mx ? 96 : 128);
-    s.outs = mx && many ? 2 : 1;
+    s.two = T > 16 && T * k >= 12 * E;
+    const int64_t items = s.slots * (padded(I) / 128);
+    const bool many = items >= (mx ? (N > 2048 ? 512 : 256) : 128);
+    s.outs = s.two ? 2 : mx && many ? 4 : 1;
     s.lay.tiles = (int)((N + 16 * s.outs - 1) / (16 * s.outs));
     s.lay.width = s.lay.tiles * 16 * s.outs;
-    s.lay.splits = many && s.lay.tiles <= 128 ? (s.lay.tiles > 32 ? 256 / s.lay.tiles : 8) : 1;
+    const int most = s.two ? 4 : 8;
+    s.lay.splits = (many || (s.two && items > 0)) && s.lay.tiles <= 128 ? (most * s.lay.tiles < 256 ? most : 256 / s.lay.tiles) : 1;
     return s;
 }
 
-template <int ACT, bool MX, int TT, int NW>
+template <int ACT, bool MX, int P, int TT, int NW>
 hipError_t in_go(const MlpArgs& a, const Shape& s, int waves, hipStream_t stream) {
-    const int64_t room = (int64_t)device_cus() * waves / NW;
-    hipLaunchKernelGGL((mlp_in<ACT, MX, kInPairs<MX>, kPieceChunks<MX>, TT, NW>), dim3((unsigned)(s.units < room ? s.units : room)),
-                       dim3(64 * NW), 0, stream, a, s.lay);
+    const int64_t room = (int64_t)device_cus() * waves / NW, units = s.slots * (padded(a.I) / (16 * P));
+    hipLaunchKernelGGL((mlp_in<ACT, MX, P, TT, NW>), dim3((unsigned)(units < room ? units : room)), dim3(64 * NW), 0, stream, a, s.lay);
     return hipGetLastError();
 }
 template <int ACT, bool MX, int M, int TT, int NW>
 hipError_t out_go(const MlpArgs& a, const Layout& lay, hipStream_t stream) {
-    hipLaunchKernelGGL((mlp_out<ACT, MX, M, kPieceChunks<MX>, TT, NW>), dim3((unsigned)lay.tiles, (unsigned)lay.splits), dim3(64 * NW),
+    hipLaunchKernelGGL((mlp_out<ACT, MX, M, TT, NW>), dim3((unsigned)lay.tiles, (unsigned)lay.splits), dim3(64 * NW),
                        (size_t)NW * a.T * 64 * M, stream, a, lay);
     return hipGetLastError();
 }
 template <int ACT, bool MX>
 hipError_t mlp_go(const MlpArgs& a, hipStream_t stream) {
     const Shape s = shape_of(a.T, a.k, a.E, a.I, a.N, MX);
-    if (s.units > 0) {
+    const int64_t units = s.slots * (padded(a.I) / (MX ? 32 : 16));
+    if (units > 0) {
         hipError_t e;
-        if constexpr (MX) e = in_go<ACT, true, 1, 4>(a, s, s.units >= 4096 ? 16 : 8, stream);
-        else if (a.T > 16) e = in_go<ACT, false, 2, 4>(a, s, 16, stream);
-        else if (s.units >= 1024) e = in_go<ACT, false, 1, 8>(a, s, 8, stream);
-        else e = in_go<ACT, false, 1, 4>(a, s, 16, stream);
+        if constexpr (MX) {
+            if (s.two) e = in_go<ACT, true, 2, 2, 4>(a, s, 16, stream);
+            else if (units < 512) e = in_go<ACT, true, 1, 1, 8>(a, s, 16, stream);
+            else e = in_go<ACT, true, 2, 1, 2>(a, s, a.T > 32 ? 24 : 12, stream);
+        } else {
+            if (a.T > 16) e = in_go<ACT, false, 1, 2, 4>(a, s, 24, stream);
+            else if (units >= 1024) e = in_go<ACT, false, 1, 1, 8>(a, s, 8, stream);
+            else e = in_go<ACT, false, 1, 1, 4>(a, s, 16, stream);
+        }
         if (e != hipSuccess) return e;
     }
-    if constexpr (MX) return s.outs == 2 ? out_go<ACT, true, 2, 1, 8>(a, s.lay, stream) : out_go<ACT, true, 1, 1, 16>(a, s.lay, stream);
-    else return a.T > 16 ? out_go<ACT, false, 1, 2, 8>(a, s.lay, stream) : out_go<ACT, false, 1, 1, 16>(a, s.lay, stream);
+    if (s.outs == 2) return out_go<ACT, MX, 2, 2, 8>(a, s.lay, stream);
+    if constexpr (MX)
+        if (s.outs == 4) return out_go<ACT, true, 4, 1, 8>(a, s.lay, stream);
+    return out_go<ACT, MX, 1, 1, 16>(a, s.lay, stream);
 }
 
 }  // namespace

@@ -1,9 +1,9 @@
 // gfx950 MXFP4 row quantizer, its inverse, and MXFP4 matrix products: Y[m][n] = sum over blocks b of 32 of
 // 2^(sx[m][b] + sw[n][b] - 254) sum_{k in b} X[m][k] W[n][k] (+ bias[n]) on the matrix cores, which take the codes
-// and the scale bytes as they are (v_mfma_scale_f32_16x16x128_f8f6f4), fp32 sums. The format and its layout stand in
+// and the scale bytes as they are (v_mfma_scale_f32_16x16x128_f8f6f4 and 32x32x64), fp32 sums. The format and its layout stand in
 // mxfp4.h.
 //
-// Operand lane layout (checked on the device): lane l supplies 32 codes (16 bytes) of A row l % 16 and of B column
+// Operand lane layout of the 16-row instruction (checked on the device): lane l supplies 32 codes (16 bytes) of A row l % 16 and of B column
 // l % 16, K group l / 16, and a scale byte for each, and receives C[4 (l / 16) + i][l % 16], i < 4. A and B take the
 // same K positions per lane, so equal k meet whatever the order. W is the A operand and X the B operand: a lane then
 // holds four consecutive output columns of one row. A scale byte of 255 gives NaN, whatever the codes.
@@ -34,7 +34,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 //
 // Every block of 32 stands alone, so a wave takes 16 rows x 128 columns: four lanes to a block, eight elements
 // to a lane, four rows to a load; the maximum goes over the four lanes (DPP). The scales of 16 rows
-// leave in one store of 64 bytes.
+// leave in one store of 64 bytes. Bound by HBM: 4096 x 10240 BF16 in 20 us, 5.3 TB/s; one row takes a launch (4 us).
 template <int SRC> struct Elem { typedef uint16_t type; };
 template <> struct Elem<EP_F32> { typedef uint32_t type; };
 
@@ -217,9 +217,9 @@ MxGrid mx_grid(int64_t rows, int64_t M, int64_t K) {
 // are neighbours in one dword and the instruction picks the byte. The scales of a stage are two dwords per row, loaded
 // into LDS beside the codes: [2][rows], a contiguous piece of each 128 columns.
 //
-// 4096 x 8192 x 8192 takes 122-138 us (boxes differ), 4.0-4.5 PFLOP/s, of which 20 go to the starts of the two rounds of
+// 4096 x 8192 x 8192 takes 117-124 us (boxes differ), 4.4-4.7 PFLOP/s, of which 20 go to the starts of the two rounds of
 // tiles and their 67 MB of outputs. Per 4096 of K it takes 53 us, 5.1 PFLOP/s: the matrix cores alone, without any memory,
-// reach 7.2 on random codes, where the card holds 1.7-1.9 GHz (9.9 on zeros).
+// reach 7.2 on random codes, where the card holds 1.7-1.9 GHz (9.9 on zeros). They are busy for 65% of the cycles.
 template <int ROWS>
 constexpr int scale_words() { return 2 * ROWS < 64 ? 64 : 2 * ROWS; }
 
@@ -562,7 +562,7 @@ hipError_t launch_dequantize_rows_mx(const uint8_t* Q, const uint8_t* S, int64_t
 // Tile of a product with one weight: the least of (1 + share (rounds - 1)) (steps step_us + tile_us), rounds of tiles over the
 // CUs, steps of 256 KS columns; share is below 1 where a CU holds several blocks. The figures are fitted to 120 products (M 1 ...
 // 4096; N x K 1024 x 2048 ... 8192 x 8192 and 4096 x 16384, weights that come from HBM), where the tile that they pick takes
-// 1.6% longer than the fastest of 20 on average and 15% at most. They pick, e.g., 256 x 256 for 4096 x 8192 x 8192 (122 us; 256
+// 1.6% longer than the fastest of 20 on average and 15% at most. They pick, e.g., 256 x 256 for 4096 x 8192 x 8192 (117-122 us; 256
 // x 192: 145, 256 x 128: 154, 128 x 128: 165), 256 x 192 for 1024 x 11520 x 3840 (28; 256 x 256: 29, 256 x 128: 39), 128 x 128 for
 // 512 x 8192 x 8192 (25; 128 x 64: 31), 128 x 64 for 333 x 5003 x 3968 (11.3; 64 x 64: 11.8, 128 x 128: 12.0), 64 x 64 for 256 x 4096 x
 // 4096 (7.7; 128 x 64: 10.5), 32 x 32 for 64 x 8192 x 8192 (13.1; 64 x 64: 14.5), 16 x 32 with two K groups for 1 x 11520 x 3840 (7.0;

@@ -382,30 +382,22 @@ __device__ __forceinline__ void store_staged(const GemmMxArgs& g, const TileAt& 
     }
 }
 
-template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS, bool EXPERTS>
-__global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
+template <int BM, int BN>
+constexpr int stage_bytes() { return (BM + BN) * 128 + 4 * scale_words<BM>() + 4 * scale_words<BN>(); }
+
+// The tile t. smem: the rings of the K groups, then a spare KiB.
+template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS>
+__device__ __forceinline__ void tile_product(const GemmMxArgs& g, const TileAt& t, uint8_t* smem) {
     constexpr int NW = WGM * WGN;                            // waves of a K group
     constexpr int TI = BM / WGM / MR, TJ = BN / WGN / MR, SUB = Instr<MR>::kSub, Q = Instr<MR>::kQuads;
     static_assert(TI * WGM * MR == BM && TJ * WGN * MR == BN, "whole parts per wave");
     constexpr int kScalesX = (BM + BN) * 128, kScalesW = kScalesX + 4 * scale_words<BM>();
-    constexpr int kStage = kScalesW + 4 * scale_words<BN>();
+    constexpr int kStage = stage_bytes<BM, BN>();
     constexpr int kLoads = Dma<BM, NW>::kLoads + Dma<BN, NW>::kLoads + ScaleDma<BM, BN, NW>::kEach;      // per wave and stage
     constexpr int kRing = S * kStage;                        // of a K group
     constexpr int kSums = (KS - 1) * BM * BN * 4;
     static_assert(kSums <= KS * kRing, "the sums of the other K groups reuse the rings");
-    __shared__ __align__(1024) uint8_t smem[KS * kRing + 1024];
     uint8_t* spare = smem + KS * kRing;
-    TileAt t;
-    if constexpr (EXPERTS) {
-        t = expert_tile<BM, BN>(g);
-        if (!t.any) return;
-        if (t.e == g.experts) {
-            zero_rows(g, t, BM, BN);
-            return;
-        }
-    } else {
-        t = block_tile<BM, BN>(g);
-    }
     const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) % NW);
     const int kg = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6) / NW);   // K group of the wave
     uint8_t* lds = smem + kg * kRing;
@@ -513,15 +505,37 @@ __global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
     else store(std::integral_constant<int, EP_F32>{});
 }
 
-template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS>
+// A tile of 256 rows of which an expert has at most 128 is one of 128 rows with a stage more (4096 tokens, 4 of 64 experts of
+// 2048 x 2048, 256 rows each on average: 78.6 us, as full tiles 83.2; 512 rows each of 32 of 2048 x 4096: 103.3 and 103.7).
+template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS, bool EXPERTS>
+__global__ __launch_bounds__(64 * WGM * WGN * KS) void gemm_mx(GemmMxArgs g) {
+    constexpr int kFull = KS * S * stage_bytes<BM, BN>();
+    if constexpr (EXPERTS && BM == 256) {
+        constexpr int kHalf = 3 * stage_bytes<BM / 2, BN>();
+        __shared__ __align__(1024) uint8_t smem[(kFull > kHalf ? kFull : kHalf) + 1024];
+        const TileAt t = expert_tile<BM, BN>(g);
+        if (!t.any) return;
+        if (t.e == g.experts) zero_rows(g, t, BM, BN);
+        else if (t.m_end - t.m0 <= BM / 2) tile_product<BM / 2, BN, MR, WGM, WGN, 3, 1>(g, t, smem);
+        else tile_product<BM, BN, MR, WGM, WGN, S, KS>(g, t, smem);
+    } else if constexpr (EXPERTS) {
+        __shared__ __align__(1024) uint8_t smem[kFull + 1024];
+        const TileAt t = expert_tile<BM, BN>(g);
+        if (!t.any) return;
+        if (t.e == g.experts) zero_rows(g, t, BM, BN);
+        else tile_product<BM, BN, MR, WGM, WGN, S, KS>(g, t, smem);
+    } else {
+        __shared__ __align__(1024) uint8_t smem[kFull + 1024];
+        tile_product<BM, BN, MR, WGM, WGN, S, KS>(g, block_tile<BM, BN>(g), smem);
+    }
+}
+
+template <int BM, int BN, int MR, int WGM, int WGN, int S, int KS, bool EXPERTS>
 hipError_t tiled_go(const GemmMxArgs& g, hipStream_t stream) {
     int64_t blocks = row_tiles(g, BM) * (((int64_t)g.N + BN - 1) / BN);
-    if (g.experts) blocks = (blocks + 7) / 8 * 8;              // an eighth of the tiles for each XCD
+    if (EXPERTS) blocks = (blocks + 7) / 8 * 8;                // an eighth of the tiles for each XCD
     if (blocks * (64 * WGM * WGN * KS) > kMaxThreads) return hipErrorInvalidValue;
-    if (g.experts)
-        hipLaunchKernelGGL((gemm_mx<BM, BN, MR, WGM, WGN, S, KS, true>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
-    else
-        hipLaunchKernelGGL((gemm_mx<BM, BN, MR, WGM, WGN, S, KS, false>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
+    hipLaunchKernelGGL((gemm_mx<BM, BN, MR, WGM, WGN, S, KS, EXPERTS>), dim3((unsigned)blocks), dim3(64 * WGM * WGN * KS), 0, stream, g);
     return hipGetLastError();
 }
 
@@ -575,11 +589,11 @@ struct TileCost {
     hipError_t (*go)(const GemmMxArgs&, hipStream_t);
 };
 const TileCost kTiles[] = {
-    {256, 256, 1, 1.309f, 3.06f, 1.0f, tiled_go<256, 256, 16, 2, 4, 2, 1>}, {256, 192, 1, 1.088f, 2.90f, 1.0f, tiled_go<256, 192, 16, 2, 4, 2, 1>},
-    {256, 128, 1, 0.848f, 2.22f, 1.0f, tiled_go<256, 128, 16, 4, 2, 3, 1>}, {128, 128, 1, 0.553f, 0.76f, 1.0f, tiled_go<128, 128, 32, 2, 4, 3, 1>},
-    {128, 64, 1, 0.431f, 0.91f, 0.86f, tiled_go<128, 64, 16, 4, 2, 3, 1>},  {64, 64, 1, 0.257f, 0.25f, 0.91f, tiled_go<64, 64, 32, 2, 2, 4, 1>},
-    {32, 32, 2, 0.246f, 0.53f, 0.95f, tiled_go<32, 32, 16, 1, 2, 4, 2>},    {16, 32, 2, 0.259f, 0.10f, 0.65f, tiled_go<16, 32, 16, 1, 2, 3, 2>},
-    {16, 32, 4, 0.436f, 1.42f, 1.0f, tiled_go<16, 32, 16, 1, 2, 4, 4>},
+    {256, 256, 1, 1.309f, 3.06f, 1.0f, tiled_go<256, 256, 16, 2, 4, 2, 1, false>}, {256, 192, 1, 1.088f, 2.90f, 1.0f, tiled_go<256, 192, 16, 2, 4, 2, 1, false>},
+    {256, 128, 1, 0.848f, 2.22f, 1.0f, tiled_go<256, 128, 16, 4, 2, 3, 1, false>}, {128, 128, 1, 0.553f, 0.76f, 1.0f, tiled_go<128, 128, 32, 2, 4, 3, 1, false>},
+    {128, 64, 1, 0.431f, 0.91f, 0.86f, tiled_go<128, 64, 16, 4, 2, 3, 1, false>},  {64, 64, 1, 0.257f, 0.25f, 0.91f, tiled_go<64, 64, 32, 2, 2, 4, 1, false>},
+    {32, 32, 2, 0.246f, 0.53f, 0.95f, tiled_go<32, 32, 16, 1, 2, 4, 2, false>},    {16, 32, 2, 0.259f, 0.10f, 0.65f, tiled_go<16, 32, 16, 1, 2, 3, 2, false>},
+    {16, 32, 4, 0.436f, 1.42f, 1.0f, tiled_go<16, 32, 16, 1, 2, 4, 4, false>},
 };
 
 hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
@@ -611,11 +625,12 @@ hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
     if (rows > 150) {
         // a partly filled tile per expert: half a tile on average
         const int64_t tiles = (2 * g.M + 256 * used) / 512;
-        return cost(kTiles[1], tiles) < cost(kTiles[0], tiles) ? kTiles[1].go(g, stream) : kTiles[0].go(g, stream);
+        return cost(kTiles[1], tiles) < cost(kTiles[0], tiles) ? tiled_go<256, 192, 16, 2, 4, 2, 1, true>(g, stream)
+                                                               : tiled_go<256, 256, 16, 2, 4, 2, 1, true>(g, stream);
     }
-    if (rows <= 2) return tiled_go<16, 64, 16, 1, 4, 4, 1>(g, stream);
-    if (rows <= 20 || (rows > 40 && rows <= 64)) return tiled_go<64, 128, 32, 2, 4, 3, 1>(g, stream);
-    return tiled_go<128, 128, 32, 2, 4, 2, 1>(g, stream);
+    if (rows <= 2) return tiled_go<16, 64, 16, 1, 4, 4, 1, true>(g, stream);
+    if (rows <= 20 || (rows > 40 && rows <= 64)) return tiled_go<64, 128, 32, 2, 4, 3, 1, true>(g, stream);
+    return tiled_go<128, 128, 32, 2, 4, 2, 1, true>(g, stream);
 }
 
 }  // namespace ep

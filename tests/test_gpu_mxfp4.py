@@ -184,7 +184,8 @@ def test_product_of_misaligned_codes():
 
 @pytest.mark.parametrize("counts,behind,N,K", [
     ([3], 0, 70, 128), ([0, 5, 0, 1, 17], 0, 130, 384), ([2, 0, 0, 40], 9, 64, 256), ([200, 1, 130, 0, 90], 3, 515, 640),
-    ([0, 0, 0], 6, 33, 128), ([1] * 70, 2, 66, 256), ([0] * 127 + [300], 0, 129, 384), ([700, 650], 0, 300, 512)])
+    ([0, 0, 0], 6, 33, 128), ([1] * 70, 2, 66, 256), ([0] * 127 + [300], 0, 129, 384), ([700, 650], 0, 300, 512),
+    ([300, 515, 1, 700], 5, 200, 640), ([300, 515, 128, 640], 130, 8192, 256)])
 def test_product_of_experts(counts, behind, N, K):
     g = gen(len(counts) + N)
     E, R = len(counts), sum(counts) + behind

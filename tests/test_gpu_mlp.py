@@ -89,6 +89,15 @@ def test_sizes(T, k, E, H, I, N, dtype, mxfp4):
 
 
 @pytest.mark.parametrize("mxfp4", [False, True])
+@pytest.mark.parametrize("T,k,E,H,I,N", [(64, 16, 1024, 16, 8, 8), (1, 1024, 1024, 40, 24, 20), (2, 1, 1, 2 ** 20, 8, 8), (2, 1, 1, 8, 2 ** 20, 8),
+                                         (2, 1, 1, 8, 8, 2 ** 20), (64, 2, 2, 130, 20, 2 ** 15 + 3)])
+def test_limits(T, k, E, H, I, N, mxfp4):
+    """The largest numbers of choices and experts, and the longest and widest matrices."""
+    l = Layer(T, k, E, H, I, N, mxfp4=mxfp4)
+    l.check(ep.mlp_forward_experts(*l.args()))
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
 def test_choices(mxfp4):
     """Dropped choices, tokens without any, an expert named twice in a token, all tokens on one expert."""
     g = torch.Generator().manual_seed(3)

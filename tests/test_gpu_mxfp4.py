@@ -354,7 +354,7 @@ def test_threads():
 def repeats(y, rows):
     """All rows of y (its first dimension) repeat the first `rows`, bit for bit."""
     v = y.view(torch.int16) if y.dtype == torch.bfloat16 else y
-    return all(torch.equal(v[i:i + rows], v[:rows]) for i in range(rows, y.shape[0], rows))
+    return bool((v.reshape(-1, rows, *v.shape[1:]) == v[:rows]).all())
 
 
 def test_many_rows():
@@ -394,3 +394,29 @@ def test_experts_past_32_bits():
     offsets = torch.tensor([0] * E + [5], dtype=torch.int32).cuda()
     y = ep.gemm_mxfp4_experts(xq.cuda(), xs.cuda(), allq, alls, offsets)
     mx.check_product(y[:, -40:], mx.values(xq, xs), mx.values(wq[-40:], ws[:, -40:]))
+
+
+def test_longest_rows():
+    """K = 2^22, the limit, in a small tile and, by the experts' product, in tiles of 256 rows: rows that repeat."""
+    K = 2 ** 22
+    (xq, xs), (wq, ws) = mx.random_matrix(gen(24), 1, K), mx.random_matrix(gen(25), 1, K)
+    x, w = mx.values(xq, xs), mx.values(wq, ws)
+    mx.check_product(ep.gemm_mxfp4(*(t.cuda() for t in (xq, xs, wq, ws))), x, w)
+    many = [xq.cuda().repeat(300, 1), xs.cuda().repeat(1, 300, 1), wq.cuda().repeat(260, 1)[None], ws.cuda().repeat(1, 260, 1)[None]]
+    y = ep.gemm_mxfp4_experts(*many, torch.tensor([0, 300], dtype=torch.int32).cuda(), out_dtype=torch.float32)
+    assert (y == y[0, 0]).all()
+    mx.check_product(y[:1, :1], x, w)
+    v = torch.randn((2, K), generator=gen(26))
+    same_codes(v, *ep.quantize_rows_mxfp4(v.cuda()))
+
+
+def test_most_rows():
+    """2^27 rows, the limit, of one block."""
+    base = torch.randn((4096, 32), generator=gen(27)).to(torch.bfloat16)
+    q, s = ep.quantize_rows_mxfp4(base.cuda().repeat(2 ** 15, 1))
+    assert repeats(q, 4096) and repeats(s[0], 4096)
+    same_codes(base, q[:4096], s[:, :4096])
+    wq, ws = mx.random_matrix(gen(28), 3, 128)
+    y = ep.gemm_mxfp4(q, s, wq.cuda(), ws.cuda())
+    assert repeats(y, 4096)
+    mx.check_product(y[:4096], mx.values(*mx.quantize(base)), mx.values(wq, ws))

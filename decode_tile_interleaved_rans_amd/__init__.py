@@ -1099,7 +1099,7 @@ def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out
     weights); weights: fp32 [T, k] or None (ones). w_in: [experts, 2 I, H], rows 0 ... I - 1 of an expert give g, the others u;
     w_out: [experts, N, I]; both of x's type, or, with in_scales and out_scales, MXFP4 codes and scales as
     quantize_rows_mxfp4 gives them (exact in BF16; in FP16 values below 2^-14 lose bits and none may pass 65504). Biases: BF16 [experts, 2 I] and
-    [experts, N]. fp32 sums; weights[t, j] h is rounded once to x's type, and y [T, N] once.
+    [experts, N]. fp32 sums; h is rounded once to x's type (in FP16 a magnitude above 65504 is infinite), and y [T, N] once.
 
     The weights of the experts that some token chose are read once; the host waits for nothing, so the call can be captured
     into a graph. For more tokens use sort_tokens, a product per expert and combine_tokens. It has no gradient: tensors

@@ -3,9 +3,9 @@
 // some token chose are all that counts: both kernels stream them from memory straight into the matrix operands and split K
 // over the waves of a block, whose sums are added in a fixed order.
 //
-// A token that names an expert twice meets it once, with the sum of the two weights. w[t][j] goes into h before its one
-// rounding to the activations' type (the same relative error as rounding h itself), so that the second product's sums
-// over the experts need no further factors.
+// A token that names an expert twice meets it once, with the sum of the two weights. h is rounded once to the activations'
+// type, which the matrix instruction takes. w[t][j] is not in it: it multiplies the 32-bit sums of the second product where
+// a wave leaves an expert, since in FP16 w h may pass 65504 or fall below 2^-14 where h does not.
 //
 // What bounds it: 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16 read 1.4 GB in 214-226 us, over 6 TB/s (a read of 400 MB in
 // this pattern alone reaches 6.0). In MXFP4 the tokens' loads count as well: 64 tokens on 8 of 128 experts of 2048 x 1408
@@ -124,6 +124,7 @@ __device__ __forceinline__ int part_start(int n, int parts, int i) {
 // What the first kernel leaves for the second, before h in the scratch.
 struct Plan {
     int slots;
+    float weight[kMlpMaxChoices];                                           // of a row, as in Routing
     uint16_t expert[kMlpMaxChoices], first[kMlpMaxChoices + 1];              // of a slot, as in Routing
     uint8_t token[kMlpMaxChoices];                                          // of a row
 };
@@ -322,7 +323,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
     if (blockIdx.x == 0) {
         for (int s = threadIdx.x; s < r.slots; s += blockDim.x) to.plan->expert[s] = r.expert[s];
         for (int s = threadIdx.x; s <= r.slots; s += blockDim.x) to.plan->first[s] = r.first[s];
-        for (int i = threadIdx.x; i < r.first[r.slots]; i += blockDim.x) to.plan->token[i] = r.token[i];
+        for (int i = threadIdx.x; i < r.first[r.slots]; i += blockDim.x) to.plan->token[i] = r.token[i], to.plan->weight[i] = r.weight[i];
         for (int i = threadIdx.x; i < lay.tiles; i += blockDim.x) to.done[i] = 0;
         if (threadIdx.x == 0) to.plan->slots = r.slots;
     }
@@ -418,10 +419,9 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
                     us[v] += bf16_at(a.b_in, b + a.I);
                 }
             }
-            const float part = r.weight[t.base + at];
             uint16_t o4[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) o4[v] = col + v < a.I ? to_act<ACT>(part * (gs[v] / (1.0f + expf(-gs[v])) * us[v])) : 0;
+            for (int v = 0; v < 4; ++v) o4[v] = col + v < a.I ? to_act<ACT>(gs[v] / (1.0f + expf(-gs[v])) * us[v]) : 0;
             *reinterpret_cast<uint2*>(to.h + (t.base + at) * ldh + col) = make_uint2(o4[0] | (uint32_t)o4[1] << 16, o4[2] | (uint32_t)o4[3] << 16);
         }
         turn += P * TT;
@@ -435,8 +435,8 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
 
 // ---------------------------------------------------------------------------------- second product
 // A block: 16 M columns of y and one of the splits of all slots' chunks of K, of which each wave takes a contiguous
-// part. A wave multiplies a slot's rows of h, 16 TT in a pass, and adds the sums to its own y [token][columns] in LDS when
-// it leaves the slot. The waves' y are added in their order; with several splits the block that finishes last adds the
+// part. A wave multiplies a slot's rows of h, 16 TT in a pass, and adds the sums, times the rows' weights, to its own y
+// [token][columns] in LDS when it leaves the slot. The waves' y are added in their order; with several splits the block that finishes last adds the
 // splits' in theirs.
 template <int ACT, bool MX, int M, int TT, int NW>
 __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
@@ -444,6 +444,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     extern __shared__ __align__(16) float ys[];      // [NW][T][COLS]
     __shared__ uint16_t expert[kMlpMaxChoices], first[kMlpMaxChoices + 1];
     __shared__ uint8_t token[kMlpMaxChoices];
+    __shared__ float weight[kMlpMaxChoices];
     __shared__ bool last;
     const Scratch from = scratch_of(a, lay);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -454,7 +455,7 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     if (a.I > 0 && a.k > 0) {
         const int most = a.T * a.k < a.E ? a.T * a.k : a.E;
         for (int i = threadIdx.x; i < most; i += blockDim.x) expert[i] = from.plan->expert[i], first[i + 1] = from.plan->first[i + 1];
-        for (int i = threadIdx.x; i < a.T * a.k; i += blockDim.x) token[i] = from.plan->token[i];
+        for (int i = threadIdx.x; i < a.T * a.k; i += blockDim.x) token[i] = from.plan->token[i], weight[i] = from.plan->weight[i];
         if (threadIdx.x == 0) first[0] = 0;
         slots = __builtin_amdgcn_readfirstlane(from.plan->slots);
     }
@@ -522,11 +523,11 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
             if (left) {
 #pragma unroll
                 for (int i = 0; i < TT; ++i) {
-                    const int at = t.from + 16 * i + (lane & 15);
-                    float* y = ys + (wave * a.T + token[t.base + (at < t.n ? at : t.n - 1)]) * COLS + 4 * (lane >> 4);
+                    const int at = t.from + 16 * i + (lane & 15), row = t.base + (at < t.n ? at : t.n - 1);
+                    float* y = ys + (wave * a.T + token[row]) * COLS + 4 * (lane >> 4);
 #pragma unroll
                     for (int q = 0; q < M; ++q) {
-                        if (at < t.n) *reinterpret_cast<f32x4*>(y + 16 * q) += acc[q][i];
+                        if (at < t.n) *reinterpret_cast<f32x4*>(y + 16 * q) += weight[row] * acc[q][i];
                         acc[q][i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     }
                 }

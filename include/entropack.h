@@ -548,7 +548,8 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
  * scales [E][Hp / 128][2 I][4] and [E][Ip / 128][N][4] as ep_quantize_rows_mxfp4 lays them out (codes 16-byte, scales
  * 4-byte aligned, EP_EINVAL); MXFP4 weights meet the activations in act's type (exact in EP_BF16 up to scale bytes of 251;
  * in EP_F16 from 2^-14 to 65504). in_bias: [E][2 I], out_bias: [E][N], bf16 or NULL.
- * fp32 sums; w h is rounded once to act's type, y once. The same bits on every call.
+ * fp32 sums; h is rounded once to act's type (in EP_F16 a magnitude above 65504 is infinite), y once. The same bits on
+ * every call.
  *   scratch: ep_mlp_forward_experts_scratch bytes of device memory, 16-byte aligned (NULL when that is 0), read and written
  * by this call's kernels only. T in 0 ... 64, T k <= 1024, E in 1 ... 1024, H, I and N <= 2^20 (EP_ERANGE): for more
  * tokens sort them (ep_sort_tokens) and use a product per expert. Asynchronous on hip_stream; allocates nothing. */

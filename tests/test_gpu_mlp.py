@@ -1,4 +1,5 @@
 """The expert layer for few tokens on the GPU, against its formula in 64 bits."""
+import math
 from concurrent.futures import ThreadPoolExecutor
 
 import pytest
@@ -314,3 +315,42 @@ def test_refusals():
     import torch.autograd.forward_ad as fwd
     with fwd.dual_level(), pytest.raises(ValueError):
         ep.mlp_forward_experts(fwd.make_dual(x, torch.ones_like(x)), *a[1:])
+
+
+@pytest.mark.parametrize("mxfp4", [False, True])
+@pytest.mark.parametrize("T,k,E,H,I,N,dup", [(5, 2, 4, 128, 96, 64, False), (3, 3, 4, 140, 70, 33, True), (64, 2, 8, 128, 130, 96, False),
+                                             (40, 8, 128, 64, 256, 64, False)])
+@pytest.mark.parametrize("weight,x_scale,out_scale", [(16.0, 48.0, 2.0 ** -8), (2.0 ** -12, 0.045, 2.0 ** 8), (-40.0, 48.0, 2.0 ** -9)])
+def test_fp16_weights_far_from_one(T, k, E, H, I, N, dup, weight, x_scale, out_scale, mxfp4):
+    """h fits FP16 and the weighted h does not: it would pass 65504, or lose bits below 2^-14. The weights belong to the 32-bit sums, so
+    y is off by h's own rounding (half a step, 2^-11 of it or 2^-25) times the weight, and by what Layer.check counts otherwise."""
+    ids = torch.full((T, k), 1) if dup else None
+    l = Layer(T, k, E, H, I, N, torch.float16, mxfp4, seed=11, ids=ids)
+    l.x = (l.x.double() * x_scale).to(torch.float16)
+    l.w = torch.full((T, k), weight)
+    if mxfp4:
+        l.scales = (l.scales[0], (l.scales[1].int() + round(math.log2(out_scale))).to(torch.uint8))
+        l.v_out = mx.values(l.wout, l.scales[1])[..., :I]
+    else:
+        l.wout = (l.wout.double() * out_scale).to(torch.float16)
+        l.v_out = l.wout.double()
+    ulp, half = 2.0 ** -23, 2.0 ** -11
+    y0, off, top = torch.zeros((T, N), dtype=torch.float64), torch.zeros((T, N), dtype=torch.float64), 0.0
+    for t in range(T):
+        for e in set(l.ids[t].tolist()):
+            p = l.w[t].double()[l.ids[t] == e].sum()
+            x = l.x[t].double()
+            a, d = l.v_in[e] @ x, (H + 1) * ulp * (l.v_in[e].abs() @ x.abs())
+            gate, up, dg, du = a[:I], a[I:], d[:I], d[I:]
+            s = gate * torch.sigmoid(gate)
+            h = s * up
+            dh = 1.1 * dg * up.abs() + s.abs() * du + 1.1 * dg * du + h.abs() * 2.0 ** -20
+            dh = dh + (h.abs() + dh) * half + 2.0 ** -25
+            top = max(top, (h.abs() + dh).max().item())
+            y0[t] += p * (l.v_out[e] @ h)
+            off[t] += p.abs() * (l.v_out[e].abs() @ dh + (I + k + 8) * ulp * (l.v_out[e].abs() @ h.abs()))
+    off = off + 2 * k * ulp * y0.abs()
+    off = off + (y0.abs() + off) * half + 2.0 ** -25
+    assert top < 65504 and (abs(weight) * top > 65504 or abs(weight) * top < 2.0 ** -14) and (y0.abs() + off).max() < 65504
+    got = ep.mlp_forward_experts(*l.args()).cpu().double()
+    assert ((got - y0).abs() <= off).all(), ((got - y0).abs() / off).max().item()

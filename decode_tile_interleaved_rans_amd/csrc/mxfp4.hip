@@ -14,6 +14,7 @@
 
 #include "entropack.h"
 #include "kernels.h"
+#include "mx_tiles.h"
 #include "mxfp4.h"
 #include "tiles.h"
 
@@ -573,46 +574,23 @@ hipError_t launch_dequantize_rows_mx(const uint8_t* Q, const uint8_t* S, int64_t
     }
 }
 
-// Tile of a product with one weight: the least of (1 + share (rounds - 1)) (steps step_us + tile_us), rounds of tiles over the
-// CUs, steps of 256 KS columns; share is below 1 where a CU holds several blocks. The figures are fitted to 120 products (M 1 ...
-// 4096; N x K 1024 x 2048 ... 8192 x 8192 and 4096 x 16384, weights that come from HBM), where the tile that they pick takes
-// 1.6% longer than the fastest of 20 on average and 15% at most. They pick, e.g., 256 x 256 for 4096 x 8192 x 8192 (117-122 us; 256
-// x 192: 145, 256 x 128: 154, 128 x 128: 165), 256 x 192 for 1024 x 11520 x 3840 (28; 256 x 256: 29, 256 x 128: 39), 128 x 128 for
-// 512 x 8192 x 8192 (25; 128 x 64: 31), 128 x 64 for 333 x 5003 x 3968 (11.3; 64 x 64: 11.8, 128 x 128: 12.0), 64 x 64 for 256 x 4096 x
-// 4096 (7.7; 128 x 64: 10.5), 32 x 32 for 64 x 8192 x 8192 (13.1; 64 x 64: 14.5), 16 x 32 with two K groups for 1 x 11520 x 3840 (7.0;
-// 32 x 32: 7.3) and with four for 1 x 4096 x 16384 (10.4; two: 11.6). The instruction of 16 rows takes less power than that
-// of 32 (7.2 PFLOP/s of random codes without memory, 6.4), which tells in the largest tiles; in 128 x 128 and 64 x 64, where
-// waves have 64 x 32 or 32 x 32 of them, the one of 32 rows is ahead by 4 to 10%.
-struct TileCost {
-    int bm, bn, ks;
-    float step_us, tile_us, share;
-    hipError_t (*go)(const GemmMxArgs&, hipStream_t);
+// The kernels of kMxTiles. The instruction of 16 rows takes less power than that of 32 (7.2 PFLOP/s of random codes without
+// memory, 6.4), which tells in the largest tiles; in 128 x 128 and 64 x 64, where waves have 64 x 32 or 32 x 32 of
+// them, the one of 32 rows is ahead by 4 to 10%.
+template <int I, int MR, int WGM, int WGN, int S>
+constexpr hipError_t (*tile_go())(const GemmMxArgs&, hipStream_t) {
+    return tiled_go<kMxTiles[I].bm, kMxTiles[I].bn, MR, WGM, WGN, S, kMxTiles[I].ks, false>;
+}
+hipError_t (*const kTileGo[])(const GemmMxArgs&, hipStream_t) = {
+    tile_go<0, 16, 2, 4, 2>(), tile_go<1, 16, 2, 4, 2>(), tile_go<2, 16, 4, 2, 3>(), tile_go<3, 32, 2, 4, 3>(), tile_go<4, 16, 4, 2, 3>(),
+    tile_go<5, 32, 2, 2, 4>(), tile_go<6, 16, 1, 2, 4>(), tile_go<7, 16, 1, 2, 3>(), tile_go<8, 16, 1, 2, 4>(),
 };
-const TileCost kTiles[] = {
-    {256, 256, 1, 1.309f, 3.06f, 1.0f, tiled_go<256, 256, 16, 2, 4, 2, 1, false>}, {256, 192, 1, 1.088f, 2.90f, 1.0f, tiled_go<256, 192, 16, 2, 4, 2, 1, false>},
-    {256, 128, 1, 0.848f, 2.22f, 1.0f, tiled_go<256, 128, 16, 4, 2, 3, 1, false>}, {128, 128, 1, 0.553f, 0.76f, 1.0f, tiled_go<128, 128, 32, 2, 4, 3, 1, false>},
-    {128, 64, 1, 0.431f, 0.91f, 0.86f, tiled_go<128, 64, 16, 4, 2, 3, 1, false>},  {64, 64, 1, 0.257f, 0.25f, 0.91f, tiled_go<64, 64, 32, 2, 2, 4, 1, false>},
-    {32, 32, 2, 0.246f, 0.53f, 0.95f, tiled_go<32, 32, 16, 1, 2, 4, 2, false>},    {16, 32, 2, 0.259f, 0.10f, 0.65f, tiled_go<16, 32, 16, 1, 2, 3, 2, false>},
-    {16, 32, 4, 0.436f, 1.42f, 1.0f, tiled_go<16, 32, 16, 1, 2, 4, 4, false>},
-};
+static_assert(sizeof kTileGo / sizeof *kTileGo == kMxTileCount, "a kernel for each tile");
 
 hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
     if (g.M <= 0 || g.N <= 0) return hipSuccess;
     const int64_t cus = device_cus();
-    auto over = [](int64_t n, int64_t by) { return (n + by - 1) / by; };
-    auto cost = [&](const TileCost& t, int64_t row_tiles) {
-        const int64_t rounds = over(row_tiles * over(g.N, t.bn), cus);
-        return (1.0f + t.share * (float)(rounds - 1)) * ((float)over(g.K, 256 * t.ks) * t.step_us + t.tile_us);
-    };
-    if (!g.experts) {
-        const TileCost* best = nullptr;
-        float least = 0.0f;
-        for (const TileCost& t : kTiles) {
-            const float us = cost(t, over(g.M, t.bm));
-            if (!best || us < least) best = &t, least = us;
-        }
-        return best->go(g, stream);
-    }
+    if (!g.experts) return kTileGo[mx_tile(g.M, g.N, g.K, cus)](g, stream);
     // Experts: how many rows each has is known to the device only, so the tile goes by the average. Measured with rows
     // spread unevenly (a factor of e^0.5 as standard deviation), weights that come from HBM, in us: 2 rows each on 16 x 64 23.2 (32
     // experts of 4096 x 2048; 64 x 128: 24.1) and 12.1 at 1 row each of 64 of 1024 x 2048 (64 x 128: 14.2); 8 rows on 64 x 128 28.8 (16 x 64:
@@ -621,12 +599,13 @@ hipError_t launch_gemm_mx(const GemmMxArgs& g, hipStream_t stream) {
     // row tile: 45.7 and over 40); 100 rows on 128 x 128 43.3 and 121 (128 of 2816 x 2048; 64 x 128: 50.6, 256 x 256: 136). Above that
     // whichever of 256 x 256 and 256 x 192 fills its rounds better: 200 rows 62 and 56 (128 x 128: 66 and 63), 400 rows of 8 of
     // 8192 x 4096 on 256 x 192 86 (256 x 256: 99), 800 rows of 128 of 2816 x 2048 on 256 x 256 505 (256 x 192: 545).
-    const int64_t used = g.M < g.experts ? g.M : g.experts, rows = over(g.M, used);
+    const int64_t used = g.M < g.experts ? g.M : g.experts, rows = mx_over(g.M, used);
     if (rows > 150) {
         // a partly filled tile per expert: half a tile on average
         const int64_t tiles = (2 * g.M + 256 * used) / 512;
-        return cost(kTiles[1], tiles) < cost(kTiles[0], tiles) ? tiled_go<256, 192, 16, 2, 4, 2, 1, true>(g, stream)
-                                                               : tiled_go<256, 256, 16, 2, 4, 2, 1, true>(g, stream);
+        return mx_cost(kMxTiles[1], tiles, g.N, g.K, cus) < mx_cost(kMxTiles[0], tiles, g.N, g.K, cus)
+                   ? tiled_go<256, 192, 16, 2, 4, 2, 1, true>(g, stream)
+                   : tiled_go<256, 256, 16, 2, 4, 2, 1, true>(g, stream);
     }
     if (rows <= 2) return tiled_go<16, 64, 16, 1, 4, 4, 1, true>(g, stream);
     if (rows <= 20 || (rows > 40 && rows <= 64)) return tiled_go<64, 128, 32, 2, 4, 3, 1, true>(g, stream);

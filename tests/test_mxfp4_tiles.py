@@ -6,6 +6,8 @@ import subprocess
 
 import pytest
 
+from test_gpu_mxfp4_tiles import SIZES
+
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "decode_tile_interleaved_rans_amd", "csrc")
 CUS = 256
 
@@ -49,3 +51,12 @@ def test_named_examples(tile, M, N, K, want):
 def test_fastest_measured(tile, M, N, K, want):
     """Products of the fit whose picked tile is the fastest of the nine that there are."""
     assert tile(M, N, K) == want
+
+
+def test_sizes_reach_every_tile(tile):
+    """The sizes of the GPU test take the tiles they stand for, leave none out, end inside a tile in both directions and turn its
+    ring (four stages at most) more than once."""
+    for want, M, N, K in SIZES:
+        assert tile(M, N, K) == want, (M, N, K)
+        assert M % want[0] and N % want[1] and K % 256 == 128 and -(-K // (256 * want[2])) > 4
+    assert len({s[0] for s in SIZES}) == tile.count

@@ -761,7 +761,7 @@ def gemm_mxfp4_experts(xq, xs, wq, ws, offsets, bias=None, out_dtype=None, strea
 
 
 # ------------------------------------------------------------------------------------ expert routing
-def _no_tangents(*tensors):
+def _no_tangents(*tensors, of="the expert routing has no forward-mode derivative; use reverse mode"):
     """Refuses the dual tensors of forward-mode differentiation: they do not require a gradient, so the
     kernels would drop their tangents without a word."""
     forward_ad = _torch().autograd.forward_ad
@@ -769,7 +769,7 @@ def _no_tangents(*tensors):
         return
     for t in tensors:
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
-            raise ValueError("the expert routing has no forward-mode derivative; use reverse mode")
+            raise ValueError(of)
 
 
 def _sort_raw(x, ids, n_experts):
@@ -1114,7 +1114,7 @@ def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out
         for t in (x, weights, w_in, w_out, in_bias, out_bias):
             if t is not None and t.requires_grad:
                 raise ValueError("the expert layer for few tokens has no gradient; detach its inputs")
-    _no_tangents(x, weights, w_in, w_out, in_bias, out_bias)
+    _no_tangents(x, weights, w_in, w_out, in_bias, out_bias, of="the expert layer for few tokens has no derivative; detach its inputs")
     dtype, f32, bf16, u8 = x.dtype, torch.float32, torch.bfloat16, torch.uint8
     if dtype is not bf16 and dtype is not torch.float16:
         raise ValueError(f"x must be bfloat16 or float16, got {dtype}")

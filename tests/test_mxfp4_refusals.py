@@ -149,3 +149,13 @@ def test_expert_layer_tensors_on_the_host():
     with pytest.raises(ValueError):
         ep.mlp_forward_experts(t((4, 64), dtype=torch.bfloat16), t((4, 2), dtype=torch.int64), None, t((3, 64, 64), dtype=torch.bfloat16),
                                t((3, 16, 32), dtype=torch.bfloat16))
+
+
+def test_tangents_are_refused():
+    """The expert layer has no derivative of either mode: its message does not send to the other."""
+    import torch.autograd.forward_ad as fwd
+    t = lambda *shape: torch.zeros(shape, dtype=torch.bfloat16)
+    with fwd.dual_level():
+        with pytest.raises(ValueError, match="derivative") as e:
+            ep.mlp_forward_experts(fwd.make_dual(t(4, 64), t(4, 64)), torch.zeros((4, 2), dtype=torch.int64), None, t(3, 64, 64), t(3, 16, 32))
+        assert "reverse" not in str(e.value)

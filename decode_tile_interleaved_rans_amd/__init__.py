@@ -632,11 +632,12 @@ def quantize_rows_mxfp4(x, stream=None):
     Returns (codes, scales), uint8, with Kp the width rounded up to whole 128 elements, zeros behind: codes [..., M,
     Kp / 2], two to a byte, the even element in the low half; scales [..., Kp / 128, M, 4], the bytes b of a row's 128
     elements side by side. Row-major scales s [M, Kp / 32] from elsewhere are
-    s.view(M, -1, 4).transpose(0, 1).contiguous(). On `stream` (default: the current stream; another stream first
-    waits for the current one)."""
+    s.view(M, -1, 4).transpose(0, 1).contiguous(). It has no gradient: an x that asks for one is refused (detach it).
+    On `stream` (default: the current stream; another stream first waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: quantize_rows_mxfp4(x), x)
     torch = _torch()
+    _no_gradient("the MXFP4 quantizer has", x)
     dims, dtype, dev = x.dim(), x.dtype, torch.cuda.current_device() if x.is_cuda else None
     if dims == 2:
         M, K = rows, ldx = x.shape
@@ -712,6 +713,8 @@ def _mx_aligned(t, to: int):
 
 def _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype):
     torch = _torch()
+    if bias is not None:
+        _no_gradient("the MXFP4 product has", bias)
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if out_dtype not in _float_types():
         raise ValueError(f"out_dtype must be bfloat16, float16 or float32, got {out_dtype}")
@@ -742,8 +745,8 @@ def _gemm_mxfp4(xq, xs, wq, ws, offsets, bias, out_dtype):
 def gemm_mxfp4(xq, xs, wq, ws, bias=None, out_dtype=None, stream=None):
     """Y = X W^T (+ bias) of two MXFP4 matrices: codes xq [M, Kp / 2] and wq [N, Kp / 2] with scales xs [Kp / 128, M, 4]
     and ws [Kp / 128, N, 4], as quantize_rows_mxfp4 gives them; fp32 sums, bias BF16 [N], output BF16 (default), FP16
-    or FP32, rounded once. Codes at an address that is no multiple of 16 are copied first. On `stream` (default: the
-    current stream; another stream first waits for the current one)."""
+    or FP32, rounded once. Codes at an address that is no multiple of 16 are copied first. It has no gradient: a bias that asks for one
+    is refused. On `stream` (default: the current stream; another stream first waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: _gemm_mxfp4(xq, xs, wq, ws, None, bias, out_dtype), xq, xs, wq, ws, bias)
     return _gemm_mxfp4(xq, xs, wq, ws, None, bias, out_dtype)
@@ -770,6 +773,16 @@ def _no_tangents(*tensors, of="the expert routing has no forward-mode derivative
     for t in tensors:
         if t is not None and forward_ad.unpack_dual(t).tangent is not None:
             raise ValueError(of)
+
+
+def _no_gradient(what: str, *tensors):
+    """Refuses tensors that ask for a derivative, of either mode, of a call that has none."""
+    torch = _torch()
+    for t in tensors:
+        if t is not None and t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{what} no gradient; detach its inputs")
+    if getattr(torch.autograd.forward_ad, "_current_level", 0) >= 0:
+        _no_tangents(*tensors, of=f"{what} no derivative; detach its inputs")
 
 
 def _sort_raw(x, ids, n_experts):
@@ -1110,11 +1123,7 @@ def mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales=None, out
         return _on_stream(stream, lambda: mlp_forward_experts(x, expert_ids, weights, w_in, w_out, in_scales, out_scales, in_bias,
                                                               out_bias),
                           x, expert_ids, weights, w_in, w_out, in_scales, out_scales, in_bias, out_bias)
-    if torch.is_grad_enabled():
-        for t in (x, weights, w_in, w_out, in_bias, out_bias):
-            if t is not None and t.requires_grad:
-                raise ValueError("the expert layer for few tokens has no gradient; detach its inputs")
-    _no_tangents(x, weights, w_in, w_out, in_bias, out_bias, of="the expert layer for few tokens has no derivative; detach its inputs")
+    _no_gradient("the expert layer for few tokens has", x, weights, w_in, w_out, in_bias, out_bias)
     dtype, f32, bf16, u8 = x.dtype, torch.float32, torch.bfloat16, torch.uint8
     if dtype is not bf16 and dtype is not torch.float16:
         raise ValueError(f"x must be bfloat16 or float16, got {dtype}")

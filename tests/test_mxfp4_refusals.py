@@ -151,6 +151,21 @@ def test_expert_layer_tensors_on_the_host():
                                t((3, 16, 32), dtype=torch.bfloat16))
 
 
+def test_gradients_are_refused():
+    """The quantizer and the products have no gradient: inputs that ask for one are refused, not dropped, before any other check."""
+    asks = lambda *shape, dtype=torch.float32: torch.zeros(shape, dtype=dtype, requires_grad=True)
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    gemm = (u8(4, 64), u8(1, 4, 4), u8(6, 64), u8(1, 6, 4))
+    experts = (u8(4, 64), u8(1, 4, 4), u8(2, 6, 64), u8(2, 1, 6, 4), torch.zeros(3, dtype=torch.int32))
+    calls = [lambda: ep.quantize_rows_mxfp4(asks(4, 64)), lambda: ep.quantize_rows_mxfp4(asks(2, 4, 64)),
+             lambda: ep.gemm_mxfp4(*gemm, asks(6, dtype=torch.bfloat16)), lambda: ep.gemm_mxfp4_experts(*experts, asks(2, 6, dtype=torch.bfloat16))]
+    for call in calls:
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):       # without gradients the next check speaks
+            call()
+
+
 def test_tangents_are_refused():
     """The expert layer has no derivative of either mode: its message does not send to the other."""
     import torch.autograd.forward_ad as fwd
@@ -159,3 +174,13 @@ def test_tangents_are_refused():
         with pytest.raises(ValueError, match="derivative") as e:
             ep.mlp_forward_experts(fwd.make_dual(t(4, 64), t(4, 64)), torch.zeros((4, 2), dtype=torch.int64), None, t(3, 64, 64), t(3, 16, 32))
         assert "reverse" not in str(e.value)
+
+
+def test_tangents_of_rows_and_biases_are_refused():
+    import torch.autograd.forward_ad as fwd
+    u8 = lambda *shape: torch.zeros(shape, dtype=torch.uint8)
+    with fwd.dual_level():
+        dual = lambda *shape: fwd.make_dual(torch.zeros(shape, dtype=torch.bfloat16), torch.ones(shape, dtype=torch.bfloat16))
+        for call in (lambda: ep.quantize_rows_mxfp4(dual(4, 64)), lambda: ep.gemm_mxfp4(u8(4, 64), u8(1, 4, 4), u8(6, 64), u8(1, 6, 4), dual(6))):
+            with pytest.raises(ValueError, match="no derivative"):
+                call()

@@ -184,3 +184,14 @@ def test_tangents_of_rows_and_biases_are_refused():
         for call in (lambda: ep.quantize_rows_mxfp4(dual(4, 64)), lambda: ep.gemm_mxfp4(u8(4, 64), u8(1, 4, 4), u8(6, 64), u8(1, 6, 4), dual(6))):
             with pytest.raises(ValueError, match="no derivative"):
                 call()
+
+
+def test_relative_error_of_normal_values():
+    """What the format costs: products of random normal rows in MXFP4 are 16% off (relative, L2), in INT8 with a scale per row below
+    2%. 2 x 65536 values and more make the figure, so that it varies by far less than the 1% between the bounds."""
+    g = torch.Generator().manual_seed(1)
+    x, w = torch.randn((100, 2048), generator=g), torch.randn((120, 2048), generator=g)
+    int8 = lambda t: ((t / t.abs().amax(1, keepdim=True) * 127).round() * t.abs().amax(1, keepdim=True) / 127).double()
+    want = x.double() @ w.double().T
+    off = lambda a, b: ((a @ b.T - want).norm() / want.norm()).item()
+    assert 0.155 < off(mx.values(*mx.quantize(x)), mx.values(*mx.quantize(w))) < 0.165 and off(int8(x), int8(w)) < 0.02

@@ -681,7 +681,7 @@ def _mx_shapes(q, s, qname: str, sname: str, dims: int, dev):
 def dequantize_rows_mxfp4(codes, scales, out_dtype=None, columns=None, stream=None):
     """The values of MXFP4 codes and scales (quantize_rows_mxfp4's, of a matrix or of the experts' matrices) as
     [..., M, columns] in BF16 (default), FP16 or FP32; columns: how many of the Kp padded columns (default: all).
-    Exact in BF16 and FP32 for scale bytes up to 251, rounded to nearest even in FP16. On `stream` (default: the
+    Exact in BF16 and FP32 for scale bytes up to 252, rounded to nearest even in FP16. On `stream` (default: the
     current stream; another stream first waits for the current one)."""
     if stream is not None:
         return _on_stream(stream, lambda: dequantize_rows_mxfp4(codes, scales, out_dtype, columns), codes, scales)

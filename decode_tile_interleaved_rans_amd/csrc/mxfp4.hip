@@ -136,8 +136,8 @@ __global__ __launch_bounds__(256) void quantize_rows_mx(const void* Xv, int64_t 
     }
 }
 
-// The inverse: a lane turns the eight codes of a dword into values, exactly in BF16 and FP32 where they have the
-// range (BF16 and FP32: up to scale bytes of 251), rounded once in FP16.
+// The inverse: a lane turns the eight codes of a dword into values, exactly in BF16 and FP32 (up to scale bytes
+// of 252, the largest that the quantizer gives; above it 6 times the scale passes their range), rounded once in FP16.
 template <int DST>
 __device__ __forceinline__ void eight_values(uint32_t q, float unit, Eight<DST>* out) {
     auto two = [&](auto sel) {

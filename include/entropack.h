@@ -453,8 +453,8 @@ ep_status ep_quantize_rows_mxfp4(const void* dev_x, ep_dtype src, int64_t rows, 
 
 /* The values of MXFP4 codes: Y [rows][K] of dst (EP_BF16, EP_F16 or EP_F32; EP_EUNSUPPORTED otherwise) from the first K
  * columns of codes and scales of Kp columns (Kp % 128 == 0, Kp >= K, EP_EINVAL otherwise), laid out as
- * ep_quantize_rows_mxfp4 does. Exact in EP_BF16 and EP_F32 up to scale bytes of 251, rounded to nearest even in EP_F16;
- * a scale byte of 255 gives NaN.
+ * ep_quantize_rows_mxfp4 does. Exact in EP_BF16 and EP_F32 up to scale bytes of 252 (the largest that
+ * ep_quantize_rows_mxfp4 gives), rounded to nearest even in EP_F16; a scale byte of 255 gives NaN.
  * Source: "EntroPack: Fast and Accurate Entropy-Coded Weight Compression at Arbitrary Bitrates", Abstract
  * (reconstruction of numerical values into a container). Limits as ep_quantize_rows_mxfp4. Asynchronous on
  * hip_stream; allocates nothing. */
@@ -546,7 +546,7 @@ ep_status ep_combine_tokens_grad(const void* dev_ys, ep_dtype dtype, const int32
  *   w_in: [E][2 I][H], rows 0 ... I - 1 of an expert give g, the others u; w_out: [E][N][I]. Elements of act, or, with
  * in_scales and out_scales (both or neither, EP_EINVAL otherwise), MXFP4 codes [E][2 I][Hp / 2] and [E][N][Ip / 2] with
  * scales [E][Hp / 128][2 I][4] and [E][Ip / 128][N][4] as ep_quantize_rows_mxfp4 lays them out (codes 16-byte, scales
- * 4-byte aligned, EP_EINVAL); MXFP4 weights meet the activations in act's type (exact in EP_BF16 up to scale bytes of 251;
+ * 4-byte aligned, EP_EINVAL); MXFP4 weights meet the activations in act's type (exact in EP_BF16 up to scale bytes of 252;
  * in EP_F16 from 2^-14 to 65504). in_bias: [E][2 I], out_bias: [E][N], bf16 or NULL.
  * fp32 sums; h is rounded once to act's type (in EP_F16 a magnitude above 65504 is infinite), y once. The same bits on
  * every call.

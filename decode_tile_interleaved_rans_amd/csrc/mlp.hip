@@ -4,8 +4,11 @@
 // over the waves of a block, whose sums are added in a fixed order.
 //
 // A token that names an expert twice meets it once, with the sum of the two weights. h is rounded once to the activations'
-// type, which the matrix instruction takes. w[t][j] is not in it: it multiplies the 32-bit sums of the second product where
-// a wave leaves an expert, since in FP16 w h may pass 65504 or fall below 2^-14 where h does not.
+// type, which the matrix instruction takes: y is then 0.0023 off (relative, L2; 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16),
+// where its own rounding alone makes 0.0017. h as the sum of two such numbers brings that back, but was measured 6 to 25%
+// slower (that layer 215 -> 250 us, 64 tokens on 2 of 8 experts of 8192 x 4096 in MXFP4 162 -> 203). w[t][j] is not in h: it
+// multiplies the 32-bit sums of the second product where a wave leaves an expert, since in FP16 w h may pass 65504 or fall below
+// 2^-14 where h does not.
 //
 // What bounds it: 16 tokens on 4 of 32 experts of 4096 x 2048 in BF16 read 1.4 GB in 214-226 us, over 6 TB/s (a read of 400 MB in
 // this pattern alone reaches 6.0). In MXFP4 the tokens' loads count as well: 64 tokens on 8 of 128 experts of 2048 x 1408
@@ -597,17 +600,28 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
 // 110 / 117; 32 x 2048 x 1408 on 8 of 128, 2 per expert: 112, with 32 tokens 120). In the first product of 16-bit weights it does so for
 // more than 16 tokens however few an expert has (64 tokens, 4 of 32 of 4096 x 2048: 362 / 381).
 //
-// First product: blocks of two waves with 32 columns of h, 24 waves to a CU where tokens are many (64 x 2048 x 1408 on 8
-// of 128 in MXFP4: 185 / 192 with 12) and experts differ in their passes, else 12, which are resident together (16 tokens:
-// 96 / 98; blocks of four waves 102; two chunks of K at a time for four waves 105). Below 512 units blocks of eight waves with 16
-// columns (one token, 4096 x 2048, 2 of 8: 17.0 / 19.4). 16-bit weights take 16 columns, up to 16 tokens from 1024 units on in blocks of
-// eight waves, one to a CU (16 tokens, 4 of 32 of 4096 x 2048: 214 / 217), else of four, 16 waves to a CU.
+// First product: blocks of two waves with 32 columns of h, where 64 tokens' experts differ in their passes a grid of 24 waves
+// to a CU (64 x 2048 x 1408 on 8 of 128 in MXFP4: 185 / 192 with 12), up to 32 tokens of 12 (16 tokens: 96 / 98 with 24; blocks of four waves
+// 102; two chunks of K at a time for four waves 105). Below 512 units blocks of eight waves with 16 columns (one token,
+// 4096 x 2048, 2 of 8: 17.0 / 19.4). 16-bit weights take 16 columns: above 16 tokens in passes of 32, a grid of 24 waves to a CU (64 tokens, 4
+// of 32 of 4096 x 2048: 362 / 374 with 16), up to 16 tokens from 1024 units on in blocks of eight waves, one to a CU (16
+// tokens, 4 of 32 of 4096 x 2048: 214 / 217), else in blocks of four and a grid of 16 waves to a CU (16 x 1024 x 512 on 2 of 16: 8 to 32
+// all 23.4). A grid's waves to a CU are not those that run at once: the registers hold 16 with 16 columns in MXFP4, 8 in passes of 32
+// tokens and 12 else, and the blocks past those start as others end, which evens experts of unlike passes out at the price of
+// their routing.
 //
 // Second product: 16 columns in blocks of 16 waves where there is little work for 256 blocks, unsplit (one token, 8 of 128 of
 // 2048 x 1408 in MXFP4: 22.3, 64 columns 23.9; 16 tokens, 2 of 8 of 4096 x 2048: 36.0 / 39.7), and for 16-bit weights in
 // splits until there are 256 blocks (4 x 2048 x 768 on 8 of 128 in BF16: 63.7, unsplit 66.6). More work in MXFP4 takes 64 columns
 // of y in blocks of eight waves, which reads h four times less often (64 x 2048 x 1408 on 8 of 128: 160 / 168), and
 // passes of 32 tokens take 32 columns (64 tokens, 2 of 8 of 8192 x 4096 in BF16: 356, 16 columns 385).
+//
+// Work is counted in items, a slot's 128 of K. `many` of them are, for 16-bit weights, 128: splits gain nothing at 88 (one token, 8
+// of 128 of 2048 x 1408: 42.4 / 42.3 unsplit; two, 4 of 32: 40.1 / 39.1) and 5% at 192 and 256 (the case above; 24 x 2048 x 2048 on 2 of 16: 83.7 /
+// 88.5). In MXFP4, up to 2048 columns of y, which make at most 128 blocks of 16, 256 (24 x 2048 x 2048 on 2 of 16, 256 items: 64 columns in
+// splits 38.9 / 39.5; 4 x 2048 x 768 on 8 of 128, 192: 32.6 / 31.8); wider y fill the CUs with blocks of 16 columns, and 64 columns are worth their
+// splits from 512 on (32 x 4096 x 2048 on 4 of 32, 512: 106.7 / 107.6, though 8 tokens of that layer take 69.7 / 68.6; 16 tokens, 2 of 8,
+// 128: 41.1 / 36.0).
 struct Shape {
     Layout lay;
     bool two;                   // 32 tokens to a pass

@@ -66,7 +66,7 @@ __device__ __forceinline__ int expert_counts(const Args& g, int e0, int* a, int*
 // Every wave looks its tile up on its own. Tiles are numbered expert by expert, within an expert in groups
 // of 8 row tiles that walk the column tiles together. Consecutive block ids land on different XCDs, so
 // each XCD takes a contiguous eighth of the numbers: the rows and the weight of a group then meet in
-// one L2. Against tiles dealt out round robin, column tiles innermost (same weights every call): 4096 tokens
+// one L2. Against tiles dealt out round robin, column tiles innermost (INT8, same weights every call): 4096 tokens
 // on 4 of 32 experts (2048 x 4096) 183 us for 261, 1024 tokens 73 for 80, 8 of 128 (1408 x 2048) 175 for 178, 2 of
 // 8 (8192 x 4096) 307 for 373, with groups of one row tile 355; 16 tokens (4096 x 2048) 30.7 for 31.4.
 template <int BM, int BN, typename Args>

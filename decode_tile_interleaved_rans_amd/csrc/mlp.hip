@@ -439,8 +439,8 @@ __global__ __launch_bounds__(64 * NW) void mlp_in(MlpArgs a, Layout lay) {
 // ---------------------------------------------------------------------------------- second product
 // A block: 16 M columns of y and one of the splits of all slots' chunks of K, of which each wave takes a contiguous
 // part. A wave multiplies a slot's rows of h, 16 TT in a pass, and adds the sums, times the rows' weights, to its own y
-// [token][columns] in LDS when it leaves the slot. The waves' y are added in their order; with several splits the block that finishes last adds the
-// splits' in theirs.
+// [token][columns] in LDS when it leaves the slot. The waves' y are added in their order; with several splits the block
+// that finishes last adds the splits' in theirs.
 template <int ACT, bool MX, int M, int TT, int NW>
 __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
     constexpr int COLS = 16 * M;
@@ -603,7 +603,8 @@ __global__ __launch_bounds__(64 * NW) void mlp_out(MlpArgs a, Layout lay) {
 // First product: blocks of two waves with 32 columns of h, where 64 tokens' experts differ in their passes a grid of 24 waves
 // to a CU (64 x 2048 x 1408 on 8 of 128 in MXFP4: 185 / 192 with 12), up to 32 tokens of 12 (16 tokens: 96 / 98 with 24; blocks of four waves
 // 102; two chunks of K at a time for four waves 105). Below 512 units blocks of eight waves with 16 columns (one token,
-// 4096 x 2048, 2 of 8: 17.0 / 19.4). 16-bit weights take 16 columns: above 16 tokens in passes of 32, a grid of 24 waves to a CU (64 tokens, 4
+// 4096 x 2048, 2 of 8: 17.0 / 19.4), and passes of 32 tokens blocks of four waves, a grid of 16 to a CU (64 tokens, 2 of 8 of 4096 x
+// 2048: 60.3, with 12 or 24 the same; of 8192 x 4096 178, 12 181). 16-bit weights take 16 columns: above 16 tokens in passes of 32, a grid of 24 waves to a CU (64 tokens, 4
 // of 32 of 4096 x 2048: 362 / 374 with 16), up to 16 tokens from 1024 units on in blocks of eight waves, one to a CU (16
 // tokens, 4 of 32 of 4096 x 2048: 214 / 217), else in blocks of four and a grid of 16 waves to a CU (16 x 1024 x 512 on 2 of 16: 8 to 32
 // all 23.4). A grid's waves to a CU are not those that run at once: the registers hold 16 with 16 columns in MXFP4, 8 in passes of 32
